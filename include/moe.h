@@ -1,6 +1,8 @@
 /*
  * moe.h -- C ABI of libmoe_mi355x.so, the sparse Mixture-of-Experts layer
- * forward for AMD Instinct MI355X (gfx950).
+ * for AMD Instinct MI355X (gfx950): its forward pass, and, in the second
+ * part of this file, what training it needs (layer norm, the expert FFN that
+ * keeps its pre-activations, and the gradients).
  *
  * What is computed follows "How Mixture of Experts Scales Model Parameters"
  * (zhangchitc.github.io/posts/mixture-of-experts/):
@@ -58,7 +60,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 4
+#define MOE_ABI_VERSION 5
 
 typedef enum {
   MOE_OK = 0,
@@ -307,6 +309,39 @@ int moe_forward(const moe_shape *s, const void *x, int act, const void *wg,
 int moe_forward_noalloc(const moe_shape *s, const void *x, int act, const void *wg,
                         const float *bias, const moe_expert_weights *w, void *y, int out,
                         int32_t *topk_idx, float *topk_w, void *stream);
+
+/* ---- training ------------------------------------------------------------ */
+
+/* Layer norm over the rows of x [n][d], the norm in front of the layer:
+ *   mean[t] = sum_c x[t][c] / d
+ *   rstd[t] = 1 / sqrt(sum_c (x[t][c] - mean[t])^2 / d + eps)
+ *   y[t][c] = (x[t][c] - mean[t]) rstd[t] weight[c] + bias[c]
+ *   x, y       [n][d] (act = MOE_F32 or MOE_BF16); sums are float32, the
+ *              variance is taken from differences from the mean, and y is
+ *              rounded once
+ *   weight     [d] f32; bias [d] f32 or NULL (none)
+ *   mean, rstd [n] f32 outputs for the gradient; each may be NULL
+ * 0 <= n < 2^30 (n = 0 does nothing), 1 <= d <= 16384, eps >= 0
+ * (MOE_ERR_SHAPE otherwise); bf16 rows need d % 8 == 0 and 16-byte aligned
+ * pointers. */
+int moe_layer_norm(int32_t n, int32_t d, const void *x, int act, const float *weight,
+                   const float *bias, float eps, void *y, float *mean, float *rstd, void *stream);
+
+/* Gradient of moe_layer_norm.  With xh = (x - mean) rstd:
+ *   dx[t]   = rstd[t] (w dy - avg(w dy) - xh avg(w dy xh))   (averages over c)
+ *   dweight = sum_t dy[t] xh[t],  dbias = sum_t dy[t]
+ *   dy, x, dx [n][d] (act); weight, mean, rstd as given to and written by
+ *             the forward pass
+ *   dweight, dbias [d] f32 outputs, overwritten; each may be NULL
+ *   ws / ws_bytes: device workspace of at least
+ *             moe_layer_norm_backward_workspace_bytes(n, d), 16-byte aligned
+ * Same limits as moe_layer_norm; n = 0 writes zeros to dweight and dbias.
+ * Sums over rows run in a fixed order (deterministic).  The size helper
+ * returns 0 for sizes out of range and for n = 0, which needs no workspace. */
+size_t moe_layer_norm_backward_workspace_bytes(int32_t n, int32_t d);
+int moe_layer_norm_backward(int32_t n, int32_t d, const void *dy, const void *x, int act,
+                            const float *weight, const float *mean, const float *rstd, void *dx,
+                            float *dweight, float *dbias, void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,9 @@ _BINDING_NAMES = (
     "moe_expert_down",
     "moe_combine",
     "moe_forward",
+    "moe_layer_norm",
+    "moe_layer_norm_backward",
+    "moe_layer_norm_backward_workspace_bytes",
     "MoeError",
     "Shape",
     "ExpertWeights",

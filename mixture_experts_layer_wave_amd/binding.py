@@ -89,12 +89,19 @@ lib.moe_forward.restype = _I
 lib.moe_forward.argtypes = [_SP, _P, _I, _P, _P, _WP, _P, _I, _P, _P, _P, _SZ, _P]
 lib.moe_forward_noalloc.restype = _I
 lib.moe_forward_noalloc.argtypes = [_SP, _P, _I, _P, _P, _WP, _P, _I, _P, _P, _P]
+lib.moe_layer_norm.restype = _I
+lib.moe_layer_norm.argtypes = [_I, _I, _P, _I, _P, _P, ctypes.c_float, _P, _P, _P, _P]
+lib.moe_layer_norm_backward_workspace_bytes.restype = _SZ
+lib.moe_layer_norm_backward_workspace_bytes.argtypes = [_I, _I]
+lib.moe_layer_norm_backward.restype = _I
+lib.moe_layer_norm_backward.argtypes = [_I, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
 
 EXPORTS = ("moe_abi_version", "moe_status_string", "moe_workspace_bytes", "moe_mxfp8_bytes",
            "moe_quantize_mxfp8", "moe_router_topk",
            "moe_router_stats_workspace_bytes", "moe_router_stats", "moe_active_experts",
            "moe_dispatch_workspace_bytes", "moe_dispatch", "moe_grouped_ffn", "moe_expert_up", "moe_expert_down", "moe_combine",
-           "moe_forward", "moe_forward_noalloc")
+           "moe_forward", "moe_forward_noalloc", "moe_layer_norm",
+           "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward")
 
 
 def _ptr(t):
@@ -232,3 +239,20 @@ def moe_forward_noalloc(shape, x, act, wg, bias, weights, y, out, topk_idx, topk
     _check("moe_forward_noalloc", lib.moe_forward_noalloc(
         ctypes.byref(_shape(shape)), _ptr(x), _dt(act), _ptr(wg), _ptr(bias), ctypes.byref(w),
         _ptr(y), _dt(out), _ptr(topk_idx), _ptr(topk_w), _stream(stream)))
+
+
+def moe_layer_norm(n, d, x, act, weight, bias, eps, y, mean=None, rstd=None, stream=None):
+    _check("moe_layer_norm", lib.moe_layer_norm(
+        int(n), int(d), _ptr(x), _dt(act), _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(mean),
+        _ptr(rstd), _stream(stream)))
+
+
+def moe_layer_norm_backward_workspace_bytes(n, d) -> int:
+    return int(lib.moe_layer_norm_backward_workspace_bytes(int(n), int(d)))
+
+
+def moe_layer_norm_backward(n, d, dy, x, act, weight, mean, rstd, dx, dweight, dbias, ws, ws_bytes,
+                            stream=None):
+    _check("moe_layer_norm_backward", lib.moe_layer_norm_backward(
+        int(n), int(d), _ptr(dy), _ptr(x), _dt(act), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx),
+        _ptr(dweight), _ptr(dbias), _ptr(ws), int(ws_bytes), _stream(stream)))

@@ -162,4 +162,18 @@ hipError_t launch_tail_sum(const float *tail, int S, size_t plane, const int32_t
 // aligned.
 hipError_t launch_f32_to_bf16(const float *src, uint16_t *dst, size_t count, hipStream_t st);
 
+// ---- layer norm -----------------------------------------------------------
+// y = (x - mean) rstd w + b over rows of d (<= kLayerNormMaxD); b, mean and
+// rstd may be NULL.  n = 0 launches nothing.  bf16: d % 8 == 0 and 16-byte aligned
+// pointers; float32: any d.
+constexpr int kLayerNormMaxD = 16384;
+hipError_t launch_layer_norm(const void *x, bool bf16, const float *w, const float *b, float eps, int n,
+                             int d, void *y, float *mean, float *rstd, hipStream_t st);
+// Its gradient; part: scratch of layer_norm_grad_bytes(n, d); dw and db may
+// be NULL.  n = 0 writes zeros to dw and db.
+size_t layer_norm_grad_bytes(int n, int d);
+hipError_t launch_layer_norm_grad(const void *dy, const void *x, bool bf16, const float *w,
+                                  const float *mean, const float *rstd, int n, int d, void *dx,
+                                  float *dw, float *db, float *part, hipStream_t st);
+
 }  // namespace moe

@@ -11,13 +11,16 @@
 #include "gemm_mxw.h"
 #include "kernels.h"
 
+using moe::align_up;
+using moe::aligned16;
+using moe::check_dtypes;
+using moe::check_shape;
+using moe::check_weights;
+using moe::ffn_args;
+using moe::hip_status;
+using moe::renorm_of;
+
 namespace {
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 struct WsLayout {
   size_t logits, idx, w, counts, offsets, perm, inv, dscratch, h, yp, part, tail, total;
@@ -36,37 +39,6 @@ moe::FfnArgs plan_args(const moe_shape *s, int wdt) {
   f.k = s->k;
   f.split_ok = true;
   return f;
-}
-
-int check_shape(const moe_shape *s) {
-  if (!s) return MOE_ERR_NULL;
-  if (s->n < 1 || s->d < 1 || s->d_ff < 1 || s->E < 1 || s->E > 1024 || s->k < 1 ||
-      s->k > s->E || s->k > 32 || s->renorm < -1 || s->renorm > 1)
-    return MOE_ERR_SHAPE;
-  if ((long long)s->n * s->k >= (1ll << 31)) return MOE_ERR_SHAPE;
-  return MOE_OK;
-}
-
-bool renorm_of(const moe_shape *s) { return s->renorm < 0 ? s->k > 1 : s->renorm == 1; }
-
-// Activation / weight dtype pairing and the shape rules each needs.
-int check_dtypes(const moe_shape *s, int act, int wdt) {
-  if (act != MOE_F32 && act != MOE_BF16) return MOE_ERR_DTYPE;
-  if (wdt == MOE_F32) {
-    if (act != MOE_F32) return MOE_ERR_DTYPE;
-  } else if (wdt == MOE_BF16 || wdt == MOE_MXFP4) {
-    if (act != MOE_BF16) return MOE_ERR_DTYPE;
-    if (s->d % 8 || s->d_ff % 8) return MOE_ERR_SHAPE;
-    if (wdt == MOE_MXFP4 && (s->d % 32 || s->d_ff % 32)) return MOE_ERR_SHAPE;
-    // The MFMA GEMMs address the pile matrices (R x d and R x d_ff bf16) and
-    // one expert matrix (d x d_ff) with 32-bit byte offsets.
-    const long long R = (long long)s->n * s->k;
-    if (R * std::max(s->d, s->d_ff) * 2 >= (1ll << 31) || (long long)s->d * s->d_ff * 2 >= (1ll << 31))
-      return MOE_ERR_SHAPE;
-  } else {
-    return MOE_ERR_DTYPE;
-  }
-  return MOE_OK;
 }
 
 // K splits of the router logits (the bf16 MFMA router only).
@@ -112,67 +84,6 @@ WsLayout layout(const moe_shape *s, int wdt) {
   L.tail = take(moe::down_tail_bytes(plan_args(s, wdt)));
   L.total = o;
   return L;
-}
-
-// The W4A8 mode: MXFP4 weights, shapes the scaled-MFMA GEMM takes, and
-// 32-bit offsets into the MXFP8 operands (the larger of n*k and n rows).
-int check_w4a8(const moe_shape *s, const moe_expert_weights *w) {
-  if (w->act_quant == 0) return MOE_OK;
-  if (w->act_quant != MOE_MXFP8 || w->dtype != MOE_MXFP4) return MOE_ERR_DTYPE;
-  if (s->d > moe::kW4A8MaxK || s->d_ff > moe::kW4A8MaxK) return MOE_ERR_SHAPE;
-  if (((long long)s->d_ff * (s->d / 32)) % 4 || ((long long)s->d * (s->d_ff / 32)) % 4)
-    return MOE_ERR_SHAPE;
-  const long long R = (long long)s->n * s->k;
-  if (R * std::max(s->d, s->d_ff) >= (1ll << 31)) return MOE_ERR_SHAPE;
-  return MOE_OK;
-}
-
-// act_mx8: the activations handed in are already an MXFP8 matrix.
-int check_weights(const moe_shape *s, int act, const moe_expert_weights *w,
-                  bool act_mx8 = false) {
-  if (!w) return MOE_ERR_NULL;
-  if (act_mx8 && !w->act_quant) return MOE_ERR_DTYPE;
-  const int st = check_dtypes(s, act_mx8 ? MOE_BF16 : act, w->dtype);
-  if (st != MOE_OK) return st;
-  const int sq = check_w4a8(s, w);
-  if (sq != MOE_OK) return sq;
-  if (!w->w1 || !w->w3 || !w->w2) return MOE_ERR_NULL;
-  if (w->slot && w->n_slots < 1) return MOE_ERR_SHAPE;
-  if (w->dtype == MOE_MXFP4 && (!w->s1 || !w->s3 || !w->s2)) return MOE_ERR_NULL;
-  if (w->dtype != MOE_F32 && (!aligned16(w->w1) || !aligned16(w->w3) || !aligned16(w->w2)))
-    return MOE_ERR_ALIGN;
-  if (w->dtype == MOE_MXFP4 && (!aligned16(w->s1) || !aligned16(w->s3) || !aligned16(w->s2)))
-    return MOE_ERR_ALIGN;
-  return MOE_OK;
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-
-moe::FfnArgs ffn_args(const moe_shape *s, const void *a, const int32_t *perm,
-                      const int32_t *offsets, const moe_expert_weights *w, void *h, float *yp) {
-  moe::FfnArgs f{};
-  f.a = a;
-  f.perm = perm;
-  f.offsets = offsets;
-  f.E = s->E;
-  f.R = s->n * s->k;
-  f.d = s->d;
-  f.d_ff = s->d_ff;
-  f.w_dtype = w->dtype;
-  f.w1 = w->w1;
-  f.w3 = w->w3;
-  f.w2 = w->w2;
-  f.s1 = w->s1;
-  f.s3 = w->s3;
-  f.s2 = w->s2;
-  f.slot = w->slot;
-  f.n_slots = w->slot ? w->n_slots : s->E;
-  f.h = h;
-  f.y_perm = yp;
-  f.n = s->n;
-  f.k = s->k;
-  f.act_quant = w->act_quant == MOE_MXFP8;
-  return f;
 }
 
 }  // namespace
@@ -384,6 +295,99 @@ int moe_forward(const moe_shape *s, const void *x, int act, const void *wg, cons
 }  // extern "C"
 
 namespace moe {
+
+int check_shape(const moe_shape *s) {
+  if (!s) return MOE_ERR_NULL;
+  if (s->n < 1 || s->d < 1 || s->d_ff < 1 || s->E < 1 || s->E > 1024 || s->k < 1 ||
+      s->k > s->E || s->k > 32 || s->renorm < -1 || s->renorm > 1)
+    return MOE_ERR_SHAPE;
+  if ((long long)s->n * s->k >= (1ll << 31)) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+bool renorm_of(const moe_shape *s) { return s->renorm < 0 ? s->k > 1 : s->renorm == 1; }
+
+// Activation / weight dtype pairing and the shape rules each needs.
+int check_dtypes(const moe_shape *s, int act, int wdt) {
+  if (act != MOE_F32 && act != MOE_BF16) return MOE_ERR_DTYPE;
+  if (wdt == MOE_F32) {
+    if (act != MOE_F32) return MOE_ERR_DTYPE;
+  } else if (wdt == MOE_BF16 || wdt == MOE_MXFP4) {
+    if (act != MOE_BF16) return MOE_ERR_DTYPE;
+    if (s->d % 8 || s->d_ff % 8) return MOE_ERR_SHAPE;
+    if (wdt == MOE_MXFP4 && (s->d % 32 || s->d_ff % 32)) return MOE_ERR_SHAPE;
+    // The MFMA GEMMs address the pile matrices (R x d and R x d_ff bf16) and
+    // one expert matrix (d x d_ff) with 32-bit byte offsets.
+    const long long R = (long long)s->n * s->k;
+    if (R * std::max(s->d, s->d_ff) * 2 >= (1ll << 31) || (long long)s->d * s->d_ff * 2 >= (1ll << 31))
+      return MOE_ERR_SHAPE;
+  } else {
+    return MOE_ERR_DTYPE;
+  }
+  return MOE_OK;
+}
+
+namespace {
+
+// The W4A8 mode: MXFP4 weights, shapes the scaled-MFMA GEMM takes, and
+// 32-bit offsets into the MXFP8 operands (the larger of n*k and n rows).
+int check_w4a8(const moe_shape *s, const moe_expert_weights *w) {
+  if (w->act_quant == 0) return MOE_OK;
+  if (w->act_quant != MOE_MXFP8 || w->dtype != MOE_MXFP4) return MOE_ERR_DTYPE;
+  if (s->d > moe::kW4A8MaxK || s->d_ff > moe::kW4A8MaxK) return MOE_ERR_SHAPE;
+  if (((long long)s->d_ff * (s->d / 32)) % 4 || ((long long)s->d * (s->d_ff / 32)) % 4)
+    return MOE_ERR_SHAPE;
+  const long long R = (long long)s->n * s->k;
+  if (R * std::max(s->d, s->d_ff) >= (1ll << 31)) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+}  // namespace
+
+// act_mx8: the activations handed in are already an MXFP8 matrix.
+int check_weights(const moe_shape *s, int act, const moe_expert_weights *w, bool act_mx8) {
+  if (!w) return MOE_ERR_NULL;
+  if (act_mx8 && !w->act_quant) return MOE_ERR_DTYPE;
+  const int st = check_dtypes(s, act_mx8 ? MOE_BF16 : act, w->dtype);
+  if (st != MOE_OK) return st;
+  const int sq = check_w4a8(s, w);
+  if (sq != MOE_OK) return sq;
+  if (!w->w1 || !w->w3 || !w->w2) return MOE_ERR_NULL;
+  if (w->slot && w->n_slots < 1) return MOE_ERR_SHAPE;
+  if (w->dtype == MOE_MXFP4 && (!w->s1 || !w->s3 || !w->s2)) return MOE_ERR_NULL;
+  if (w->dtype != MOE_F32 && (!aligned16(w->w1) || !aligned16(w->w3) || !aligned16(w->w2)))
+    return MOE_ERR_ALIGN;
+  if (w->dtype == MOE_MXFP4 && (!aligned16(w->s1) || !aligned16(w->s3) || !aligned16(w->s2)))
+    return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+FfnArgs ffn_args(const moe_shape *s, const void *a, const int32_t *perm,
+                      const int32_t *offsets, const moe_expert_weights *w, void *h, float *yp) {
+  FfnArgs f{};
+  f.a = a;
+  f.perm = perm;
+  f.offsets = offsets;
+  f.E = s->E;
+  f.R = s->n * s->k;
+  f.d = s->d;
+  f.d_ff = s->d_ff;
+  f.w_dtype = w->dtype;
+  f.w1 = w->w1;
+  f.w3 = w->w3;
+  f.w2 = w->w2;
+  f.s1 = w->s1;
+  f.s3 = w->s3;
+  f.s2 = w->s2;
+  f.slot = w->slot;
+  f.n_slots = w->slot ? w->n_slots : s->E;
+  f.h = h;
+  f.y_perm = yp;
+  f.n = s->n;
+  f.k = s->k;
+  f.act_quant = w->act_quant == MOE_MXFP8;
+  return f;
+}
 
 int forward_impl(const moe_shape *s, const void *x, int act, const void *wg, const float *bias,
                  const moe_expert_weights *w, void *y, int out, int32_t *topk_idx,

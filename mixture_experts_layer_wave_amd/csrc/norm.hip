@@ -1,0 +1,396 @@
+// Layer norm and its gradient (the norm in front of the layer's router and
+// experts, and what training it needs).
+//
+//   mean = sum_c x_c / d,  rstd = (sum_c (x_c - mean)^2 / d + eps)^-1/2,
+//   xh = (x - mean) rstd,  y = xh w + b
+//
+//   dx = rstd (w dy - m1 - xh m2),  m1 = sum_c w_c dy_c / d,
+//                                   m2 = sum_c w_c dy_c xh_c / d
+//   dw_c = sum_t dy_tc xh_tc,  db_c = sum_t dy_tc
+//
+// Both are bound by HBM: a row is read once (x, or x and dy) and written
+// once.  TPR threads hold a row in registers, C chunks of V consecutive
+// elements each (16-B accesses where rows allow), so the variance is the sum
+// of squared differences from the mean, not a difference of sums, and
+// nothing is read twice.  A thread owns the same columns of every row it
+// meets: w and b stay in its registers, and so do its columns' partial dw
+// and db in the gradient.  Those are added over the block's rows and row
+// groups, then, by a second kernel, over the blocks, always in the same
+// order.  Sums are float32; rows are rounded once on their way out.
+#include <type_traits>
+
+#include "common.h"
+#include "kernels.h"
+#include "route_dev.h"
+
+namespace moe {
+namespace {
+
+// A row's elements in chunks of V, as float32: bf16 rows are multiples of 8
+// wide, float32 rows of any width (TAIL: not a multiple of 4).  float32
+// chunks are 16-B accesses on 4-B boundaries, which global memory takes; a
+// row's last, partial chunk goes element by element, its missing elements
+// staying 0.
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+template <bool BF, bool TAIL>
+struct Chunk {
+  static constexpr int V = BF ? 8 : 4;
+  typedef typename std::conditional<BF, u32x4, f32x4>::type Raw;
+  Raw q = {};
+  __device__ __forceinline__ void load(const void *p, size_t row, int col, int d) {
+    if (col >= d) return;
+    if constexpr (BF) {
+      q = *(const u32x4 *)((const uint16_t *)p + row * d + col);
+    } else {
+      const float *f = (const float *)p + row * d + col;
+      if (!TAIL || col + 4 <= d)
+        q = *(const f32x4_any *)f;
+      else
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (col + j < d) q[j] = f[j];
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (BF)
+      return __uint_as_float((j & 1) ? (q[j / 2] & 0xffff0000u) : (q[j / 2] << 16));
+    else
+      return q[j];
+  }
+  // Element j of the chunk at col is inside the row.
+  static __device__ __forceinline__ bool in(int col, int j, int d) { return TAIL ? col + j < d : col < d; }
+  static __device__ __forceinline__ void store(void *p, size_t row, int col, int d, const float *v) {
+    if (col >= d) return;
+    if constexpr (BF) {
+      const u32x4 o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7])};
+      *(u32x4 *)((uint16_t *)p + row * d + col) = o;
+    } else {
+      float *f = (float *)p + row * d + col;
+      if (!TAIL || col + 4 <= d)
+        *(f32x4_any *)f = f32x4{v[0], v[1], v[2], v[3]};
+      else
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (col + j < d) f[j] = v[j];
+    }
+  }
+};
+
+// Sums over the TPR threads of a row, in every thread.  Up to a wave the
+// sum is lane permutations; above that the waves' sums meet in LDS, in two
+// buffers used in turn: a wave can write a buffer again only after the
+// barrier of the sum in between, which every reader of the old values has
+// passed.  N values at once.
+template <int TPR, int NT, int N>
+struct RowSum {
+  float (*buf)[N][NT / 64];
+  int turn = 0;
+  __device__ __forceinline__ explicit RowSum(float (*b)[N][NT / 64]) : buf(b) {}
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = group_sum(v[i], TPR < 64 ? TPR : 64);
+    if constexpr (TPR > 64) {
+      constexpr int W = TPR / 64;
+      const int wave = threadIdx.x >> 6, first = wave / W * W;
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) buf[turn][i][wave] = v[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) s += buf[turn][i][first + j];
+        v[i] = s;
+      }
+      turn ^= 1;
+    }
+  }
+};
+
+template <bool BF, bool TAIL, int C, int TPR>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void layer_norm_kernel(
+    const void *__restrict__ x, const float *__restrict__ w, const float *__restrict__ b, float eps,
+    int n, int d, void *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd) {
+  using K = Chunk<BF, TAIL>;
+  constexpr int V = K::V;
+  constexpr int NT = TPR > 256 ? TPR : 256, G = NT / TPR;  // G rows at a time
+  __shared__ float s_buf[2][1][NT / 64];
+  RowSum<TPR, NT, 1> row_sum(s_buf);
+  const int grp = threadIdx.x / TPR, gl = threadIdx.x % TPR;
+  const int stride = gridDim.x * G;
+  float wv[C][V], bv[C][V];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int col = (c * TPR + gl) * V + j;
+      wv[c][j] = col < d ? w[col] : 0.f;
+      bv[c][j] = b && col < d ? b[col] : 0.f;
+    }
+  K cur[C];
+  auto load_row = [&](int row) {
+    if (row < n)
+#pragma unroll
+      for (int c = 0; c < C; ++c) cur[c].load(x, row, (c * TPR + gl) * V, d);
+  };
+  load_row(blockIdx.x * G + grp);
+  // (every thread of a block takes the same number of turns: the sums of a
+  // row over several waves meet at barriers)
+  for (int base = blockIdx.x * G; base < n; base += stride) {
+    const int row = base + grp;
+    float v[C][V], s[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        v[c][j] = cur[c].get(j);  // 0 past the row's end
+        s[0] += v[c][j];
+      }
+    load_row(row + stride);  // the next row's loads run under this row's sums
+    row_sum(s);
+    // (divided, not multiplied by 1 / d: the mean of equal values is that value)
+    const float mu = s[0] / (float)d;
+    s[0] = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        v[c][j] = K::in((c * TPR + gl) * V, j, d) ? v[c][j] - mu : 0.f;
+        s[0] = fmaf(v[c][j], v[c][j], s[0]);
+      }
+    row_sum(s);
+    const float rs = 1.0f / sqrtf(s[0] / (float)d + eps);
+    if (row < n) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float o[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = fmaf(v[c][j] * rs, wv[c][j], bv[c][j]);
+        K::store(y, row, (c * TPR + gl) * V, d, o);
+      }
+      if (gl == 0) {
+        if (mean) mean[row] = mu;
+        if (rstd) rstd[row] = rs;
+      }
+    }
+  }
+}
+
+// Gradient: dx, and the block's partial dw and db in part[block][2][d].
+constexpr int kGradThreads = 1024;
+
+template <bool BF, bool TAIL, int C, int TPR>
+__global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(
+    const void *__restrict__ dy, const void *__restrict__ x, const float *__restrict__ w,
+    const float *__restrict__ mean, const float *__restrict__ rstd, int n, int d,
+    void *__restrict__ dx, float *__restrict__ part) {
+  using K = Chunk<BF, TAIL>;
+  constexpr int V = K::V, NT = kGradThreads, G = NT / TPR;
+  __shared__ float s_buf[2][2][NT / 64];
+  __shared__ float s_col[G > 1 ? 2 : 1][G > 1 ? TPR * C * V : 1];
+  RowSum<TPR, NT, 2> row_sum(s_buf);
+  const int grp = threadIdx.x / TPR, gl = threadIdx.x % TPR;
+  const int stride = gridDim.x * G;
+  const float inv_d = 1.0f / (float)d;
+  // (w is read again for every row, from L1 or L2, where a thread's columns
+  // are too many to keep beside their sums)
+  constexpr bool kKeepW = C * V <= 8;
+  auto w_at = [&](int c, int j) {
+    const int col = (c * TPR + gl) * V + j;
+    return col < d ? w[col] : 0.f;
+  };
+  float wv[C][V], dw[C][V], db[C][V];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if constexpr (kKeepW) wv[c][j] = w_at(c, j);
+      dw[c][j] = db[c][j] = 0.f;
+    }
+  K cx[C], cy[C];
+  float mu = 0.f, rs = 0.f;
+  auto load_row = [&](int row) {
+    if (row < n) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        cx[c].load(x, row, (c * TPR + gl) * V, d);
+        cy[c].load(dy, row, (c * TPR + gl) * V, d);
+      }
+      mu = mean[row];
+      rs = rstd[row];
+    }
+  };
+  load_row(blockIdx.x * G + grp);
+  for (int base = blockIdx.x * G; base < n; base += stride) {
+    const int row = base + grp;
+    const bool live = row < n;
+    float t[C][V], xh[C][V], s[2] = {0.f, 0.f};
+    const float r = rs;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const bool in = live && K::in((c * TPR + gl) * V, j, d);
+        const float g = in ? cy[c].get(j) : 0.f;
+        xh[c][j] = in ? (cx[c].get(j) - mu) * r : 0.f;
+        db[c][j] += g;
+        dw[c][j] = fmaf(g, xh[c][j], dw[c][j]);
+        t[c][j] = g * (kKeepW ? wv[c][j] : w_at(c, j));
+        s[0] += t[c][j];
+        s[1] = fmaf(t[c][j], xh[c][j], s[1]);
+      }
+    }
+    load_row(row + stride);
+    row_sum(s);
+    const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
+    if (live) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float o[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = r * (t[c][j] - m1 - xh[c][j] * m2);
+        K::store(dx, row, (c * TPR + gl) * V, d, o);
+      }
+    }
+  }
+  float *out = part + (size_t)blockIdx.x * 2 * d;
+  if constexpr (G == 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int col = (c * TPR + gl) * V + j;
+        if (col < d) {
+          out[col] = dw[c][j];
+          out[d + col] = db[c][j];
+        }
+      }
+  } else {
+    // the row groups' columns, added in group order
+    for (int g = 0; g < G; ++g) {
+      if (grp == g)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const int col = (c * TPR + gl) * V + j;
+            s_col[0][col] = (g ? s_col[0][col] : 0.f) + dw[c][j];
+            s_col[1][col] = (g ? s_col[1][col] : 0.f) + db[c][j];
+          }
+      __syncthreads();
+    }
+    for (int col = threadIdx.x; col < d; col += NT) {
+      out[col] = s_col[0][col];
+      out[d + col] = s_col[1][col];
+    }
+  }
+}
+
+// dw | db [2 d] = the sum of P partial rows [P][2 d], in a fixed order: a
+// block takes 64 columns, 16 threads each, thread s the rows s, s + 16, ...
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restrict__ part, int P,
+                                                          int d, float *__restrict__ dw,
+                                                          float *__restrict__ db) {
+  __shared__ float s_p[16][64];
+  const int lane = threadIdx.x & 63, s = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  float v = 0.f;
+  if (col < 2 * d)
+    for (int p = s; p < P; p += 16) v += part[(size_t)p * 2 * d + col];
+  s_p[s][lane] = v;
+  __syncthreads();
+  if (s == 0 && col < 2 * d) {
+    v = 0.f;
+    for (int i = 0; i < 16; ++i) v += s_p[i][lane];
+    if (col < d) {
+      if (dw) dw[col] = v;
+    } else if (db) {
+      db[col - d] = v;
+    }
+  }
+}
+
+// Threads per row and chunks per thread for rows of d: the fewest threads
+// that hold a row in at most two 16-B chunks each (the gradient: one, up to
+// 1024 threads; float32 above 8192: four), so narrow rows share a block.
+template <bool BF, bool TAIL, bool GRAD, typename Launch>
+hipError_t with_layout(int d, Launch go) {
+  constexpr int V = Chunk<BF, TAIL>::V;
+#define MOE_LN(C_, T_) \
+  if (d <= V * C_ * T_) return go(std::integral_constant<int, C_>{}, std::integral_constant<int, T_>{});
+  MOE_LN(1, 16)
+  MOE_LN(1, 64)
+  MOE_LN(1, 256)
+  if constexpr (GRAD) {
+    MOE_LN(1, 512)
+    MOE_LN(1, 1024)
+  } else {
+    MOE_LN(2, 256)
+  }
+  MOE_LN(2, 1024)
+  if constexpr (!BF) MOE_LN(4, 1024)
+#undef MOE_LN
+  return hipErrorInvalidValue;
+}
+
+// Blocks of the gradient: one per CU (1024 threads, about 100 VGPRs each),
+// fewer for few rows; each writes one partial row of 2 d floats.
+int grad_blocks(int n) { return n < 256 ? n : 256; }
+
+template <bool BF, bool TAIL>
+hipError_t launch_fwd(const void *x, const float *w, const float *b, float eps, int n, int d, void *y,
+                      float *mean, float *rstd, hipStream_t st) {
+  return with_layout<BF, TAIL, false>(d, [&](auto cc, auto tt) {
+    constexpr int C = decltype(cc)::value, TPR = decltype(tt)::value;
+    constexpr int NT = TPR > 256 ? TPR : 256, G = NT / TPR;
+    const int want = (n + G - 1) / G, cap = 256 * 2048 / NT;  // every CU full
+    layer_norm_kernel<BF, TAIL, C, TPR><<<want < cap ? want : cap, NT, 0, st>>>(x, w, b, eps, n, d, y,
+                                                                             mean, rstd);
+    return hipGetLastError();
+  });
+}
+
+template <bool BF, bool TAIL>
+hipError_t launch_grad(const void *dy, const void *x, const float *w, const float *mean,
+                       const float *rstd, int n, int d, void *dx, float *dw, float *db, float *part,
+                       hipStream_t st) {
+  int P = 0;
+  const hipError_t e = with_layout<BF, TAIL, true>(d, [&](auto cc, auto tt) {
+    constexpr int C = decltype(cc)::value, TPR = decltype(tt)::value;
+    constexpr int G = kGradThreads / TPR;
+    P = grad_blocks((n + G - 1) / G);
+    if (P > 0)
+      layer_norm_grad_kernel<BF, TAIL, C, TPR><<<P, kGradThreads, 0, st>>>(dy, x, w, mean, rstd, n, d, dx,
+                                                                        part);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return e;
+  if (!dw && !db) return hipSuccess;
+  column_sum_kernel<<<(2 * d + 63) / 64, 1024, 0, st>>>(part, P, d, dw, db);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t layer_norm_grad_bytes(int n, int d) { return (size_t)grad_blocks(n) * 2 * d * sizeof(float); }
+
+hipError_t launch_layer_norm(const void *x, bool bf16, const float *w, const float *b, float eps, int n,
+                             int d, void *y, float *mean, float *rstd, hipStream_t st) {
+  if (n == 0) return hipSuccess;
+  if (bf16) return launch_fwd<true, false>(x, w, b, eps, n, d, y, mean, rstd, st);
+  if (d % 4 == 0) return launch_fwd<false, false>(x, w, b, eps, n, d, y, mean, rstd, st);
+  return launch_fwd<false, true>(x, w, b, eps, n, d, y, mean, rstd, st);
+}
+
+hipError_t launch_layer_norm_grad(const void *dy, const void *x, bool bf16, const float *w,
+                                  const float *mean, const float *rstd, int n, int d, void *dx,
+                                  float *dw, float *db, float *part, hipStream_t st) {
+  if (bf16) return launch_grad<true, false>(dy, x, w, mean, rstd, n, d, dx, dw, db, part, st);
+  if (d % 4 == 0) return launch_grad<false, false>(dy, x, w, mean, rstd, n, d, dx, dw, db, part, st);
+  return launch_grad<false, true>(dy, x, w, mean, rstd, n, d, dx, dw, db, part, st);
+}
+
+}  // namespace moe

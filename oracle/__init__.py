@@ -34,3 +34,12 @@ from .moe_oracle import (  # noqa: F401
     active_experts,
     resolve_slots,
 )
+from .train_oracle import (  # noqa: F401
+    layer_norm,
+    layer_norm_grad,
+    expert_up,
+    row_weights,
+    grouped_ffn_grad,
+    router_weights,
+    router_grad,
+)
