@@ -343,6 +343,56 @@ int moe_layer_norm_backward(int32_t n, int32_t d, const void *dy, const void *x,
                             const float *weight, const float *mean, const float *rstd, void *dx,
                             float *dweight, float *dbias, void *ws, size_t ws_bytes, void *stream);
 
+/* moe_expert_up with its pre-activations kept for the gradient:
+ *   g[r] = a[src(r)] W1_e^T, u[r] = a[src(r)] W3_e^T, h[r] = silu(g[r]) u[r]
+ * g, u and h [n*k][d_ff]: bf16 for BF16 weights (each rounded once from its
+ * float32 value), f32 for F32 weights.  The other arguments and src(r) as in
+ * moe_expert_up; h goes to moe_expert_down.  Rows outside the piles are left
+ * as they were.  F32 and BF16 weights only (MOE_ERR_DTYPE otherwise); d and
+ * d_ff below 2^20; with BF16 weights a, h, g and u 16-byte aligned.
+ * A dense gated feed-forward block is the case E = 1, k = 1, perm = NULL,
+ * offsets = {0, n}. */
+int moe_expert_up_save(const moe_shape *s, const void *a, int act, const int32_t *perm,
+                       const int32_t *offsets, const moe_expert_weights *w, void *h, void *g,
+                       void *u, void *stream);
+
+/* Gradient of the expert FFN and of the combine behind it.  For the forward
+ * pass  y[t] = sum_j topk_w[t][j] yp[inv[t][j]],
+ *       yp[r] = (silu(g[r]) u[r]) W2_e^T,  g[r], u[r] as moe_expert_up_save
+ * and dy, the loss's gradient with respect to y:
+ *   dh0[r]       = dy[perm[r]] W2_e
+ *   dtopk_w[t][j] = <dh0[r], silu(g[r]) u[r]> at r = inv[t][j]  (0 for a pair
+ *                   without a pile row)
+ *   dh[r] = w_r dh0[r],  w_r the combine weight of row r's pair
+ *   dg = dh u silu'(g),  du = dh silu(g)
+ *   da_perm[r] = dg W1_e + du W3_e
+ *   dw1_e = dg^T a,  dw3_e = du^T a,  dw2_e = dy^T (w silu(g) u), summed over
+ *                   the rows of pile e; zeros for an empty pile
+ *   dy, a     [n][d] token rows, gathered through perm [n*k]; inv and topk_w
+ *             [n][k] as in the forward pass, dtopk_w [n][k] f32 output.
+ *             perm, inv, topk_w and dtopk_w are given together; with all
+ *             four NULL there is no combine: dy and a are pile rows
+ *             [n*k][d], y = yp and w_r = 1
+ *   g, u      [n*k][d_ff] as kept by moe_expert_up_save
+ *   da_perm   [n*k][d] output, the gradient of each pile row's input (rows
+ *             outside the piles are left as they were); the tokens' sums of
+ *             it are taken by moe_router_backward
+ *   dw1, dw3  [E][d_ff][d] and dw2 [E][d][d_ff] outputs, by logical expert
+ *             (with a slot table too), overwritten
+ *   ws        at least moe_grouped_ffn_backward_workspace_bytes(s, w->dtype)
+ * Matrices have the type of act and the weights, F32 or BF16 (MOE_ERR_DTYPE
+ * otherwise).  Products accumulate in float32 and outputs are rounded once;
+ * with BF16 weights dg, du and w silu(g) u are rounded to bf16 in between
+ * (the matrix cores' input type) and pointers are 16-byte aligned.  d and
+ * d_ff below 2^20.  Deterministic.  The size helper returns 0 for an invalid
+ * shape or weight dtype. */
+size_t moe_grouped_ffn_backward_workspace_bytes(const moe_shape *s, int w_dtype);
+int moe_grouped_ffn_backward(const moe_shape *s, const void *dy, const void *a, int act,
+                             const int32_t *perm, const int32_t *inv, const float *topk_w,
+                             const int32_t *offsets, const moe_expert_weights *w, const void *g,
+                             const void *u, void *da_perm, void *dw1, void *dw3, void *dw2,
+                             float *dtopk_w, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

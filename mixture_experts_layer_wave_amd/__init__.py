@@ -22,6 +22,9 @@ _BINDING_NAMES = (
     "moe_layer_norm",
     "moe_layer_norm_backward",
     "moe_layer_norm_backward_workspace_bytes",
+    "moe_expert_up_save",
+    "moe_grouped_ffn_backward",
+    "moe_grouped_ffn_backward_workspace_bytes",
     "MoeError",
     "Shape",
     "ExpertWeights",

@@ -95,13 +95,21 @@ lib.moe_layer_norm_backward_workspace_bytes.restype = _SZ
 lib.moe_layer_norm_backward_workspace_bytes.argtypes = [_I, _I]
 lib.moe_layer_norm_backward.restype = _I
 lib.moe_layer_norm_backward.argtypes = [_I, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+lib.moe_expert_up_save.restype = _I
+lib.moe_expert_up_save.argtypes = [_SP, _P, _I, _P, _P, _WP, _P, _P, _P, _P]
+lib.moe_grouped_ffn_backward_workspace_bytes.restype = _SZ
+lib.moe_grouped_ffn_backward_workspace_bytes.argtypes = [_SP, _I]
+lib.moe_grouped_ffn_backward.restype = _I
+lib.moe_grouped_ffn_backward.argtypes = [_SP, _P, _P, _I, _P, _P, _P, _P, _WP, _P, _P, _P, _P, _P, _P, _P,
+                                         _P, _SZ, _P]
 
 EXPORTS = ("moe_abi_version", "moe_status_string", "moe_workspace_bytes", "moe_mxfp8_bytes",
            "moe_quantize_mxfp8", "moe_router_topk",
            "moe_router_stats_workspace_bytes", "moe_router_stats", "moe_active_experts",
            "moe_dispatch_workspace_bytes", "moe_dispatch", "moe_grouped_ffn", "moe_expert_up", "moe_expert_down", "moe_combine",
            "moe_forward", "moe_forward_noalloc", "moe_layer_norm",
-           "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward")
+           "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward",
+           "moe_expert_up_save", "moe_grouped_ffn_backward_workspace_bytes", "moe_grouped_ffn_backward")
 
 
 def _ptr(t):
@@ -256,3 +264,23 @@ def moe_layer_norm_backward(n, d, dy, x, act, weight, mean, rstd, dx, dweight, d
     _check("moe_layer_norm_backward", lib.moe_layer_norm_backward(
         int(n), int(d), _ptr(dy), _ptr(x), _dt(act), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx),
         _ptr(dweight), _ptr(dbias), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moe_expert_up_save(shape, a, act, perm, offsets, weights, h, g, u, stream=None):
+    w = _weights(weights)
+    _check("moe_expert_up_save", lib.moe_expert_up_save(
+        ctypes.byref(_shape(shape)), _ptr(a), _dt(act), _ptr(perm), _ptr(offsets), ctypes.byref(w),
+        _ptr(h), _ptr(g), _ptr(u), _stream(stream)))
+
+
+def moe_grouped_ffn_backward_workspace_bytes(shape, w_dtype) -> int:
+    return int(lib.moe_grouped_ffn_backward_workspace_bytes(ctypes.byref(_shape(shape)), _dt(w_dtype)))
+
+
+def moe_grouped_ffn_backward(shape, dy, a, act, perm, inv, topk_w, offsets, weights, g, u, da_perm, dw1,
+                             dw3, dw2, dtopk_w, ws, ws_bytes, stream=None):
+    w = _weights(weights)
+    _check("moe_grouped_ffn_backward", lib.moe_grouped_ffn_backward(
+        ctypes.byref(_shape(shape)), _ptr(dy), _ptr(a), _dt(act), _ptr(perm), _ptr(inv), _ptr(topk_w),
+        _ptr(offsets), ctypes.byref(w), _ptr(g), _ptr(u), _ptr(da_perm), _ptr(dw1), _ptr(dw3), _ptr(dw2),
+        _ptr(dtopk_w), _ptr(ws), int(ws_bytes), _stream(stream)))

@@ -424,6 +424,19 @@ hipError_t launch_expert_up(const FfnArgs &a, hipStream_t st) {
   return hipErrorInvalidValue;
 }
 
+hipError_t launch_expert_up_save(const FfnArgs &a, void *g, void *u, hipStream_t st) {
+  if (a.R == 0) return hipSuccess;
+  if (a.w_dtype == 0) return launch_up_save_f32(a, g, u, st);
+  if (!big_ok(a, (size_t)(a.perm ? a.n : a.R) * a.d * 2, a.d_ff, a.d)) return hipErrorInvalidValue;
+  static const TileChoice cand[2] = {{256, 256, 1}, {320, 256, 1}};
+  const TileChoice t = choose_tile(a, true, cand, 2);
+  BigGemmParams p = big_params(a, true);
+  p.n_tiles = (a.d_ff + t.bnb / 2 - 1) / (t.bnb / 2);
+  p.out_g = g;
+  p.out_u = u;
+  return launch_big_gemm(p, true, false, a.perm != nullptr, false, t.bm, t.bnb, st);
+}
+
 hipError_t launch_expert_down(const FfnArgs &a, hipStream_t st, bool *fused, bool *yp_bf16) {
   if (fused) *fused = false;
   if (yp_bf16) *yp_bf16 = false;

@@ -20,6 +20,7 @@ struct BigGemmParams {
   const int32_t *perm_out;  // fused combine: pile row -> token
   const float *comb_w;      // fused combine: token -> weight (one expert per token)
   int fuse_rows;            // fused combine: rows of y (tokens)
+  void *out_g, *out_u;      // up, keeping the pre-activations: bf16 [R][N] each, or NULL
   int out_bf16;             // down, neither fused nor split: pile outputs as bf16
                             // (the f32 result rounded once) in out
   // Split K (down only): each block tile is computed by `splits` blocks over

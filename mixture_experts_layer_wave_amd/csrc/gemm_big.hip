@@ -87,9 +87,13 @@ __device__ __forceinline__ void lgkm_wait0() {
 
 // Up: H rows [row0, row0 + rows) in ro (row pitch N bf16) = silu(gate) * value,
 // gate = acc[tm][j], value = acc[tm][j + TN/2].  TM * TN stores per wave.
-template <int TM, int TN, int WM, int WN>
+// SAVE: gate and value, each rounded once, go to rg and ru too (H is formed
+// from the float32 values).
+template <int TM, int TN, int WM, int WN, bool SAVE>
 __device__ __forceinline__ void store_swiglu_regs(const f32x16 (&acc)[TM][TN],
-                                                  __amdgpu_buffer_rsrc_t ro, int N, int rows,
+                                                  __amdgpu_buffer_rsrc_t ro,
+                                                  __amdgpu_buffer_rsrc_t rg,
+                                                  __amdgpu_buffer_rsrc_t ru, int N, int rows,
                                                   int n0, int wm, int wn) {
   // (the lane id is read afresh: lane-derived values of the K loop are
   // not kept live across it for the epilogue)
@@ -117,6 +121,17 @@ __device__ __forceinline__ void store_swiglu_regs(const f32x16 (&acc)[TM][TN],
         const uint32_t off =
             (r < rows && col < N) ? (rowoff + (uint32_t)(tm * 32 * N) + col) * 2u : kOOB;
         __builtin_amdgcn_raw_buffer_store_b128(o, ro, off, 0, 0);
+        if constexpr (SAVE) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const f32x16 &x = acc[tm][v ? j + TN / 2 : j];
+            const u32x4 q = swap_halves(pack_bf16x2(x[8 * h], x[8 * h + 1]),
+                                        pack_bf16x2(x[8 * h + 2], x[8 * h + 3]),
+                                        pack_bf16x2(x[8 * h + 4], x[8 * h + 5]),
+                                        pack_bf16x2(x[8 * h + 6], x[8 * h + 7]));
+            __builtin_amdgcn_raw_buffer_store_b128(q, v ? ru : rg, off, 0, 0);
+          }
+        }
       }
     }
   }
@@ -207,8 +222,9 @@ __device__ __forceinline__ void store_scaled_rows_regs(const f32x16 (&acc)[TM][T
 //
 // LPT: longest-first tile order (map_block_fn), for unsplit down GEMMs of
 // three or more rounds of blocks, where the ragged last row tiles then fill
-// the last round.  FUSE is the combine-fused down pass.
-template <bool UP, bool GATHER, bool FUSE, int BM, int BNB, bool LPT>
+// the last round.  FUSE is the combine-fused down pass.  SAVE is the up pass
+// of training, which keeps the pre-activations.
+template <bool UP, bool GATHER, bool FUSE, int BM, int BNB, bool LPT, bool SAVE>
 __global__ __launch_bounds__(kNT, 1) void big_gemm_kernel(BigGemmParams p) {
   constexpr int BK = kBK;
   using T = Tile<BM, BNB, BK>;
@@ -414,9 +430,11 @@ __global__ __launch_bounds__(kNT, 1) void big_gemm_kernel(BigGemmParams p) {
 
   // ---- epilogue (stores from registers) --------------------------------------
   if constexpr (UP) {
-    store_swiglu_regs<T::TM, T::TN, T::WM, T::WN>(
-        acc, rsrc((uint16_t *)p.out + (size_t)row0 * N, (uint32_t)rows * (uint32_t)N * 2u), N, rows,
-        n0, wm, wn);
+    const uint32_t bytes = (uint32_t)rows * (uint32_t)N * 2u;
+    const __amdgpu_buffer_rsrc_t ro = rsrc((uint16_t *)p.out + (size_t)row0 * N, bytes);
+    store_swiglu_regs<T::TM, T::TN, T::WM, T::WN, SAVE>(
+        acc, ro, SAVE ? rsrc((uint16_t *)p.out_g + (size_t)row0 * N, bytes) : ro,
+        SAVE ? rsrc((uint16_t *)p.out_u + (size_t)row0 * N, bytes) : ro, N, rows, n0, wm, wn);
   } else if constexpr (FUSE) {
     store_scaled_rows_regs<T::TM, T::TN, T::WM, T::WN>(
         acc, rsrc(p.out, (uint32_t)p.fuse_rows * (uint32_t)N * 2u), N, p.perm_out, p.comb_w, row0,
@@ -665,9 +683,8 @@ __global__ __launch_bounds__(kNT, 1) void mxdq_gemm_kernel(BigGemmParams p) {
     }
   }
   if constexpr (UP) {
-    store_swiglu_regs<T::TM, T::TN, T::WM, T::WN>(
-        acc, rsrc((uint16_t *)p.out + (size_t)row0 * N, (uint32_t)rows * N * 2u), N, rows, n0, wm,
-        wn);
+    const __amdgpu_buffer_rsrc_t ro = rsrc((uint16_t *)p.out + (size_t)row0 * N, (uint32_t)rows * N * 2u);
+    store_swiglu_regs<T::TM, T::TN, T::WM, T::WN, false>(acc, ro, ro, ro, N, rows, n0, wm, wn);
   } else if constexpr (FUSE) {
     store_scaled_rows_regs<T::TM, T::TN, T::WM, T::WN>(
         acc, rsrc(p.out, (uint32_t)p.fuse_rows * (uint32_t)N * 2u), N, p.perm_out, p.comb_w, row0, rows,
@@ -693,11 +710,11 @@ hipError_t allow_lds(Kern kern, int lds, std::atomic<uint64_t> &done) {
   return hipSuccess;
 }
 
-template <bool UP, bool GATHER, bool FUSE, int BM, int BNB, bool LPT>
+template <bool UP, bool GATHER, bool FUSE, int BM, int BNB, bool LPT, bool SAVE = false>
 hipError_t launch_bf16(const BigGemmParams &p, int blocks, hipStream_t st) {
   using T = Tile<BM, BNB, kBK>;
   constexpr int lds = 2 * T::STAGE;
-  auto kern = big_gemm_kernel<UP, GATHER, FUSE, BM, BNB, LPT>;
+  auto kern = big_gemm_kernel<UP, GATHER, FUSE, BM, BNB, LPT, SAVE>;
   static std::atomic<uint64_t> attr_done{0};
   hipError_t err = allow_lds(kern, lds, attr_done);
   if (err != hipSuccess) return err;
@@ -735,6 +752,8 @@ hipError_t launch_big_gemm(const BigGemmParams &p, bool up, bool mx, bool gather
                                             : 0);
 #define MOE_BF16(U, G, F, A, B)                                                     \
   if (!mx && up == U && gather == G && fuse == F && bm == A && bnb == B) {         \
+    if constexpr (U)                                                                \
+      if (p.out_g) return launch_bf16<U, G, F, A, B, false, true>(p, blocks, st);   \
     if constexpr (!U && !F)                                                         \
       if (lpt) return launch_bf16<U, G, F, A, B, true>(p, blocks + spare, st);      \
     return launch_bf16<U, G, F, A, B, false>(p, blocks, st);                        \

@@ -1,0 +1,238 @@
+// Grouped float32 products of training: the up projection that keeps its
+// pre-activations, and the expert FFN's gradient (formulas in gemm_grad.h).
+// Everything stays float32 (v_mfma_f32_32x32x2_f32 accumulates each product
+// in float32), so dg, du and w h are not rounded between the products.
+// Any d and d_ff; pointers need no alignment beyond a float's.
+#include "common.h"
+#include "gemm_common.h"
+#include "gemm_f32.h"
+#include "gemm_grad.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+using namespace f32gemm;
+using gemm::TileSlot;
+
+struct F32Params {
+  const float *a, *dy;
+  const int32_t *perm, *inv, *offsets, *slot;
+  const float *topk_w;
+  int n_slots, n, k, E, R, d, f, n_nt;
+  const float *w1, *w3, *w2, *g, *u;
+  float *dg, *du, *hs, *part;  // gradient
+  float *o0, *o1, *o2;         // outputs of the product
+};
+
+__device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + expf(-g)); }
+
+// The tile's pile, first row, rows and column tile, from the pile sizes.
+__device__ __forceinline__ bool row_tile(const F32Params &p, TileSlot &s_t) {
+  if (threadIdx.x < 64) gemm::map_block<kT>(p.offsets, p.E, p.n_nt, 1, threadIdx.x, &s_t);
+  __syncthreads();
+  return s_t.e >= 0;
+}
+
+// Rows of this thread's elements of an operand contiguous along K, gathered
+// or not (past the tile's rows: -1).
+__device__ __forceinline__ void source_rows(int (&src)[kPer], const int32_t *perm, int row0, int rows) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    int k, r;
+    place<false>(i, k, r);
+    src[i] = r < rows ? (perm ? perm[row0 + r] : row0 + r) : -1;
+  }
+}
+
+// g = a W1^T, u = a W3^T, h = silu(g) u.
+__global__ __launch_bounds__(kThreads) void up_save_f32_kernel(F32Params p) {
+  __shared__ float smem[2 * kK * kPitch];
+  __shared__ TileSlot s_t;
+  if (!row_tile(p, s_t)) return;
+  const int row0 = s_t.row0, rows = s_t.rows, n0 = s_t.nt * kT;
+  const size_t mat = (size_t)phys_slot(p.slot, p.n_slots, s_t.e) * p.f * p.d;
+  int src[kPer];
+  source_rows(src, p.perm, row0, rows);
+  auto fa = [&](int i, int k, int) { return src[i] >= 0 ? p.a[(size_t)src[i] * p.d + k] : 0.f; };
+  auto weights = [&](const float *w) {
+    return [=](int, int k, int c) { return n0 + c < p.f ? w[mat + (size_t)(n0 + c) * p.d + k] : 0.f; };
+  };
+  f32x16 ga = {}, ua = {};
+  product<false, false>(ga, smem, p.d, fa, weights(p.w1));
+  product<false, false>(ua, smem, p.d, fa, weights(p.w3));
+  const int r = out_row();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = n0 + out_col(i);
+    if (r < rows && c < p.f) {
+      const size_t at = (size_t)(row0 + r) * p.f + c;
+      p.o1[at] = ga[i];
+      p.o2[at] = ua[i];
+      p.o0[at] = ga[i] * sigmoid_f32(ga[i]) * ua[i];
+    }
+  }
+}
+
+// dh0 = dy W2 and what follows from it; row sums of dh0 h over each wave's 32
+// columns go to part[plane][row].
+__global__ __launch_bounds__(kThreads) void dh_f32_kernel(F32Params p) {
+  __shared__ float smem[2 * kK * kPitch];
+  __shared__ TileSlot s_t;
+  if (!row_tile(p, s_t)) return;
+  const int row0 = s_t.row0, rows = s_t.rows, n0 = s_t.nt * kT;
+  const float *w2 = p.w2 + (size_t)phys_slot(p.slot, p.n_slots, s_t.e) * p.d * p.f;
+  int src[kPer];
+  source_rows(src, p.perm, row0, rows);
+  f32x16 acc = {};
+  product<false, true>(
+      acc, smem, p.d, [&](int i, int k, int) { return src[i] >= 0 ? p.dy[(size_t)src[i] * p.d + k] : 0.f; },
+      [&](int, int k, int c) { return n0 + c < p.f ? w2[(size_t)k * p.f + n0 + c] : 0.f; });
+  const int r = out_row();
+  float wr = 1.f, sum = 0.f;
+  if (p.perm && r < rows) {
+    const int t = p.perm[row0 + r];
+    wr = 0.f;
+    for (int j = 0; j < p.k; ++j)
+      if (p.inv[(size_t)t * p.k + j] == row0 + r) wr = p.topk_w[(size_t)t * p.k + j];
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = n0 + out_col(i);
+    if (r < rows && c < p.f) {
+      const size_t at = (size_t)(row0 + r) * p.f + c;
+      const float g = p.g[at], u = p.u[at], s = sigmoid_f32(g), a = g * s, h = a * u;
+      sum = fmaf(acc[i], h, sum);
+      const float dh = acc[i] * wr;
+      p.dg[at] = dh * u * fmaf(a, 1.0f - s, s);
+      p.du[at] = dh * a;
+      p.hs[at] = wr * h;
+    }
+  }
+  sum += __shfl_xor(sum, 32, 64);
+  const int plane = s_t.nt * 2 + ((threadIdx.x >> 6) & 1);
+  if (p.perm && (threadIdx.x & 63) < 32 && r < rows) p.part[(size_t)plane * p.R + row0 + r] = sum;
+}
+
+// da = dg W1 + du W3.
+__global__ __launch_bounds__(kThreads) void dx_f32_kernel(F32Params p) {
+  __shared__ float smem[2 * kK * kPitch];
+  __shared__ TileSlot s_t;
+  if (!row_tile(p, s_t)) return;
+  const int row0 = s_t.row0, rows = s_t.rows, n0 = s_t.nt * kT;
+  const size_t mat = (size_t)phys_slot(p.slot, p.n_slots, s_t.e) * p.f * p.d;
+  f32x16 acc = {};
+  for (int half = 0; half < 2; ++half) {
+    const float *dz = half ? p.du : p.dg, *w = (half ? p.w3 : p.w1) + mat;
+    product<false, true>(
+        acc, smem, p.f, [&](int, int k, int m) { return m < rows ? dz[(size_t)(row0 + m) * p.f + k] : 0.f; },
+        [&](int, int k, int c) { return n0 + c < p.d ? w[(size_t)k * p.d + n0 + c] : 0.f; });
+  }
+  const int r = out_row();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = n0 + out_col(i);
+    if (r < rows && c < p.d) p.o0[(size_t)(row0 + r) * p.d + c] = acc[i];
+  }
+}
+
+// Weight gradients of expert blockIdx.z: dW1 and dW3 (f x d; blockIdx.y runs
+// over the row tiles of dW1, then of dW3), or dW2 (d x f).
+template <bool W2>
+__global__ __launch_bounds__(kThreads) void dw_f32_kernel(F32Params p) {
+  __shared__ float smem[2 * kK * kPitch];
+  const int e = blockIdx.z, n0 = blockIdx.x * kT;
+  const int M = W2 ? p.d : p.f, N = W2 ? p.f : p.d, mt = (M + kT - 1) / kT;
+  const bool second = !W2 && (int)blockIdx.y >= mt;
+  const int m0 = ((int)blockIdx.y - (second ? mt : 0)) * kT;
+  const int row0 = p.offsets[e], rows = p.offsets[e + 1] - row0;
+  const float *dz = second ? p.du : p.dg;
+  auto token = [&](int k) { return (size_t)(p.perm ? p.perm[row0 + k] : row0 + k); };
+  f32x16 acc = {};
+  product<true, true>(
+      acc, smem, rows,
+      [&](int, int k, int m) {
+        if (m0 + m >= M) return 0.f;
+        return W2 ? p.dy[token(k) * p.d + m0 + m] : dz[(size_t)(row0 + k) * p.f + m0 + m];
+      },
+      [&](int, int k, int c) {
+        if (n0 + c >= N) return 0.f;
+        return W2 ? p.hs[(size_t)(row0 + k) * p.f + n0 + c] : p.a[token(k) * p.d + n0 + c];
+      });
+  float *out = (second ? p.o1 : p.o0) + (size_t)e * M * N;
+  const int r = m0 + out_row();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = n0 + out_col(i);
+    if (r < M && c < N) out[(size_t)r * N + c] = acc[i];
+  }
+}
+
+int row_tiles(int R, int E) { return (R + kT - 1) / kT + (E < R ? E : R); }
+
+}  // namespace
+
+int grad_planes_f32(int d_ff) { return (d_ff + kT - 1) / kT * 2; }
+
+hipError_t launch_up_save_f32(const FfnArgs &a, void *g, void *u, hipStream_t st) {
+  F32Params p{};
+  p.a = (const float *)a.a;
+  p.perm = a.perm;
+  p.offsets = a.offsets;
+  p.slot = a.slot;
+  p.n_slots = a.n_slots;
+  p.E = a.E;
+  p.R = a.R;
+  p.d = a.d;
+  p.f = a.d_ff;
+  p.w1 = (const float *)a.w1;
+  p.w3 = (const float *)a.w3;
+  p.o0 = (float *)a.h;
+  p.o1 = (float *)g;
+  p.o2 = (float *)u;
+  p.n_nt = (p.f + kT - 1) / kT;
+  up_save_f32_kernel<<<row_tiles(p.R, p.E) * p.n_nt, kThreads, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t st) {
+  F32Params p{};
+  p.a = (const float *)a.a;
+  p.dy = (const float *)a.dy;
+  p.perm = a.perm;
+  p.inv = a.inv;
+  p.topk_w = a.topk_w;
+  p.offsets = a.offsets;
+  p.slot = a.slot;
+  p.n_slots = a.n_slots;
+  p.n = a.n;
+  p.k = a.k;
+  p.E = a.E;
+  p.R = a.R;
+  p.d = a.d;
+  p.f = a.d_ff;
+  p.w1 = (const float *)a.w1;
+  p.w3 = (const float *)a.w3;
+  p.w2 = (const float *)a.w2;
+  p.g = (const float *)a.g;
+  p.u = (const float *)a.u;
+  p.dg = (float *)w.dg;
+  p.du = (float *)w.du;
+  p.hs = (float *)w.hs;
+  p.part = w.part;
+  const int ft = (p.f + kT - 1) / kT, dt = (p.d + kT - 1) / kT;
+  const int tiles = row_tiles(p.R, p.E);
+  p.n_nt = ft;
+  dh_f32_kernel<<<tiles * ft, kThreads, 0, st>>>(p);
+  p.n_nt = dt;
+  p.o0 = (float *)a.da;
+  dx_f32_kernel<<<tiles * dt, kThreads, 0, st>>>(p);
+  p.o0 = (float *)a.dw1;
+  p.o1 = (float *)a.dw3;
+  dw_f32_kernel<false><<<dim3(dt, 2 * ft, p.E), kThreads, 0, st>>>(p);
+  p.o0 = (float *)a.dw2;
+  dw_f32_kernel<true><<<dim3(ft, dt, p.E), kThreads, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace moe

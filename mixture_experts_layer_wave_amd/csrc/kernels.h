@@ -122,6 +122,11 @@ hipError_t launch_expert_down(const FfnArgs &a, hipStream_t st, bool *fused = nu
 hipError_t launch_grouped_ffn(const FfnArgs &a, hipStream_t st, bool *fused = nullptr,
                               bool *yp_bf16 = nullptr);
 
+// The up projection with its pre-activations kept: h, and g = a W1^T and
+// u = a W3^T, [R][d_ff] each in the activations' type (f32 or bf16 weights).
+hipError_t launch_expert_up_save(const FfnArgs &a, void *g, void *u, hipStream_t st);
+hipError_t launch_up_save_f32(const FfnArgs &a, void *g, void *u, hipStream_t st);
+
 // Compute units of the current device (read once and cached).
 int cu_count();
 

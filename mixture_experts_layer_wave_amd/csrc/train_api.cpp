@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include "api_internal.h"
+#include "gemm_grad.h"
 #include "kernels.h"
 
 using namespace moe;
@@ -17,6 +18,35 @@ int check_norm(int32_t n, int32_t d, int act) {
   if (act != MOE_F32 && act != MOE_BF16) return MOE_ERR_DTYPE;
   if (act == MOE_BF16 && d % 8) return MOE_ERR_SHAPE;
   return MOE_OK;
+}
+
+// Shapes and weights of the training FFN: weights that are trained (F32 or
+// BF16), sizes that every product's grid and buffer offsets take.
+int check_ffn_shape(const moe_shape *s, int act, int wdt) {
+  int st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (wdt != MOE_F32 && wdt != MOE_BF16) return MOE_ERR_DTYPE;
+  st = check_dtypes(s, act, wdt);
+  if (st != MOE_OK) return st;
+  return s->d < (1 << 20) && s->d_ff < (1 << 20) ? MOE_OK : MOE_ERR_SHAPE;
+}
+
+int check_ffn(const moe_shape *s, int act, const moe_expert_weights *w) {
+  if (!s || !w) return MOE_ERR_NULL;
+  const int st = check_ffn_shape(s, act, w->dtype);
+  return st == MOE_OK ? check_weights(s, act, w) : st;
+}
+
+FfnGradArgs grad_args(const moe_shape *s, int wdt) {
+  FfnGradArgs a{};
+  a.n = s->n;
+  a.k = s->k;
+  a.E = s->E;
+  a.R = s->n * s->k;
+  a.d = s->d;
+  a.d_ff = s->d_ff;
+  a.bf16 = wdt == MOE_BF16;
+  return a;
 }
 
 }  // namespace
@@ -53,6 +83,62 @@ int moe_layer_norm_backward(int32_t n, int32_t d, const void *dy, const void *x,
   }
   return hip_status(launch_layer_norm_grad(dy, x, act == MOE_BF16, weight, mean, rstd, n, d, dx,
                                            dweight, dbias, (float *)ws, (hipStream_t)stream));
+}
+
+int moe_expert_up_save(const moe_shape *s, const void *a, int act, const int32_t *perm,
+                       const int32_t *offsets, const moe_expert_weights *w, void *h, void *g, void *u,
+                       void *stream) {
+  const int st = check_ffn(s, act, w);
+  if (st != MOE_OK) return st;
+  if (!a || !offsets || !h || !g || !u) return MOE_ERR_NULL;
+  if (act == MOE_BF16 && (!aligned16(a) || !aligned16(h) || !aligned16(g) || !aligned16(u)))
+    return MOE_ERR_ALIGN;
+  return hip_status(launch_expert_up_save(ffn_args(s, a, perm, offsets, w, h, nullptr), g, u,
+                                          (hipStream_t)stream));
+}
+
+size_t moe_grouped_ffn_backward_workspace_bytes(const moe_shape *s, int w_dtype) {
+  if (!s || check_ffn_shape(s, w_dtype, w_dtype) != MOE_OK) return 0;
+  return align_up(ffn_grad_bytes(grad_args(s, w_dtype)));
+}
+
+int moe_grouped_ffn_backward(const moe_shape *s, const void *dy, const void *a, int act,
+                             const int32_t *perm, const int32_t *inv, const float *topk_w,
+                             const int32_t *offsets, const moe_expert_weights *w, const void *g,
+                             const void *u, void *da_perm, void *dw1, void *dw3, void *dw2,
+                             float *dtopk_w, void *ws, size_t ws_bytes, void *stream) {
+  const int st = check_ffn(s, act, w);
+  if (st != MOE_OK) return st;
+  if (!dy || !a || !offsets || !g || !u || !da_perm || !dw1 || !dw3 || !dw2) return MOE_ERR_NULL;
+  const int given = (perm != nullptr) + (inv != nullptr) + (topk_w != nullptr) + (dtopk_w != nullptr);
+  if (given != 0 && given != 4) return MOE_ERR_NULL;
+  if (act == MOE_BF16)
+    for (const void *p : {dy, a, g, u, (const void *)da_perm, (const void *)dw1, (const void *)dw3,
+                          (const void *)dw2})
+      if (!aligned16(p)) return MOE_ERR_ALIGN;
+  if (!ws || ws_bytes < moe_grouped_ffn_backward_workspace_bytes(s, w->dtype)) return MOE_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MOE_ERR_ALIGN;
+  FfnGradArgs f = grad_args(s, w->dtype);
+  f.dy = dy;
+  f.a = a;
+  f.perm = perm;
+  f.inv = inv;
+  f.topk_w = topk_w;
+  f.offsets = offsets;
+  f.w1 = w->w1;
+  f.w3 = w->w3;
+  f.w2 = w->w2;
+  f.slot = w->slot;
+  f.n_slots = w->slot ? w->n_slots : s->E;
+  f.g = g;
+  f.u = u;
+  f.da = da_perm;
+  f.dw1 = dw1;
+  f.dw3 = dw3;
+  f.dw2 = dw2;
+  f.dtopk_w = dtopk_w;
+  f.ws = ws;
+  return hip_status(launch_ffn_grad(f, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -51,3 +51,68 @@ def test_layer_norm_backward_refusals():
         B.moe_layer_norm_backward(4, 0, FAKE, FAKE, "bf16", FAKE, FAKE, FAKE, FAKE, None, None, FAKE, 0,
                                   stream=0)
     assert ei.value.status == -2
+
+
+def _weights(dtype=BF16, **kw):
+    fields = dict(dtype=dtype, w1=FAKE, w3=FAKE, w2=FAKE)
+    fields.update(kw)
+    return B.ExpertWeights(**fields)
+
+
+def _up(shape=(4, 64, 4, 2, 64), a=FAKE, act=BF16, off=FAKE, w=None, h=FAKE, g=FAKE, u=FAKE):
+    sp = None if shape is None else ctypes.byref(B._shape(shape))
+    w = _weights(act) if w is None else w
+    return B.lib.moe_expert_up_save(sp, a, act, FAKE, off, ctypes.byref(w), h, g, u, None)
+
+
+def _back(shape=(4, 64, 4, 2, 64), act=BF16, w=None, nb=1 << 40, **kw):
+    sp = None if shape is None else ctypes.byref(B._shape(shape))
+    w = _weights(act) if w is None else w
+    v = dict(dy=FAKE, a=FAKE, perm=FAKE, inv=FAKE, tw=FAKE, off=FAKE, g=FAKE, u=FAKE, da=FAKE, dw1=FAKE,
+             dw3=FAKE, dw2=FAKE, dtw=FAKE, ws=FAKE)
+    v.update(kw)
+    return B.lib.moe_grouped_ffn_backward(
+        sp, v["dy"], v["a"], act, v["perm"], v["inv"], v["tw"], v["off"], ctypes.byref(w), v["g"], v["u"],
+        v["da"], v["dw1"], v["dw3"], v["dw2"], v["dtw"], v["ws"], nb, None)
+
+
+@pytest.mark.parametrize("call", [_up, _back])
+def test_ffn_training_refuses_shapes_and_types(call):
+    assert call(shape=None) == -1
+    assert call(shape=(0, 64, 4, 2, 64)) == -2
+    assert call(shape=(4, 64, 4, 5, 64)) == -2
+    assert call(shape=(4, 60, 4, 2, 64)) == -2 and call(shape=(4, 64, 4, 2, 60)) == -2
+    assert call(shape=(4, 1 << 20, 4, 2, 64)) == -2 and call(shape=(4, 64, 4, 2, 1 << 20), act=F32) == -2
+    # bf16 operands are addressed with 32-bit offsets, as in the forward pass
+    assert call(shape=(65536, 4096, 8, 2, 14336)) == -2
+    assert call(act=MXFP8) == -3 and call(act=MXFP4) == -3
+    assert call(act=F32, w=_weights(BF16)) == -3 and call(act=BF16, w=_weights(F32)) == -3
+    # MXFP4 weights are not trained
+    assert call(w=_weights(MXFP4, s1=FAKE, s3=FAKE, s2=FAKE)) == -3
+    assert call(w=_weights(BF16, act_quant=MXFP8)) == -3
+    assert call(w=_weights(BF16, w1=None)) == -1 and call(w=_weights(BF16, w2=FAKE + 8)) == -4
+    assert call(w=_weights(BF16, slot=FAKE, n_slots=0)) == -2
+
+
+def test_up_save_refuses_pointers():
+    for name in ("a", "off", "h", "g", "u"):
+        assert _up(**{name: None}) == -1, name
+    for name in ("a", "h", "g", "u"):
+        assert _up(**{name: FAKE + 8}) == -4, name
+
+
+def test_ffn_backward_refuses_pointers_and_workspaces():
+    names = ("dy", "a", "off", "g", "u", "da", "dw1", "dw3", "dw2")
+    for name in names + ("perm", "inv", "tw", "dtw"):  # the last four are given together
+        assert _back(**{name: None}) == -1, name
+    for name in set(names) - {"off"}:
+        assert _back(**{name: FAKE + 8}) == -4, name
+    shape = (4, 64, 4, 2, 64)
+    for dt in ("bf16", "f32"):
+        need = B.moe_grouped_ffn_backward_workspace_bytes(shape, dt)
+        assert need % 256 == 0 and need >= 3 * 8 * 64 * (2 if dt == "bf16" else 4)
+        assert _back(act=B.DTYPES[dt], nb=need - 1) == -5
+    assert _back(ws=None) == -5 and _back(ws=FAKE + 4) == -4
+    assert B.moe_grouped_ffn_backward_workspace_bytes(shape, "mxfp4") == 0
+    assert B.moe_grouped_ffn_backward_workspace_bytes((4, 60, 4, 2, 64), "bf16") == 0
+    assert B.moe_grouped_ffn_backward_workspace_bytes((0, 64, 4, 2, 64), "f32") == 0
