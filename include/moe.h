@@ -393,6 +393,38 @@ int moe_grouped_ffn_backward(const moe_shape *s, const void *dy, const void *a, 
                              const void *u, void *da_perm, void *dw1, void *dw3, void *dw2,
                              float *dtopk_w, void *ws, size_t ws_bytes, void *stream);
 
+/* Gradient of the router, and the tokens' whole input gradient.  With
+ * p = softmax(logits[t]) over all E logits, D = sum_j topk_w[t][j]
+ * dtopk_w[t][j] and the shape's renorm rule:
+ *   renormalised:  dlogits[t][e] = sum_{j: idx = e} topk_w[t][j] (dtopk_w[t][j] - D)
+ *   raw:           dlogits[t][e] = p_e (sum_{j: idx = e} dtopk_w[t][j] - D)
+ *   with f given, the load-balancing loss alpha E sum_i f_i P_i of
+ *   moe_router_stats, f held constant (a count has no gradient), adds
+ *                  alpha E / n p_e (f_e - sum_i f_i p_i)
+ *   dx[t]  = dlogits[t] W_g + sum_j da_perm[inv[t][j]]
+ *   dwg    = dlogits^T x,  dbias = sum_t dlogits[t]
+ * logits   [n][E] f32, topk_idx, topk_w [n][k] as moe_router_topk wrote them;
+ *          ids outside [0, E) have no gradient
+ * dtopk_w  [n][k] f32, as moe_grouped_ffn_backward gives it
+ * f        [E] f32 (moe_router_stats), or NULL: no auxiliary loss
+ * x [n][d], wg [E][d] (act = MOE_F32 or MOE_BF16)
+ * da_perm  [n*k][d] (act) with inv [n][k], or both NULL: dx is the router's
+ *          part alone; inv entries outside [0, n*k) add nothing
+ * dlogits  [n][E] f32 output (required, as logits are in moe_router_topk)
+ * dx [n][d], dwg [E][d] outputs (act), dbias [E] f32 output or NULL
+ * ws       at least moe_router_backward_workspace_bytes(s), 16-byte aligned
+ * Sums are float32; with MOE_BF16 dlogits enters the two products with 16 of
+ * its 24 bits, and dx and dwg are rounded once.  A token whose logits are
+ * all -inf has dlogits 0; one with a NaN logit has NaN.  n < 2^24, d < 2^20;
+ * MOE_BF16 needs d % 8 == 0 and 16-byte aligned x, wg, da_perm, dx and dwg.
+ * Deterministic.  The size helper returns 0 for an invalid shape. */
+size_t moe_router_backward_workspace_bytes(const moe_shape *s);
+int moe_router_backward(const moe_shape *s, const float *logits, const int32_t *topk_idx,
+                        const float *topk_w, const float *dtopk_w, const float *f, float alpha,
+                        const void *x, int act, const void *wg, const void *da_perm,
+                        const int32_t *inv, float *dlogits, void *dx, void *dwg, float *dbias,
+                        void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,6 +25,8 @@ _BINDING_NAMES = (
     "moe_expert_up_save",
     "moe_grouped_ffn_backward",
     "moe_grouped_ffn_backward_workspace_bytes",
+    "moe_router_backward",
+    "moe_router_backward_workspace_bytes",
     "MoeError",
     "Shape",
     "ExpertWeights",

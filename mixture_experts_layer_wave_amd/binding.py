@@ -102,6 +102,11 @@ lib.moe_grouped_ffn_backward_workspace_bytes.argtypes = [_SP, _I]
 lib.moe_grouped_ffn_backward.restype = _I
 lib.moe_grouped_ffn_backward.argtypes = [_SP, _P, _P, _I, _P, _P, _P, _P, _WP, _P, _P, _P, _P, _P, _P, _P,
                                          _P, _SZ, _P]
+lib.moe_router_backward_workspace_bytes.restype = _SZ
+lib.moe_router_backward_workspace_bytes.argtypes = [_SP]
+lib.moe_router_backward.restype = _I
+lib.moe_router_backward.argtypes = [_SP, _P, _P, _P, _P, _P, ctypes.c_float, _P, _I, _P, _P, _P, _P, _P, _P,
+                                    _P, _P, _SZ, _P]
 
 EXPORTS = ("moe_abi_version", "moe_status_string", "moe_workspace_bytes", "moe_mxfp8_bytes",
            "moe_quantize_mxfp8", "moe_router_topk",
@@ -109,7 +114,8 @@ EXPORTS = ("moe_abi_version", "moe_status_string", "moe_workspace_bytes", "moe_m
            "moe_dispatch_workspace_bytes", "moe_dispatch", "moe_grouped_ffn", "moe_expert_up", "moe_expert_down", "moe_combine",
            "moe_forward", "moe_forward_noalloc", "moe_layer_norm",
            "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward",
-           "moe_expert_up_save", "moe_grouped_ffn_backward_workspace_bytes", "moe_grouped_ffn_backward")
+           "moe_expert_up_save", "moe_grouped_ffn_backward_workspace_bytes", "moe_grouped_ffn_backward",
+           "moe_router_backward_workspace_bytes", "moe_router_backward")
 
 
 def _ptr(t):
@@ -284,3 +290,15 @@ def moe_grouped_ffn_backward(shape, dy, a, act, perm, inv, topk_w, offsets, weig
         ctypes.byref(_shape(shape)), _ptr(dy), _ptr(a), _dt(act), _ptr(perm), _ptr(inv), _ptr(topk_w),
         _ptr(offsets), ctypes.byref(w), _ptr(g), _ptr(u), _ptr(da_perm), _ptr(dw1), _ptr(dw3), _ptr(dw2),
         _ptr(dtopk_w), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moe_router_backward_workspace_bytes(shape) -> int:
+    return int(lib.moe_router_backward_workspace_bytes(ctypes.byref(_shape(shape))))
+
+
+def moe_router_backward(shape, logits, topk_idx, topk_w, dtopk_w, f, alpha, x, act, wg, da_perm, inv,
+                        dlogits, dx, dwg, dbias, ws, ws_bytes, stream=None):
+    _check("moe_router_backward", lib.moe_router_backward(
+        ctypes.byref(_shape(shape)), _ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(dtopk_w), _ptr(f),
+        float(alpha), _ptr(x), _dt(act), _ptr(wg), _ptr(da_perm), _ptr(inv), _ptr(dlogits), _ptr(dx),
+        _ptr(dwg), _ptr(dbias), _ptr(ws), int(ws_bytes), _stream(stream)))

@@ -25,6 +25,7 @@
 #include "gemm_common.h"
 #include "gemm_grad.h"
 #include "kernels.h"
+#include "kmajor.h"
 
 namespace moe {
 namespace {
@@ -57,37 +58,6 @@ struct GradParams {
 
 __device__ __forceinline__ void lgkm_wait0() {
   __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
-}
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-// K-major tile: row k holds W columns; 16-B chunk c of row k is stored at
-// c ^ (k % 4 * 4).  A transposing read takes 64 consecutive bytes of four
-// consecutive rows per half wave, which the key puts in four different
-// quarters of the 64 banks.
-__device__ __forceinline__ int kmaj_key(int k) { return (k & 3) << 2; }
-
-// Byte offset in a K-major tile of W columns that this lane hands to the
-// transposing reads of the 32-column fragment at column `col`: 16-lane group
-// g of the wave covers columns 16 (g % 2) .. + 15 and K rows 8 (g / 2) .. + 3
-// of the slice; lane i of it reads four columns of row i / 4.
-template <int W>
-__device__ __forceinline__ int kmaj_lane(int col, int lane) {
-  const int grp = lane >> 4, i = lane & 15;
-  const int chunk = ((col + (grp & 1) * 16) >> 3) + ((i & 3) >> 1);
-  return ((grp >> 1) * 8 + (i >> 2)) * (W * 2) + ((chunk ^ kmaj_key(i >> 2)) << 4) + (i & 1) * 8;
-}
-
-// The fragment of slice kk: K rows 16 kk + 8 (lane / 32) + 0 .. 7.
-template <int W>
-__device__ __forceinline__ bf16x8 kmaj_frag(const uint8_t *tile, int lane_off, int kk) {
-  const uint8_t *p = tile + lane_off + kk * 16 * (W * 2);
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * (W * 2)));
-  const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-  return __builtin_bit_cast(bf16x8, v);
 }
 
 // Combine weight of pile row r of token t: that of the pair whose row it is.
@@ -260,10 +230,10 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradParams p) {
   constexpr int A_CPR = BM / 8, B_CPR = BN / 8;             // chunks per K-major row
   constexpr int A_RPR = 64 / A_CPR, B_RPR = 64 / B_CPR;     // rows per run
   const int b_kr = wave * B_RPR + lane / B_CPR;
-  const int b_col = n0 + (((lane % B_CPR) ^ kmaj_key(b_kr)) << 3);
+  const int b_col = n0 + (((lane % B_CPR) ^ kmaj_key<BN>(b_kr)) << 3);
   const uint32_t b_pen = b_col < N ? 0u : kOOB;
   const int a_kr = wave * A_RPR + lane / A_CPR;
-  const int a_col = WEIGHT ? m0 + (((lane % A_CPR) ^ kmaj_key(a_kr)) << 3) : 0;
+  const int a_col = WEIGHT ? m0 + (((lane % A_CPR) ^ kmaj_key<BM>(a_kr)) << 3) : 0;
   const uint32_t a_pen = WEIGHT && a_col >= lda ? kOOB : 0u;
   static_assert((kNW * A_RPR) % 4 == 0 && (kNW * B_RPR) % 4 == 0, "a lane's key is the same in every run");
   // Row-major A tile (rows of 64 K, 128 B): as in the forward GEMM.

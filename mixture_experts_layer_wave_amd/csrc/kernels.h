@@ -167,6 +167,26 @@ hipError_t launch_tail_sum(const float *tail, int S, size_t plane, const int32_t
 // aligned.
 hipError_t launch_f32_to_bf16(const float *src, uint16_t *dst, size_t count, hipStream_t st);
 
+// ---- router gradient -------------------------------------------------------
+struct RouterGradArgs {
+  const float *logits;             // [n][E]
+  const int32_t *idx;              // [n][k]
+  const float *topk_w, *dtopk_w;   // [n][k]
+  const float *f;                  // [E], or NULL: no auxiliary loss
+  float alpha;
+  int n, d, E, k;
+  bool renorm, bf16;
+  const void *x, *wg;              // [n][d], [E][d]
+  const void *da;                  // [n k][d] added to the tokens' rows through inv, or NULL
+  const int32_t *inv;
+  float *dlogits;                  // [n][E]
+  void *dx, *dwg;                  // [n][d], [E][d]
+  float *dbias;                    // [E] or NULL
+  void *ws;                        // router_grad_bytes
+};
+size_t router_grad_bytes(int n, int d, int E);
+hipError_t launch_router_grad(const RouterGradArgs &a, hipStream_t st);
+
 // ---- layer norm -----------------------------------------------------------
 // y = (x - mean) rstd w + b over rows of d (<= kLayerNormMaxD); b, mean and
 // rstd may be NULL.  n = 0 launches nothing.  bf16: d % 8 == 0 and 16-byte aligned

@@ -1,0 +1,405 @@
+// The router's gradient ("How Mixture of Experts Scales Model Parameters",
+// sections "Routing", "Top-K" and "Load balancing").
+//
+// With p = softmax(z) over all E logits of a token, c_j its chosen experts,
+// w_j their weights and dw_j the loss's gradient with respect to them:
+//   renormalised (w = p_c / sum p_c, a softmax over the chosen logits)
+//     dz_c += w_j (dw_j - D)                     D = sum_j w_j dw_j
+//   raw (w = p_c)
+//     dz_e  = p_e (sum_{j: c_j = e} dw_j - D)
+//   and, for the auxiliary loss alpha E sum_i f_i P_i with f held constant,
+//     dz_e += alpha E / n p_e (f_e - sum_i f_i p_i).
+// Then  dx = dz W_g (+ the token's expert rows da[inv]),  dW_g = dz^T x,
+// dbias = sum_t dz.
+//
+// dz is float32.  For bf16 x and W_g the two products run on the bf16 matrix
+// cores with dz split into a bf16 value and the bf16 rest, two MFMAs in place
+// of one: the operand keeps 16 of float32's 24 bits, so dx and dW_g are
+// rounded only on their way out.  Both products are too narrow (E) to matter
+// beside their traffic: dx reads n k + writes n rows of d, dW_g reads n.
+#include "common.h"
+#include "gemm_f32.h"
+#include "kernels.h"
+#include "kmajor.h"
+#include "route_dev.h"
+
+namespace moe {
+namespace {
+
+// ---- dz: one group of G = topk_group(E) lanes per token -----------------------
+__global__ __launch_bounds__(256) void router_dz_kernel(
+    const float *__restrict__ logits, const int32_t *__restrict__ idx, const float *__restrict__ w,
+    const float *__restrict__ dw, const float *__restrict__ f, float aux, int n, int E, int k, int renorm,
+    float *__restrict__ dz) {
+  const int G = topk_group(E);
+  const int gl = (threadIdx.x & 63) & (G - 1);
+  const int t = (blockIdx.x * 256 + threadIdx.x) / G;
+  if ((blockIdx.x * 256 + (threadIdx.x & ~63)) / G >= n) return;  // whole wave idle
+  const bool live = t < n;
+  const size_t row = live ? t : 0;
+  const float *z = logits + row * E;
+  idx += row * k;
+  w += row * k;
+  dw += row * k;
+  float D = 0.f;
+  for (int j = 0; j < k; ++j)
+    if ((unsigned)idx[j] < (unsigned)E) D = fmaf(w[j], dw[j], D);
+  float m = -__builtin_inff();
+  for (int e = gl; e < E; e += G) m = fmaxf(m, z[e]);
+  m = group_max(m, G);
+  float s = 0.f, fp = 0.f;
+  for (int e = gl; e < E; e += G) {
+    const float q = expf(z[e] - m);
+    s += q;
+    if (f) fp = fmaf(q, f[e], fp);
+  }
+  s = group_sum(s, G);
+  fp = group_sum(fp, G) / s;
+  if (!live) return;
+  for (int e = gl; e < E; e += G) {
+    float v = 0.f;
+    // a token whose logits are all -inf has no expert and no gradient
+    if (m != -__builtin_inff()) {
+      const float p = expf(z[e] - m) / s;
+      if (renorm) {
+        for (int j = 0; j < k; ++j)
+          if (idx[j] == e) v = fmaf(w[j], dw[j] - D, v);
+      } else {
+        float g = 0.f;
+        for (int j = 0; j < k; ++j)
+          if (idx[j] == e) g += dw[j];
+        v = p * (g - D);
+      }
+      if (f) v = fmaf(aux * p, f[e] - fp, v);
+    }
+    dz[row * E + e] = v;
+  }
+}
+
+// x = hi + lo + rest, the rest below 2^-16 of x.
+__device__ __forceinline__ void split_bf16(float x, uint16_t &hi, uint16_t &lo) {
+  hi = (uint16_t)f32_to_bf16_bits(x);
+  const float r = x - bf16_bits_to_f32(hi);
+  // (an infinite or NaN x keeps its value in hi; the rest would be NaN)
+  lo = __builtin_isfinite(x) ? (uint16_t)f32_to_bf16_bits(r) : 0;
+}
+
+// ---- dx, bf16 -------------------------------------------------------------------
+// Block: 4 waves, 32 tokens x 256 columns (each wave 64), 32 experts a step.
+// The router's part goes through LDS as float32, so that the gathered rows
+// and dx itself are read and written as whole 512-B row pieces.
+constexpr int kXT = 32, kXC = 256, kXE = 32, kXPitch = kXC + 4, kZPitch = kXE + 8;
+
+__global__ __launch_bounds__(256) void router_dx_bf16_kernel(
+    const float *__restrict__ dz, const uint16_t *__restrict__ wg, const uint16_t *__restrict__ da,
+    const int32_t *__restrict__ inv, int n, int d, int E, int k, uint16_t *__restrict__ dx) {
+  union Lds {
+    struct {
+      uint8_t w[kXE * kXC * 2];
+      uint16_t hi[kXT * kZPitch], lo[kXT * kZPitch];
+    } in;
+    float out[kXT * kXPitch];
+  };
+  __shared__ __attribute__((aligned(16))) Lds s;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int t0 = blockIdx.x * kXT, c0 = blockIdx.y * kXC;
+  f32x16 acc[2] = {};
+  int b_lane[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) b_lane[j] = kmaj_lane<kXC>(wave * 64 + j * 32, lane);
+  for (int e0 = 0; e0 < E; e0 += kXE) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kXE * kXC / 8 / 256; ++i) {
+      const int e = (tid >> 5) + 8 * i, ch = tid & 31;
+      u32x4 v = {};
+      if (e0 + e < E && c0 + ch * 8 < d) v = *(const u32x4 *)(wg + (size_t)(e0 + e) * d + c0 + ch * 8);
+      *(u32x4 *)(s.in.w + e * kXC * 2 + ((ch ^ kmaj_key<kXC>(e)) << 4)) = v;
+    }
+#pragma unroll
+    for (int i = 0; i < kXT * kXE / 256; ++i) {
+      const int e = tid & 31, t = (tid >> 5) + 8 * i;
+      const float v = e0 + e < E && t0 + t < n ? dz[(size_t)(t0 + t) * E + e0 + e] : 0.f;
+      split_bf16(v, s.in.hi[t * kZPitch + e], s.in.lo[t * kZPitch + e]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int kk = 0; kk < kXE / 16; ++kk) {
+      if (e0 + kk * 16 >= E) break;
+      const int at = (lane & 31) * kZPitch + kk * 16 + (lane >> 5) * 8;
+      const bf16x8 hi = *(const bf16x8 *)(s.in.hi + at), lo = *(const bf16x8 *)(s.in.lo + at);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bf16x8 b = kmaj_frag<kXC>(s.in.w, b_lane[j], kk);
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, hi, acc[j], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, lo, acc[j], 0, 0, 0);
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *(f32x4 *)(s.out + (lane & 31) * kXPitch + wave * 64 + j * 32 + g * 8 + (lane >> 5) * 4) =
+          f32x4{acc[j][g * 4], acc[j][g * 4 + 1], acc[j][g * 4 + 2], acc[j][g * 4 + 3]};
+  __syncthreads();
+  const int ch = tid & 31, col = c0 + ch * 8;
+  const unsigned R = (unsigned)n * (unsigned)k;
+  if (col >= d) return;
+#pragma unroll
+  for (int i = 0; i < kXT / 8; ++i) {
+    const int r = (tid >> 5) + 8 * i, t = t0 + r;
+    if (t >= n) break;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = s.out[r * kXPitch + ch * 8 + j];
+    if (da)
+      for (int j = 0; j < k; ++j) {
+        const int pr = inv[(size_t)t * k + j];
+        if ((unsigned)pr >= R) continue;
+        const u32x4 q = *(const u32x4 *)(da + (size_t)pr * d + col);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          v[2 * b] += __uint_as_float(q[b] << 16);
+          v[2 * b + 1] += __uint_as_float(q[b] & 0xffff0000u);
+        }
+      }
+    *(u32x4 *)(dx + (size_t)t * d + col) =
+        u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+  }
+}
+
+// ---- dW_g, bf16 -----------------------------------------------------------------
+// Block: 4 waves, EW experts x 128 columns (each wave 32) over a range of the
+// tokens, 64 at a step; the ranges' float32 planes part[s][E][d] (and the
+// bias's, after them) are added in order by router_sum_kernel.
+constexpr int kWC = 128, kWT = 64;
+
+template <int EW>
+__global__ __launch_bounds__(256) void router_dw_bf16_kernel(const float *__restrict__ dz,
+                                                             const uint16_t *__restrict__ x, int n, int d,
+                                                             int E, int range, float *__restrict__ part,
+                                                             float *__restrict__ bias_part) {
+  constexpr int TM = EW / 32;
+  constexpr int ZR = 256 / EW, ZN = kWT / ZR;  // dz: rows per pass, passes
+  __shared__ __attribute__((aligned(16))) uint8_t s_x[kWT * kWC * 2];
+  __shared__ __attribute__((aligned(16))) uint8_t s_hi[kWT * EW * 2], s_lo[kWT * EW * 2];
+  __shared__ float s_b[256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int c0 = blockIdx.x * kWC, e0 = blockIdx.z * EW;
+  const int tb = blockIdx.y * range, te = min(n, tb + range);
+  const int ze = tid % EW, zt = tid / EW;
+  const int xch = tid & 15, xt = tid >> 4;
+  u32x4 xr[4];
+  float zr[ZN], bias = 0.f;
+  auto fetch = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + xt + 16 * i;
+      xr[i] = u32x4{};
+      if (t < te && c0 + xch * 8 < d) xr[i] = *(const u32x4 *)(x + (size_t)t * d + c0 + xch * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < ZN; ++i) {
+      const int t = t0 + zt + ZR * i;
+      zr[i] = t < te && e0 + ze < E ? dz[(size_t)t * E + e0 + ze] : 0.f;
+    }
+  };
+  f32x16 acc[TM] = {};
+  int a_lane[TM];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) a_lane[i] = kmaj_lane<EW>(i * 32, lane);
+  const int b_lane = kmaj_lane<kWC>(wave * 32, lane);
+  fetch(tb);
+  for (int t0 = tb; t0 < te; t0 += kWT) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = xt + 16 * i;
+      *(u32x4 *)(s_x + t * kWC * 2 + ((xch ^ kmaj_key<kWC>(t)) << 4)) = xr[i];
+    }
+#pragma unroll
+    for (int i = 0; i < ZN; ++i) {
+      const int t = zt + ZR * i;
+      const int at = t * EW * 2 + (((ze >> 3) ^ kmaj_key<EW>(t)) << 4) + (ze & 7) * 2;
+      split_bf16(zr[i], *(uint16_t *)(s_hi + at), *(uint16_t *)(s_lo + at));
+      bias += zr[i];
+    }
+    __syncthreads();
+    if (t0 + kWT < te) fetch(t0 + kWT);
+#pragma unroll
+    for (int kk = 0; kk < kWT / 16; ++kk) {
+      const bf16x8 b = kmaj_frag<kWC>(s_x, b_lane, kk);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, kmaj_frag<EW>(s_hi, a_lane[i], kk), acc[i], 0, 0, 0);
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, kmaj_frag<EW>(s_lo, a_lane[i], kk), acc[i], 0, 0, 0);
+      }
+    }
+  }
+  float *out = part + (size_t)blockIdx.y * E * d;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int e = e0 + i * 32 + (lane & 31);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int col = c0 + wave * 32 + g * 8 + (lane >> 5) * 4;
+      if (e < E && col < d)
+        *(f32x4 *)(out + (size_t)e * d + col) =
+            f32x4{acc[i][g * 4], acc[i][g * 4 + 1], acc[i][g * 4 + 2], acc[i][g * 4 + 3]};
+    }
+  }
+  if (blockIdx.x == 0) {  // the bias's sum over this range, in row order
+    s_b[tid] = bias;
+    __syncthreads();
+    if (zt == 0 && e0 + ze < E) {
+      float v = 0.f;
+      for (int i = 0; i < ZR; ++i) v += s_b[i * EW + ze];
+      bias_part[(size_t)blockIdx.y * E + e0 + ze] = v;
+    }
+  }
+}
+
+// dW_g = the sum of S planes, in order; dbias likewise (threads past E d).
+template <bool BF>
+__global__ __launch_bounds__(256) void router_sum_kernel(const float *__restrict__ part,
+                                                         const float *__restrict__ bias_part, int S, int E,
+                                                         int d, void *__restrict__ dwg,
+                                                         float *__restrict__ dbias) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, ed = (size_t)E * d;
+  if (i < ed) {
+    float v = 0.f;
+    for (int s = 0; s < S; ++s) v += part[(size_t)s * ed + i];
+    if constexpr (BF)
+      ((uint16_t *)dwg)[i] = (uint16_t)f32_to_bf16_bits(v);
+    else
+      ((float *)dwg)[i] = v;
+  } else if (i < ed + E && dbias) {
+    float v = 0.f;
+    for (int s = 0; s < S; ++s) v += bias_part[(size_t)s * E + (i - ed)];
+    dbias[i - ed] = v;
+  }
+}
+
+// ---- float32 ----------------------------------------------------------------------
+using namespace f32gemm;
+
+__global__ __launch_bounds__(kThreads) void router_dx_f32_kernel(
+    const float *__restrict__ dz, const float *__restrict__ wg, const float *__restrict__ da,
+    const int32_t *__restrict__ inv, int n, int d, int E, int k, float *__restrict__ dx) {
+  __shared__ float smem[2 * kK * kPitch];
+  const int t0 = blockIdx.x * kT, c0 = blockIdx.y * kT;
+  f32x16 acc = {};
+  product<false, true>(
+      acc, smem, E, [&](int, int e, int t) { return t0 + t < n ? dz[(size_t)(t0 + t) * E + e] : 0.f; },
+      [&](int, int e, int c) { return c0 + c < d ? wg[(size_t)e * d + c0 + c] : 0.f; });
+  const int t = t0 + out_row();
+  const unsigned R = (unsigned)n * (unsigned)k;
+  if (t >= n) return;
+  if (da)
+    for (int j = 0; j < k; ++j) {
+      const int pr = inv[(size_t)t * k + j];
+      if ((unsigned)pr >= R) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int c = c0 + out_col(i);
+        if (c < d) acc[i] += da[(size_t)pr * d + c];
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = c0 + out_col(i);
+    if (c < d) dx[(size_t)t * d + c] = acc[i];
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void router_dw_f32_kernel(const float *__restrict__ dz,
+                                                                 const float *__restrict__ x, int n, int d,
+                                                                 int E, int range, float *__restrict__ part,
+                                                                 float *__restrict__ bias_part) {
+  __shared__ float smem[2 * kK * kPitch];
+  __shared__ float s_b[kThreads];
+  const int c0 = blockIdx.x * kT, e0 = blockIdx.z * kT;
+  const int tb = blockIdx.y * range, te = min(n, tb + range);
+  f32x16 acc = {};
+  product<true, true>(
+      acc, smem, te - tb,
+      [&](int, int t, int e) { return e0 + e < E ? dz[(size_t)(tb + t) * E + e0 + e] : 0.f; },
+      [&](int, int t, int c) { return c0 + c < d ? x[(size_t)(tb + t) * d + c0 + c] : 0.f; });
+  const int e = e0 + out_row();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = c0 + out_col(i);
+    if (e < E && c < d) part[((size_t)blockIdx.y * E + e) * d + c] = acc[i];
+  }
+  if (blockIdx.x == 0) {
+    const int be = e0 + (threadIdx.x & 63), s = threadIdx.x >> 6;
+    float v = 0.f;
+    if (be < E)
+      for (int t = tb + s; t < te; t += 4) v += dz[(size_t)t * E + be];
+    s_b[threadIdx.x] = v;
+    __syncthreads();
+    if (s == 0 && be < E)
+      bias_part[(size_t)blockIdx.y * E + be] =
+          s_b[threadIdx.x] + s_b[threadIdx.x + 64] + s_b[threadIdx.x + 128] + s_b[threadIdx.x + 192];
+  }
+}
+
+// Token ranges of the dW_g product: about two blocks per CU, but planes of
+// at most the bytes of x (S E 4 <= n 2), and whole steps.
+struct Ranges {
+  int S, range;
+};
+Ranges dw_ranges(int n, int d, int E) {
+  const int tiles = ((d + kWC - 1) / kWC) * ((E + 127) / 128);
+  int S = (512 + tiles - 1) / tiles;
+  const int most = n / (2 * E) > 1 ? n / (2 * E) : 1;
+  if (S > most) S = most;
+  int range = (n + S - 1) / S;
+  range = (range + kWT - 1) / kWT * kWT;
+  return {(n + range - 1) / range, range};
+}
+
+}  // namespace
+
+size_t router_grad_bytes(int n, int d, int E) {
+  return (size_t)dw_ranges(n, d, E).S * ((size_t)E * d + E) * sizeof(float);
+}
+
+hipError_t launch_router_grad(const RouterGradArgs &a, hipStream_t st) {
+  const int per_block = 256 / topk_group(a.E);
+  router_dz_kernel<<<(a.n + per_block - 1) / per_block, 256, 0, st>>>(
+      a.logits, a.idx, a.topk_w, a.dtopk_w, a.f, a.alpha * (float)a.E / (float)a.n, a.n, a.E, a.k,
+      a.renorm ? 1 : 0, a.dlogits);
+  const Ranges q = dw_ranges(a.n, a.d, a.E);
+  float *part = (float *)a.ws, *bias_part = part + (size_t)q.S * a.E * a.d;
+  if (a.bf16) {
+    router_dx_bf16_kernel<<<dim3((a.n + kXT - 1) / kXT, (a.d + kXC - 1) / kXC), 256, 0, st>>>(
+        a.dlogits, (const uint16_t *)a.wg, (const uint16_t *)a.da, a.inv, a.n, a.d, a.E, a.k,
+        (uint16_t *)a.dx);
+    // experts of a block: as many 32-wide groups as there are, up to 128
+    const int EW = a.E <= 32 ? 32 : (a.E <= 64 ? 64 : 128);
+    const dim3 grid((a.d + kWC - 1) / kWC, q.S, (a.E + EW - 1) / EW);
+    auto go = [&](auto kern) {
+      kern<<<grid, 256, 0, st>>>(a.dlogits, (const uint16_t *)a.x, a.n, a.d, a.E, q.range, part, bias_part);
+    };
+    if (EW == 32)
+      go(router_dw_bf16_kernel<32>);
+    else if (EW == 64)
+      go(router_dw_bf16_kernel<64>);
+    else
+      go(router_dw_bf16_kernel<128>);
+  } else {
+    router_dx_f32_kernel<<<dim3((a.n + kT - 1) / kT, (a.d + kT - 1) / kT), kThreads, 0, st>>>(
+        a.dlogits, (const float *)a.wg, (const float *)a.da, a.inv, a.n, a.d, a.E, a.k, (float *)a.dx);
+    router_dw_f32_kernel<<<dim3((a.d + kT - 1) / kT, q.S, (a.E + kT - 1) / kT), kThreads, 0, st>>>(
+        a.dlogits, (const float *)a.x, a.n, a.d, a.E, q.range, part, bias_part);
+  }
+  const size_t outs = (size_t)a.E * a.d + a.E;
+  auto sum = a.bf16 ? router_sum_kernel<true> : router_sum_kernel<false>;
+  sum<<<(unsigned)((outs + 255) / 256), 256, 0, st>>>(part, bias_part, q.S, a.E, a.d, a.dwg, a.dbias);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -49,6 +49,12 @@ FfnGradArgs grad_args(const moe_shape *s, int wdt) {
   return a;
 }
 
+int check_router(const moe_shape *s) {
+  const int st = check_shape(s);
+  if (st != MOE_OK) return st;
+  return s->n < (1 << 24) && s->d < (1 << 20) ? MOE_OK : MOE_ERR_SHAPE;
+}
+
 }  // namespace
 
 extern "C" {
@@ -139,6 +145,53 @@ int moe_grouped_ffn_backward(const moe_shape *s, const void *dy, const void *a, 
   f.dtopk_w = dtopk_w;
   f.ws = ws;
   return hip_status(launch_ffn_grad(f, (hipStream_t)stream));
+}
+
+size_t moe_router_backward_workspace_bytes(const moe_shape *s) {
+  if (check_router(s) != MOE_OK) return 0;
+  return align_up(router_grad_bytes(s->n, s->d, s->E));
+}
+
+int moe_router_backward(const moe_shape *s, const float *logits, const int32_t *topk_idx,
+                        const float *topk_w, const float *dtopk_w, const float *f, float alpha,
+                        const void *x, int act, const void *wg, const void *da_perm,
+                        const int32_t *inv, float *dlogits, void *dx, void *dwg, float *dbias, void *ws,
+                        size_t ws_bytes, void *stream) {
+  const int st = check_router(s);
+  if (st != MOE_OK) return st;
+  if (act != MOE_F32 && act != MOE_BF16) return MOE_ERR_DTYPE;
+  if (act == MOE_BF16 && s->d % 8) return MOE_ERR_SHAPE;
+  if (!logits || !topk_idx || !topk_w || !dtopk_w || !x || !wg || !dlogits || !dx || !dwg)
+    return MOE_ERR_NULL;
+  if ((da_perm != nullptr) != (inv != nullptr)) return MOE_ERR_NULL;
+  if (act == MOE_BF16)
+    for (const void *p : {x, wg, da_perm, (const void *)dx, (const void *)dwg})
+      if (!aligned16(p)) return MOE_ERR_ALIGN;
+  if (!ws || ws_bytes < moe_router_backward_workspace_bytes(s)) return MOE_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MOE_ERR_ALIGN;
+  RouterGradArgs a{};
+  a.logits = logits;
+  a.idx = topk_idx;
+  a.topk_w = topk_w;
+  a.dtopk_w = dtopk_w;
+  a.f = f;
+  a.alpha = alpha;
+  a.n = s->n;
+  a.d = s->d;
+  a.E = s->E;
+  a.k = s->k;
+  a.renorm = renorm_of(s);
+  a.bf16 = act == MOE_BF16;
+  a.x = x;
+  a.wg = wg;
+  a.da = da_perm;
+  a.inv = inv;
+  a.dlogits = dlogits;
+  a.dx = dx;
+  a.dwg = dwg;
+  a.dbias = dbias;
+  a.ws = ws;
+  return hip_status(launch_router_grad(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

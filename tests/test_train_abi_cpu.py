@@ -116,3 +116,31 @@ def test_ffn_backward_refuses_pointers_and_workspaces():
     assert B.moe_grouped_ffn_backward_workspace_bytes(shape, "mxfp4") == 0
     assert B.moe_grouped_ffn_backward_workspace_bytes((4, 60, 4, 2, 64), "bf16") == 0
     assert B.moe_grouped_ffn_backward_workspace_bytes((0, 64, 4, 2, 64), "f32") == 0
+
+
+def _router(shape=(4, 64, 4, 2, 64), act=BF16, nb=1 << 40, **kw):
+    sp = None if shape is None else ctypes.byref(B._shape(shape))
+    v = dict(z=FAKE, idx=FAKE, w=FAKE, dw=FAKE, f=FAKE, x=FAKE, wg=FAKE, da=FAKE, inv=FAKE, dz=FAKE, dx=FAKE,
+             dwg=FAKE, db=FAKE, ws=FAKE)
+    v.update(kw)
+    return B.lib.moe_router_backward(sp, v["z"], v["idx"], v["w"], v["dw"], v["f"], 0.01, v["x"], act, v["wg"],
+                                     v["da"], v["inv"], v["dz"], v["dx"], v["dwg"], v["db"], v["ws"], nb, None)
+
+
+def test_router_backward_refusals():
+    assert _router(shape=None) == -1
+    assert _router(shape=(4, 64, 4, 5, 64)) == -2 and _router(shape=(1 << 24, 64, 4, 1, 64)) == -2
+    assert _router(shape=(4, 1 << 20, 4, 2, 64)) == -2 and _router(shape=(4, 60, 4, 2, 64)) == -2
+    assert _router(act=MXFP4) == -3 and _router(act=MXFP8) == -3
+    for name in ("z", "idx", "w", "dw", "x", "wg", "dz", "dx", "dwg", "da", "inv"):
+        assert _router(**{name: None}) == -1, name  # da_perm and inv are given together
+    for name in ("x", "wg", "da", "dx", "dwg"):
+        assert _router(**{name: FAKE + 8}) == -4, name
+    shape = (4, 64, 4, 2, 64)
+    need = B.moe_router_backward_workspace_bytes(shape)
+    assert need % 256 == 0 and need >= 4 * (64 + 1) * 4
+    assert _router(nb=need - 1) == -5 and _router(ws=None) == -5 and _router(ws=FAKE + 4) == -4
+    assert B.moe_router_backward_workspace_bytes((0, 64, 4, 2, 64)) == 0
+    # the partial planes of W_g's gradient stay within the bytes of x
+    for n, d, E in ((8192, 4096, 8), (4096, 2880, 128), (65536, 256, 64)):
+        assert B.moe_router_backward_workspace_bytes((n, d, E, 1, 8)) <= max(n * 2, 4 * E) * (d + 1) + 256
