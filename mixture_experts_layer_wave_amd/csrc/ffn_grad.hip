@@ -42,19 +42,18 @@ __global__ __launch_bounds__(1024) void weight_grad_kernel(const float *__restri
 }
 
 struct Layout {
-  size_t dg, du, hs, part, total;
-  int planes;
+  size_t du, hs, part, total;
 };
 
 Layout layout(const FfnGradArgs &a) {
   Layout L{};
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   const size_t mat = up((size_t)a.R * a.d_ff * (a.bf16 ? 2 : 4));
-  L.planes = a.bf16 ? grad_planes_bf16(a.d_ff) : grad_planes_f32(a.d_ff);
+  const int planes = a.bf16 ? grad_planes_bf16(a.d_ff) : grad_planes_f32(a.d_ff);
   L.du = mat;
   L.hs = 2 * mat;
   L.part = 3 * mat;
-  L.total = L.part + up((size_t)L.planes * a.R * 4);
+  L.total = L.part + up((size_t)planes * a.R * 4);
   return L;
 }
 
@@ -65,10 +64,11 @@ size_t ffn_grad_bytes(const FfnGradArgs &a) { return layout(a).total; }
 hipError_t launch_ffn_grad(const FfnGradArgs &a, hipStream_t st) {
   const Layout L = layout(a);
   char *base = (char *)a.ws;
-  const FfnGradWs w{base, base + L.du, base + L.hs, (float *)(base + L.part), L.planes};
-  const hipError_t e = a.bf16 ? launch_grad_bf16(a, w, st) : launch_grad_f32(a, w, st);
+  const FfnGradWs w{base, base + L.du, base + L.hs, (float *)(base + L.part)};
+  int planes = 0;
+  const hipError_t e = a.bf16 ? launch_grad_bf16(a, w, &planes, st) : launch_grad_f32(a, w, &planes, st);
   if (e != hipSuccess || !a.perm) return e;
-  weight_grad_kernel<<<(a.R + 63) / 64, 1024, 0, st>>>(w.part, w.planes, a.R, a.E, a.offsets, a.perm,
+  weight_grad_kernel<<<(a.R + 63) / 64, 1024, 0, st>>>(w.part, planes, a.R, a.E, a.offsets, a.perm,
                                                        a.inv, a.k, a.dtopk_w);
   return hipGetLastError();
 }

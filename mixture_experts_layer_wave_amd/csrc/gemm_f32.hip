@@ -195,7 +195,8 @@ hipError_t launch_up_save_f32(const FfnArgs &a, void *g, void *u, hipStream_t st
   return hipGetLastError();
 }
 
-hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t st) {
+hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, int *planes, hipStream_t st) {
+  *planes = grad_planes_f32(a.d_ff);
   F32Params p{};
   p.a = (const float *)a.a;
   p.dy = (const float *)a.dy;

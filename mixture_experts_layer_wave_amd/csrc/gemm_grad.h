@@ -40,13 +40,13 @@ hipError_t launch_ffn_grad(const FfnGradArgs &a, hipStream_t st);
 struct FfnGradWs {
   void *dg, *du, *hs;
   float *part;
-  int planes;
 };
 
-// The products, in this order on the stream.
-hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t st);
+// The products, in this order on the stream; *planes: the planes of part
+// that they write (at most grad_planes_*).
+hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, int *planes, hipStream_t st);
 int grad_planes_bf16(int d_ff);
-hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t st);
+hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, int *planes, hipStream_t st);
 int grad_planes_f32(int d_ff);
 
 }  // namespace moe

@@ -26,13 +26,12 @@
 #include "gemm_grad.h"
 #include "kernels.h"
 #include "kmajor.h"
+#include "route_dev.h"
 
 namespace moe {
 namespace {
 
 using namespace gemm;
-
-constexpr int kBK = 64;
 
 enum Mode { DH, DX, DW13, DW2 };
 
@@ -68,17 +67,74 @@ __device__ __forceinline__ float pair_weight(const int32_t *inv, const float *w,
   return v;
 }
 
-// DH epilogue.  Two runs of four columns of a row, held by lanes l and
-// l + 32, are exchanged so that a lane has eight consecutive columns: g and u
-// come and dg, du, w h go as 16-B pieces.  dh0, h and the products stay
-// float32; dg, du and w h are rounded once to bf16, the type of the MFMA that
-// reads them next.  The row sums of dh0 h over this wave's columns go to
-// part[plane][row].
-template <int TM, int TN, int WM, int WN>
-__device__ __forceinline__ void store_dh(const f32x16 (&acc)[TM][TN], const GradParams &p,
-                                         const float (&wrow)[TM], int row0, int rows, int n0, int nt,
-                                         int wm, int wn) {
+// Epilogues.  An accumulator holds runs of four columns of 32 rows; stored
+// straight from registers a wave's instruction would touch 32 bytes of each
+// of 32 rows.  Instead a wave passes 32 rows x 64 columns at a time through
+// its own piece of LDS (float32, rows 272 bytes apart) and goes on with whole
+// 128-byte lines: 8 lanes a row, eight consecutive columns each, 8 rows per
+// instruction.
+constexpr int kEpiPitch = 68;                      // floats per row
+constexpr int kEpiWave = 32 * kEpiPitch * 4;       // bytes per wave
+
+// Rows 32 tm .. and columns 64 jj .. of the wave's tile into its LDS piece.
+template <int TM, int TN>
+__device__ __forceinline__ void epi_put(const f32x16 (&acc)[TM][TN], int tm, int jj, float *piece) {
   const int lane = __lane_id(), lr = lane & 31, lg = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *(f32x4 *)(piece + lr * kEpiPitch + j * 32 + g * 8 + lg * 4) =
+          f32x4{acc[tm][2 * jj + j][g * 4], acc[tm][2 * jj + j][g * 4 + 1], acc[tm][2 * jj + j][g * 4 + 2],
+                acc[tm][2 * jj + j][g * 4 + 3]};
+}
+// Eight columns of row 8 i + lane / 8 of the piece.
+__device__ __forceinline__ void epi_get(const float *piece, int i, float (&v)[8]) {
+  const int lane = __lane_id();
+  const float *p = piece + (8 * i + (lane >> 3)) * kEpiPitch + (lane & 7) * 8;
+  const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = a[j];
+    v[4 + j] = b[j];
+  }
+}
+
+// bf16 rows [0, rows) of a tile in ro (row pitch N), each value rounded once.
+// AUX: cache policy of the stores; 2 is the non-temporal hint, for the weight
+// gradients, which nothing here reads again.
+template <int TM, int TN, int WM, int WN, int AUX>
+__device__ __forceinline__ void store_lines(const f32x16 (&acc)[TM][TN], __amdgpu_buffer_rsrc_t ro, int N,
+                                            int rows, int n0, int wm, int wn, float *piece) {
+  const int lane = __lane_id();
+#pragma unroll
+  for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+    for (int jj = 0; jj < TN / 2; ++jj) {
+      epi_put<TM, TN>(acc, tm, jj, piece);
+      const int col = n0 + wn * WN + jj * 64 + (lane & 7) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = wm * WM + tm * 32 + 8 * i + (lane >> 3);
+        float v[8];
+        epi_get(piece, i, v);
+        const u32x4 o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7])};
+        const uint32_t off =
+            (r < rows && col < N) ? ((uint32_t)r * (uint32_t)N + (uint32_t)col) * 2u : kOOB;
+        __builtin_amdgcn_raw_buffer_store_b128(o, ro, off, 0, AUX);
+      }
+    }
+}
+
+// DH: g and u come and dg, du, w h go as such lines.  dh0, h and the products
+// stay float32; dg, du and w h are rounded once to bf16, the type of the MFMA
+// that reads them next.  The row sums of dh0 h over 64 columns go to
+// part[column / 64][row].  s_w: combine weights of the tile's rows.
+template <int TM, int TN, int WM, int WN>
+__device__ __forceinline__ void store_dh(const f32x16 (&acc)[TM][TN], const GradParams &p, const float *s_w,
+                                         int row0, int rows, int n0, int wm, int wn, float *piece) {
+  const int lane = __lane_id();
   const int N = p.f;
   const size_t base = (size_t)row0 * N;
   const uint32_t bytes = (uint32_t)rows * (uint32_t)N * 2u;
@@ -86,72 +142,79 @@ __device__ __forceinline__ void store_dh(const f32x16 (&acc)[TM][TN], const Grad
   const __amdgpu_buffer_rsrc_t rdg = rsrc(p.dg + base, bytes), rdu = rsrc(p.du + base, bytes),
                                rhs = rsrc(p.hs + base, bytes);
 #pragma unroll
-  for (int tm = 0; tm < TM; ++tm) {
-    const int r = wm * WM + tm * 32 + lr;
-    uint32_t off[TN][2];
-    u32x4 gq[TN][2], uq[TN][2];
+  for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+    for (int jj = 0; jj < TN / 2; ++jj) {
+      const int c0 = n0 + wn * WN + jj * 64, col = c0 + (lane & 7) * 8;
+      uint32_t off[4];
+      u32x4 gq[4], uq[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int col = n0 + wn * WN + j * 32 + 16 * h + lg * 8;
-        off[j][h] = (r < rows && col < N) ? ((uint32_t)r * (uint32_t)N + (uint32_t)col) * 2u : kOOB;
-        gq[j][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rg, off[j][h], 0, 0));
-        uq[j][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ru, off[j][h], 0, 0));
+      for (int i = 0; i < 4; ++i) {
+        const int r = wm * WM + tm * 32 + 8 * i + (lane >> 3);
+        off[i] = (r < rows && col < N) ? ((uint32_t)r * (uint32_t)N + (uint32_t)col) * 2u : kOOB;
+        gq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rg, off[i], 0, 0));
+        uq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ru, off[i], 0, 0));
       }
-    float sum = 0.f;
+      epi_put<TM, TN>(acc, tm, jj, piece);
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float dh[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const auto sw = __builtin_amdgcn_permlane32_swap(
-              __float_as_uint(acc[tm][j][8 * h + i]), __float_as_uint(acc[tm][j][8 * h + 4 + i]), false,
-              false);
-          dh[i] = __uint_as_float(sw[0]);
-          dh[4 + i] = __uint_as_float(sw[1]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int r = wm * WM + tm * 32 + 8 * i + (lane >> 3);
+        const float wr = s_w[r];
+        float dh[8], sum = 0.f;
+        epi_get(piece, i, dh);
         u32x4 odg, odu, ohs;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float dgv[2], duv[2], hv[2];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const float g = __uint_as_float(b ? gq[j][h][q] & 0xffff0000u : gq[j][h][q] << 16);
-            const float u = __uint_as_float(b ? uq[j][h][q] & 0xffff0000u : uq[j][h][q] << 16);
+            const float g = __uint_as_float(b ? gq[i][q] & 0xffff0000u : gq[i][q] << 16);
+            const float u = __uint_as_float(b ? uq[i][q] & 0xffff0000u : uq[i][q] << 16);
             const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
             const float a = g * s;  // silu(g)
             const float d0 = dh[2 * q + b];
             sum = fmaf(d0, a * u, sum);
-            const float dw = d0 * wrow[tm];
+            const float dw = d0 * wr;
             duv[b] = dw * a;
             dgv[b] = dw * u * fmaf(a, 1.0f - s, s);  // silu'(g) = s + g s (1 - s)
-            hv[b] = wrow[tm] * (a * u);
+            hv[b] = wr * (a * u);
           }
           odg[q] = pack_bf16x2(dgv[0], dgv[1]);
           odu[q] = pack_bf16x2(duv[0], duv[1]);
           ohs[q] = pack_bf16x2(hv[0], hv[1]);
         }
-        __builtin_amdgcn_raw_buffer_store_b128(odg, rdg, off[j][h], 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(odu, rdu, off[j][h], 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(ohs, rhs, off[j][h], 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(odg, rdg, off[i], 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(odu, rdu, off[i], 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(ohs, rhs, off[i], 0, 0);
+        sum = group_sum(sum, 8);
+        if (p.part && (lane & 7) == 0 && r < rows && c0 < N)
+          p.part[(size_t)(c0 / 64) * p.R + row0 + r] = sum;
       }
-    sum += __shfl_xor(sum, 32, 64);
-    if (p.part && lg == 0 && r < rows) p.part[(size_t)(nt * (kNW / 2) + wn) * p.R + row0 + r] = sum;
-  }
+    }
 }
 
-template <Mode MODE, bool GATHER, int BM, int BN>
-__global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradParams p) {
+// A set of tiles: BM x BN of the products over pile rows and of the weight
+// gradients, waves per block, K step, and waves per SIMD asked of the
+// register allocator.
+template <int RBM_, int RBN_, int WBM_, int WBN_, int NW_, int BK_, int OCC_>
+struct Cfg {
+  static constexpr int RBM = RBM_, RBN = RBN_, WBM = WBM_, WBN = WBN_, NW = NW_, BK = BK_, OCC = OCC_;
+  static constexpr int NT = NW * 64;
+  static constexpr int max(int a, int b) { return a > b ? a : b; }
+  // stages, or the epilogue's pieces (and the rows' combine weights)
+  static constexpr int EPI = NW * kEpiWave + RBM * 4;
+  static constexpr int ROW_LDS = max(2 * (RBM + RBN) * BK * 2, EPI);
+  static constexpr int WEIGHT_LDS = max(2 * (WBM + WBN) * BK * 2, EPI);
+};
+
+// One block's tile; `block` counts from the product's first block.
+template <Mode MODE, bool GATHER, int BM, int BN, int NW, int BK>
+__device__ __forceinline__ void grad_tile(const GradParams &p, int block, uint8_t *smem, TileSlot &s_t) {
   constexpr bool WEIGHT = MODE == DW13 || MODE == DW2;  // A is K-major too
-  constexpr int WM = BM / 2, WN = BN / (kNW / 2), TM = WM / 32, TN = WN / 32;
-  constexpr int A_BYTES = BM * kBK * 2, B_BYTES = BN * kBK * 2, STAGE = A_BYTES + B_BYTES;
-  constexpr int A_RUNS = A_BYTES / 1024 / kNW, B_RUNS = B_BYTES / 1024 / kNW;
-  constexpr int SLICES = kBK / 16;
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ TileSlot s_t;
+  constexpr int WM = BM / 2, WN = BN / (NW / 2), TM = WM / 32, TN = WN / 32;
+  constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE = A_BYTES + B_BYTES;
+  constexpr int A_RUNS = A_BYTES / 1024 / NW, B_RUNS = B_BYTES / 1024 / NW;
+  constexpr int SLICES = BK / 16;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -172,15 +235,15 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradParams p) {
     m0 = s_t.row0;
     rows = s_t.rows;
     kcount = MODE == DH ? p.d : p.f;
-    nk = (kcount + kBK - 1) / kBK * (MODE == DX ? 2 : 1);
+    nk = (kcount + BK - 1) / BK * (MODE == DX ? 2 : 1);
   } else {
     // Every XCD (block b runs on XCD b mod 8) takes an eighth of each
     // expert's tiles, so that all have the same share of large and small
     // piles; within it, groups of eight row tiles column by column.
     const int T = p.n_mt * p.n_nt, per = (T + 7) / 8;
-    const int slot = blockIdx.x >> 3;
+    const int slot = block >> 3;
     e = slot / per;
-    const int tile = (blockIdx.x & 7) * per + slot % per;
+    const int tile = (block & 7) * per + slot % per;
     if (tile >= T) return;
     constexpr int RG = 8;
     const int grp = tile / (RG * p.n_nt), within = tile - grp * RG * p.n_nt;
@@ -196,7 +259,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradParams p) {
     rows = min(BM, M - m0);
     pile0 = p.offsets[e];
     kcount = p.offsets[e + 1] - pile0;
-    nk = (kcount + kBK - 1) / kBK;
+    nk = (kcount + BK - 1) / BK;
   }
   const int n0 = nt * BN;
 
@@ -226,75 +289,77 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradParams p) {
 
   // ---- per-lane copy offsets --------------------------------------------------
   // K-major tile of W columns: run q fills 1024 / (2 W) rows; lane i of run
-  // kNW j + wave has row kr + j KROWS, stored chunk i % (W / 8).
-  constexpr int A_CPR = BM / 8, B_CPR = BN / 8;             // chunks per K-major row
+  // NW j + wave has row kr + j KROWS, stored chunk i % (W / 8).
+  constexpr int A_CPR = WEIGHT ? BM / 8 : 8, B_CPR = BN / 8;  // chunks per K-major row
   constexpr int A_RPR = 64 / A_CPR, B_RPR = 64 / B_CPR;     // rows per run
   const int b_kr = wave * B_RPR + lane / B_CPR;
   const int b_col = n0 + (((lane % B_CPR) ^ kmaj_key<BN>(b_kr)) << 3);
   const uint32_t b_pen = b_col < N ? 0u : kOOB;
   const int a_kr = wave * A_RPR + lane / A_CPR;
-  const int a_col = WEIGHT ? m0 + (((lane % A_CPR) ^ kmaj_key<BM>(a_kr)) << 3) : 0;
+  int a_col = 0;
+  if constexpr (WEIGHT) a_col = m0 + (((lane % A_CPR) ^ kmaj_key<BM>(a_kr)) << 3);
   const uint32_t a_pen = WEIGHT && a_col >= lda ? kOOB : 0u;
-  static_assert((kNW * A_RPR) % 4 == 0 && (kNW * B_RPR) % 4 == 0, "a lane's key is the same in every run");
-  // Row-major A tile (rows of 64 K, 128 B): as in the forward GEMM.
-  const int c = dma_chunk<kBK * 2>(wave, lane);
-  const int a_r = wave * 8 + lane / 8;
+  static_assert((NW * A_RPR) % 4 == 0 && (NW * B_RPR) % 4 == 0, "a lane's key is the same in every run");
+  // Row-major A tile: as in the forward GEMM.
+  const int c = dma_chunk<BK * 2>(wave, lane);
+  constexpr int RPR = 1024 / (BK * 2), RUN_ROWS = NW * RPR;  // rows of a run, and of all waves' runs
+  const int a_r = wave * RPR + lane / (BK / 8);
   uint32_t a_off[!WEIGHT ? A_RUNS : 1];
   if constexpr (!WEIGHT) {
     int src[A_RUNS];
 #pragma unroll
     for (int j = 0; j < A_RUNS; ++j) {
-      const int r = a_r + j * 64;
+      const int r = a_r + j * RUN_ROWS;
       src[j] = A_GATHER ? p.perm[m0 + min(r, rows - 1)] : r;
     }
 #pragma unroll
     for (int j = 0; j < A_RUNS; ++j)
-      a_off[j] = a_r + j * 64 < rows ? ((uint32_t)src[j] * (uint32_t)lda + (uint32_t)c * 8u) * 2u : kOOB;
+      a_off[j] = a_r + j * RUN_ROWS < rows ? ((uint32_t)src[j] * (uint32_t)lda + (uint32_t)c * 8u) * 2u : kOOB;
   }
   // Gathered K-major operand: the token of each of this lane's K rows of the
   // next step, loaded one step ahead of the copies that use it.
   constexpr int K_RUNS = A_GATHER ? A_RUNS : B_RUNS;
   const int g_kr = A_GATHER ? a_kr : b_kr;
-  constexpr int G_ROWS = kNW * (A_GATHER ? A_RPR : B_RPR);
+  constexpr int G_ROWS = NW * (A_GATHER ? A_RPR : B_RPR);
   int tok[WEIGHT && GATHER ? K_RUNS : 1];
   auto load_tokens = [&](int kt) {
     if constexpr (WEIGHT && GATHER)
 #pragma unroll
       for (int j = 0; j < K_RUNS; ++j)
-        tok[j] = p.perm[pile0 + min(kt * kBK + g_kr + j * G_ROWS, kcount - 1)];
+        tok[j] = p.perm[pile0 + min(kt * BK + g_kr + j * G_ROWS, kcount - 1)];
   };
 
   // Copies of K step kt into LDS stage `stage`; a step past the end copies zeros.
   const int nk_range = MODE == DX ? nk / 2 : nk;
   auto issue = [&](int kt, int stage) {
     const bool sec = MODE == DX && kt >= nk_range;
-    const int k0 = (sec ? kt - nk_range : kt) * kBK;
+    const int k0 = (sec ? kt - nk_range : kt) * BK;
     uint8_t *sa = smem + stage * STAGE, *sb = sa + A_BYTES;
     if constexpr (!WEIGHT) {
       const uint32_t pen = k0 + c * 8 < kcount ? 0u : kOOB;
 #pragma unroll
       for (int j = 0; j < A_RUNS; ++j)
-        dma16(sec ? ra1 : ra0, sa + (kNW * j + wave) * 1024, (a_off[j] + (uint32_t)k0 * 2u) | pen);
+        dma16(sec ? ra1 : ra0, sa + (NW * j + wave) * 1024, (a_off[j] + (uint32_t)k0 * 2u) | pen);
     } else {
 #pragma unroll
       for (int j = 0; j < A_RUNS; ++j) {
-        const int kr = k0 + a_kr + j * kNW * A_RPR;
+        const int kr = k0 + a_kr + j * NW * A_RPR;
         const uint32_t row = A_GATHER ? (uint32_t)tok[j] : (uint32_t)kr;
         const uint32_t pen = kr < kcount ? a_pen : kOOB;
-        dma16(ra0, sa + (kNW * j + wave) * 1024, ((row * (uint32_t)lda + (uint32_t)a_col) * 2u) | pen);
+        dma16(ra0, sa + (NW * j + wave) * 1024, ((row * (uint32_t)lda + (uint32_t)a_col) * 2u) | pen);
       }
     }
 #pragma unroll
     for (int j = 0; j < B_RUNS; ++j) {
-      const int kr = k0 + b_kr + j * kNW * B_RPR;
+      const int kr = k0 + b_kr + j * NW * B_RPR;
       const uint32_t row = B_GATHER ? (uint32_t)tok[j] : (uint32_t)kr;
       const uint32_t pen = kr < kcount ? b_pen : kOOB;
-      dma16(sec ? rb1 : rb0, sb + (kNW * j + wave) * 1024, ((row * (uint32_t)ldb + (uint32_t)b_col) * 2u) | pen);
+      dma16(sec ? rb1 : rb0, sb + (NW * j + wave) * 1024, ((row * (uint32_t)ldb + (uint32_t)b_col) * 2u) | pen);
     }
     load_tokens(kt + 1);
   };
 
-  const int wm = wave / (kNW / 2), wn = wave % (kNW / 2);
+  const int wm = wave / (NW / 2), wn = wave % (NW / 2);
   const int lr = lane & 31, lg = lane >> 5;
   f32x16 acc[TM][TN];
 #pragma unroll
@@ -303,17 +368,6 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradParams p) {
     for (int b = 0; b < TN; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
-
-  // Combine weights of this lane's rows (DH), looked up before the K loop.
-  float wrow[TM];
-  if constexpr (MODE == DH) {
-#pragma unroll
-    for (int tm = 0; tm < TM; ++tm) {
-      wrow[tm] = 1.f;
-      const int r = wm * WM + tm * 32 + lr;
-      if (GATHER && r < rows) wrow[tm] = pair_weight(p.inv, p.topk_w, p.k, p.perm[m0 + r], m0 + r);
-    }
-  }
 
   int a_lane[WEIGHT ? TM : 1], b_lane[TN];
 #pragma unroll
@@ -330,7 +384,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradParams p) {
       if constexpr (WEIGHT)
         af[tm] = kmaj_frag<BM>(sa, a_lane[tm], kk);
       else
-        af[tm] = *(const bf16x8 *)(sa + swz<kBK * 2>(wm * WM + tm * 32 + lr, kk * 2 + lg));
+        af[tm] = *(const bf16x8 *)(sa + swz<BK * 2>(wm * WM + tm * 32 + lr, kk * 2 + lg));
     }
     if constexpr (ACT > 0) {
 #pragma unroll
@@ -397,7 +451,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradParams p) {
     load_tokens(0);
     issue(0, 0);
     const int act = __builtin_amdgcn_readfirstlane(min(TM, max(0, (rows - wm * WM + 31) / 32)));
-    static_assert(TM == 2 || TM == 4, "row groups per wave");
+    static_assert(TM >= 2 && TM <= 5, "row groups per wave");
     if (act == TM) {
       kloop(std::integral_constant<int, TM>{});
     } else if (act == 0) {
@@ -409,61 +463,116 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradParams p) {
         kloop(std::integral_constant<int, 2>{});
       else
         kloop(std::integral_constant<int, 3>{});
+    } else if constexpr (TM == 5) {
+      if (act == 2)
+        kloop(std::integral_constant<int, 2>{});
+      else if (act == 3)
+        kloop(std::integral_constant<int, 3>{});
+      else
+        kloop(std::integral_constant<int, 4>{});
     }
     wait_vmcnt<0>();
   }
 
   // ---- epilogue ---------------------------------------------------------------
+  __syncthreads();  // every wave is done with the stages
+  float *piece = (float *)(smem + wave * kEpiWave);
   if constexpr (MODE == DH) {
-    store_dh<TM, TN, WM, WN>(acc, p, wrow, m0, rows, n0, nt, wm, wn);
+    float *s_w = (float *)(smem + NW * kEpiWave);
+    for (int r = tid; r < BM; r += NW * 64)
+      s_w[r] = GATHER && r < rows ? pair_weight(p.inv, p.topk_w, p.k, p.perm[m0 + r], m0 + r) : 1.f;
+    __syncthreads();
+    store_dh<TM, TN, WM, WN>(acc, p, s_w, m0, rows, n0, wm, wn, piece);
   } else {
     // da: the tile's pile rows; weight gradients: rows m0 .. of expert e
     uint16_t *out = (uint16_t *)(MODE == DW13 && second ? p.c1 : p.c0) +
                     (WEIGHT ? (size_t)e * p.d * p.f : (size_t)0) + (size_t)m0 * N;
-    store_bf16_regs<TM, TN, WM, WN>(acc, rsrc(out, (uint32_t)rows * (uint32_t)N * 2u), N, rows, n0, wm, wn);
+    store_lines<TM, TN, WM, WN, WEIGHT ? 2 : 0>(acc, rsrc(out, (uint32_t)rows * (uint32_t)N * 2u), N, rows, n0,
+                                                wm, wn, piece);
   }
 }
 
-template <Mode MODE, bool GATHER, int BM, int BN>
-hipError_t launch(const GradParams &p, int blocks, hipStream_t st) {
-  constexpr int lds = 2 * (BM + BN) * kBK * 2;
-  auto kern = grad_gemm_kernel<MODE, GATHER, BM, BN>;
-  static std::atomic<uint64_t> allowed{0};  // devices on which LDS above 64 KB is allowed
+// dg, du, w h: everything else waits for them.
+template <bool GATHER, typename C>
+__global__ __launch_bounds__(C::NT, C::OCC) void grad_dh_kernel(GradParams p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ TileSlot s_t;
+  grad_tile<DH, GATHER, C::RBM, C::RBN, C::NW, C::BK>(p, blockIdx.x, smem, s_t);
+}
+
+// The products that follow, in one grid: da's blocks (the longest) first,
+// then dW1 and dW3, then dW2, so that a product's last, half-empty round of
+// blocks is filled by the next product's.
+struct RestParams {
+  GradParams dx, dw13, dw2;
+  int end_dx, end_dw13, end_dw2;  // block ranges, multiples of 8
+};
+
+template <bool GATHER, typename C>
+__global__ __launch_bounds__(C::NT, C::OCC) void grad_rest_kernel(RestParams q) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ TileSlot s_t;
+  const int b = blockIdx.x;
+  if (b < q.end_dx)
+    grad_tile<DX, false, C::RBM, C::RBN, C::NW, C::BK>(q.dx, b, smem, s_t);
+  else if (b < q.end_dw13)
+    grad_tile<DW13, GATHER, C::WBM, C::WBN, C::NW, C::BK>(q.dw13, b - q.end_dx, smem, s_t);
+  else
+    grad_tile<DW2, GATHER, C::WBM, C::WBN, C::NW, C::BK>(q.dw2, b - q.end_dw13, smem, s_t);
+}
+
+// Dynamic LDS above 64 KB must be allowed once per device and kernel.
+template <typename Kern>
+hipError_t allow_lds(Kern kern, int lds, std::atomic<uint64_t> &done) {
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
   if (err != hipSuccess) return err;
   const uint64_t bit = 1ull << (dev & 63);
-  if (!(allowed.load(std::memory_order_acquire) & bit)) {
+  if (!(done.load(std::memory_order_acquire) & bit)) {
     err = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (err != hipSuccess) return err;
-    allowed.fetch_or(bit, std::memory_order_release);
+    done.fetch_or(bit, std::memory_order_release);
   }
-  kern<<<blocks, kNT, lds, st>>>(p);
-  return hipGetLastError();
+  return hipSuccess;
 }
 
-template <Mode MODE, int BM, int BN>
-hipError_t run(GradParams p, hipStream_t st) {
-  const int N = MODE == DH || MODE == DW2 ? p.f : p.d;
-  p.n_nt = (N + BN - 1) / BN;
-  int blocks;
-  if constexpr (MODE == DW13 || MODE == DW2) {
-    const int M = MODE == DW13 ? p.f : p.d;
-    p.n_mt = (M + BM - 1) / BM * (MODE == DW13 ? 2 : 1);
-    blocks = p.E * 8 * ((p.n_mt * p.n_nt + 7) / 8);
-  } else {
-    blocks = ((p.R + BM - 1) / BM + (p.E < p.R ? p.E : p.R)) * p.n_nt;
-  }
-  if constexpr (MODE != DX)
-    if (p.perm) return launch<MODE, true, BM, BN>(p, blocks, st);
-  return launch<MODE, false, BM, BN>(p, blocks, st);
+// Blocks of a product over pile rows (at most one ragged tile per pile) and
+// of a weight gradient (E experts, each an eighth of its tiles per XCD).
+int row_blocks(const GradParams &p, int bm) {
+  return ((p.R + bm - 1) / bm + (p.E < p.R ? p.E : p.R)) * p.n_nt;
+}
+int weight_blocks(const GradParams &p) { return p.E * 8 * ((p.n_mt * p.n_nt + 7) / 8); }
+
+template <bool GATHER, typename C>
+hipError_t launch_both(GradParams dh, RestParams q, hipStream_t st) {
+  auto k1 = grad_dh_kernel<GATHER, C>;
+  auto k2 = grad_rest_kernel<GATHER, C>;
+  constexpr int rest_lds = C::ROW_LDS > C::WEIGHT_LDS ? C::ROW_LDS : C::WEIGHT_LDS;
+  static std::atomic<uint64_t> allowed1{0}, allowed2{0};
+  hipError_t err = allow_lds(k1, C::ROW_LDS, allowed1);
+  if (err == hipSuccess) err = allow_lds(k2, rest_lds, allowed2);
+  if (err != hipSuccess) return err;
+  const int f = dh.f, d = dh.d;
+  auto tiles = [](int v, int b) { return (v + b - 1) / b; };
+  dh.n_nt = tiles(f, C::RBN);
+  q.dx.n_nt = tiles(d, C::RBN);
+  q.dw13.n_mt = 2 * tiles(f, C::WBM);
+  q.dw13.n_nt = tiles(d, C::WBN);
+  q.dw2.n_mt = tiles(d, C::WBM);
+  q.dw2.n_nt = tiles(f, C::WBN);
+  k1<<<row_blocks(dh, C::RBM), C::NT, C::ROW_LDS, st>>>(dh);
+  q.end_dx = (row_blocks(q.dx, C::RBM) + 7) / 8 * 8;
+  q.end_dw13 = q.end_dx + weight_blocks(q.dw13);
+  q.end_dw2 = q.end_dw13 + weight_blocks(q.dw2);
+  k2<<<q.end_dw2, C::NT, rest_lds, st>>>(q);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-int grad_planes_bf16(int d_ff) { return (d_ff + 255) / 256 * (kNW / 2); }
+int grad_planes_bf16(int d_ff) { return (d_ff + 63) / 64; }
 
-hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t st) {
+hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, int *planes, hipStream_t st) {
   GradParams b{};
   b.offsets = a.offsets;
   b.slot = a.slot;
@@ -487,34 +596,26 @@ hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, hipStream_
   p.du = (uint16_t *)w.du;
   p.hs = (uint16_t *)w.hs;
   p.part = a.perm ? w.part : nullptr;
-  hipError_t e = run<DH, 256, 256>(p, st);
-  if (e != hipSuccess) return e;
 
-  p = b;
-  p.a0 = (const uint16_t *)w.dg;
-  p.a1 = (const uint16_t *)w.du;
-  p.b0 = (const uint16_t *)a.w1;
-  p.b1 = (const uint16_t *)a.w3;
-  p.c0 = a.da;
-  e = run<DX, 256, 256>(p, st);
-  if (e != hipSuccess) return e;
-
-  p = b;
-  p.a0 = (const uint16_t *)w.dg;
-  p.a1 = (const uint16_t *)w.du;
-  p.b0 = (const uint16_t *)a.a;
-  p.perm = a.perm;
-  p.c0 = a.dw1;
-  p.c1 = a.dw3;
-  e = run<DW13, 256, 256>(p, st);
-  if (e != hipSuccess) return e;
-
-  p = b;
-  p.a0 = (const uint16_t *)a.dy;
-  p.b0 = (const uint16_t *)w.hs;
-  p.perm = a.perm;
-  p.c0 = a.dw2;
-  return run<DW2, 256, 256>(p, st);
+  RestParams q{b, b, b, 0, 0, 0};
+  q.dx.a0 = q.dw13.a0 = (const uint16_t *)w.dg;
+  q.dx.a1 = q.dw13.a1 = (const uint16_t *)w.du;
+  q.dx.b0 = (const uint16_t *)a.w1;
+  q.dx.b1 = (const uint16_t *)a.w3;
+  q.dx.c0 = a.da;
+  q.dw13.b0 = (const uint16_t *)a.a;
+  q.dw13.perm = q.dw2.perm = a.perm;
+  q.dw13.c0 = a.dw1;
+  q.dw13.c1 = a.dw3;
+  q.dw2.a0 = (const uint16_t *)a.dy;
+  q.dw2.b0 = (const uint16_t *)w.hs;
+  q.dw2.c0 = a.dw2;
+#ifndef CFG
+#define CFG 320, 256, 256, 256, 8, 64, 1
+#endif
+  using Big = Cfg<CFG>;
+  *planes = grad_planes_bf16(a.d_ff);
+  return a.perm ? launch_both<true, Big>(p, q, st) : launch_both<false, Big>(p, q, st);
 }
 
 }  // namespace moe
