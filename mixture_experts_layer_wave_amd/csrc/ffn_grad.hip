@@ -13,47 +13,72 @@
 namespace moe {
 namespace {
 
-// dtopk_w from the partial row sums part[P][R].  A block takes 64 pile rows,
-// 16 waves the planes w, w + 16, ... of each; the 16 sums are added in wave
-// order, so the result does not depend on scheduling.  The sum of row r goes
-// to the pair whose row it is; pairs without a row (inv outside [0, R)) get 0.
-__global__ __launch_bounds__(1024) void weight_grad_kernel(const float *__restrict__ part, int P, int R,
-                                                           int E, const int32_t *__restrict__ offsets,
-                                                           const int32_t *__restrict__ perm,
-                                                           const int32_t *__restrict__ inv, int k,
-                                                           float *__restrict__ dw) {
+struct FinishParams {
+  const float *part;
+  int P, R, E, k, d;
+  const int32_t *offsets, *perm, *inv;
+  float *dw;
+  const float *dx_part;
+  int S;
+  uint16_t *da;
+  int w_blocks;  // blocks of the weights' gradient (0 without a combine)
+};
+
+// The last kernel of the pass.  Blocks 0 .. w_blocks - 1: dtopk_w from the
+// partial row sums part[P][R], 64 pile rows a block, 16 waves the planes w,
+// w + 16, ... of each; the 16 sums are added in wave order, so the result
+// does not depend on scheduling.  The sum of row r goes to the pair whose row
+// it is; pairs without a row (inv outside [0, R)) get 0.  The other blocks:
+// the piled rows of da, eight columns a thread, as the sum of their S planes
+// in order (d % 8 == 0).
+__global__ __launch_bounds__(1024) void ffn_grad_finish_kernel(FinishParams p) {
   __shared__ float s_p[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = blockIdx.x * 64 + lane;
-  const bool piled = r < R && r < offsets[E];
-  float v = 0.f;
-  if (piled)
-    for (int q = wave; q < P; q += 16) v += part[(size_t)q * R + r];
-  s_p[wave][lane] = v;
-  __syncthreads();
-  if (wave == 0 && piled) {
-    v = 0.f;
-    for (int i = 0; i < 16; ++i) v += s_p[i][lane];
-    const int t = perm[r];
-    for (int j = 0; j < k; ++j)
-      if (inv[(size_t)t * k + j] == r) dw[(size_t)t * k + j] = v;
+  if ((int)blockIdx.x < p.w_blocks) {
+    const int r = blockIdx.x * 64 + lane;
+    const bool piled = r < p.R && r < p.offsets[p.E];
+    float v = 0.f;
+    if (piled)
+      for (int q = wave; q < p.P; q += 16) v += p.part[(size_t)q * p.R + r];
+    s_p[wave][lane] = v;
+    __syncthreads();
+    if (wave == 0 && piled) {
+      v = 0.f;
+      for (int i = 0; i < 16; ++i) v += s_p[i][lane];
+      const int t = p.perm[r];
+      for (int j = 0; j < p.k; ++j)
+        if (p.inv[(size_t)t * p.k + j] == r) p.dw[(size_t)t * p.k + j] = v;
+    }
+    if (wave == 1 && r < p.R && (unsigned)p.inv[r] >= (unsigned)p.R) p.dw[r] = 0.f;  // pair r
+    return;
   }
-  if (wave == 1 && r < R && (unsigned)inv[r] >= (unsigned)R) dw[r] = 0.f;  // pair r
+  const size_t at = ((size_t)(blockIdx.x - p.w_blocks) * 1024 + threadIdx.x) * 8;
+  if (at >= (size_t)p.offsets[p.E] * p.d) return;
+  const size_t plane = (size_t)p.R * p.d;
+  f32x4 a = *(const f32x4 *)(p.dx_part + at), b = *(const f32x4 *)(p.dx_part + at + 4);
+  for (int s = 1; s < p.S; ++s) {
+    a += *(const f32x4 *)(p.dx_part + s * plane + at);
+    b += *(const f32x4 *)(p.dx_part + s * plane + at + 4);
+  }
+  *(u32x4 *)(p.da + at) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]),
+                                pack_bf16x2(b[2], b[3])};
 }
 
 struct Layout {
-  size_t du, hs, part, total;
+  GradPlan plan;
+  size_t du, hs, part, dx_part, total;
 };
 
 Layout layout(const FfnGradArgs &a) {
   Layout L{};
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   const size_t mat = up((size_t)a.R * a.d_ff * (a.bf16 ? 2 : 4));
-  const int planes = a.bf16 ? grad_planes_bf16(a.d_ff) : grad_planes_f32(a.d_ff);
+  L.plan = a.bf16 ? grad_plan_bf16(a) : grad_plan_f32(a);
   L.du = mat;
   L.hs = 2 * mat;
   L.part = 3 * mat;
-  L.total = L.part + up((size_t)planes * a.R * 4);
+  L.dx_part = L.part + up((size_t)L.plan.dw_planes * a.R * 4);
+  L.total = L.dx_part + (L.plan.dx_splits > 1 ? up((size_t)L.plan.dx_splits * a.R * a.d * 4) : 0);
   return L;
 }
 
@@ -64,12 +89,27 @@ size_t ffn_grad_bytes(const FfnGradArgs &a) { return layout(a).total; }
 hipError_t launch_ffn_grad(const FfnGradArgs &a, hipStream_t st) {
   const Layout L = layout(a);
   char *base = (char *)a.ws;
-  const FfnGradWs w{base, base + L.du, base + L.hs, (float *)(base + L.part)};
-  int planes = 0;
-  const hipError_t e = a.bf16 ? launch_grad_bf16(a, w, &planes, st) : launch_grad_f32(a, w, &planes, st);
-  if (e != hipSuccess || !a.perm) return e;
-  weight_grad_kernel<<<(a.R + 63) / 64, 1024, 0, st>>>(w.part, planes, a.R, a.E, a.offsets, a.perm,
-                                                       a.inv, a.k, a.dtopk_w);
+  const FfnGradWs w{L.plan, base, base + L.du, base + L.hs, (float *)(base + L.part), (float *)(base + L.dx_part)};
+  const hipError_t e = a.bf16 ? launch_grad_bf16(a, w, st) : launch_grad_f32(a, w, st);
+  if (e != hipSuccess) return e;
+  FinishParams p{};
+  p.part = w.part;
+  p.P = L.plan.dw_planes;
+  p.R = a.R;
+  p.E = a.E;
+  p.k = a.k;
+  p.d = a.d;
+  p.offsets = a.offsets;
+  p.perm = a.perm;
+  p.inv = a.inv;
+  p.dw = a.dtopk_w;
+  p.dx_part = w.dx_part;
+  p.S = L.plan.dx_splits;
+  p.da = (uint16_t *)a.da;
+  p.w_blocks = a.perm ? (a.R + 63) / 64 : 0;
+  const size_t sums = p.S > 1 ? ((size_t)a.R * a.d / 8 + 1023) / 1024 : 0;
+  if (p.w_blocks + sums == 0) return hipSuccess;
+  ffn_grad_finish_kernel<<<(unsigned)(p.w_blocks + sums), 1024, 0, st>>>(p);
   return hipGetLastError();
 }
 

@@ -172,7 +172,7 @@ int row_tiles(int R, int E) { return (R + kT - 1) / kT + (E < R ? E : R); }
 
 }  // namespace
 
-int grad_planes_f32(int d_ff) { return (d_ff + kT - 1) / kT * 2; }
+GradPlan grad_plan_f32(const FfnGradArgs &a) { return {(a.d_ff + kT - 1) / kT * 2, 1}; }
 
 hipError_t launch_up_save_f32(const FfnArgs &a, void *g, void *u, hipStream_t st) {
   F32Params p{};
@@ -195,8 +195,7 @@ hipError_t launch_up_save_f32(const FfnArgs &a, void *g, void *u, hipStream_t st
   return hipGetLastError();
 }
 
-hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, int *planes, hipStream_t st) {
-  *planes = grad_planes_f32(a.d_ff);
+hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t st) {
   F32Params p{};
   p.a = (const float *)a.a;
   p.dy = (const float *)a.dy;

@@ -34,19 +34,25 @@ struct FfnGradArgs {
 size_t ffn_grad_bytes(const FfnGradArgs &a);
 hipError_t launch_ffn_grad(const FfnGradArgs &a, hipStream_t st);
 
-// Workspace regions of a gradient pass: dg, du and w h, [R][d_ff] each in
-// the activations' type, and the partial row sums of <dh0, h>,
-// [planes][R] float32, one plane for each column range of the dh product.
-struct FfnGradWs {
-  void *dg, *du, *hs;
-  float *part;
+// What a gradient pass leaves for its last kernel, by shape alone: planes of
+// <dh0, h> row sums, one for each column range of the dh product, and planes
+// of da when its product is split along K (1: da is written directly).
+struct GradPlan {
+  int dw_planes, dx_splits;
 };
 
-// The products, in this order on the stream; *planes: the planes of part
-// that they write (at most grad_planes_*).
-hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, int *planes, hipStream_t st);
-int grad_planes_bf16(int d_ff);
-hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, int *planes, hipStream_t st);
-int grad_planes_f32(int d_ff);
+// Workspace regions: dg, du and w h, [R][d_ff] each in the activations' type;
+// part [dw_planes][R] and dx_part [dx_splits][R][d], float32.
+struct FfnGradWs {
+  GradPlan plan;
+  void *dg, *du, *hs;
+  float *part, *dx_part;
+};
+
+// The products, in order on the stream.
+GradPlan grad_plan_bf16(const FfnGradArgs &a);
+hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t st);
+GradPlan grad_plan_f32(const FfnGradArgs &a);
+hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t st);
 
 }  // namespace moe

@@ -46,6 +46,10 @@ struct GradParams {
   int E, R, d, f;
   int n_mt, n_nt;           // tiles along the output's rows (weight gradients) and columns
   void *c0, *c1;            // DX da; DW13 dW1, dW3; DW2 dW2
+  // DX with few blocks: K in `splits` ranges, range s of every tile to the
+  // float32 plane dx_part[s][R][d]; the planes are added later, in order.
+  int splits;
+  float *dx_part;
   // DH epilogue
   const uint16_t *g, *u;
   uint16_t *dg, *du, *hs;
@@ -127,6 +131,33 @@ __device__ __forceinline__ void store_lines(const f32x16 (&acc)[TM][TN], __amdgp
     }
 }
 
+// float32 rows [0, rows) of a tile in ro (row pitch N floats).
+template <int TM, int TN, int WM, int WN>
+__device__ __forceinline__ void store_lines_f32(const f32x16 (&acc)[TM][TN], __amdgpu_buffer_rsrc_t ro, int N,
+                                                int rows, int n0, int wm, int wn, float *piece) {
+  const int lane = __lane_id();
+#pragma unroll
+  for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+    for (int jj = 0; jj < TN / 2; ++jj) {
+      epi_put<TM, TN>(acc, tm, jj, piece);
+      const int col = n0 + wn * WN + jj * 64 + (lane & 7) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = wm * WM + tm * 32 + 8 * i + (lane >> 3);
+        float v[8];
+        epi_get(piece, i, v);
+        const uint32_t off =
+            (r < rows && col < N) ? ((uint32_t)r * (uint32_t)N + (uint32_t)col) * 4u : kOOB;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          __builtin_amdgcn_raw_buffer_store_b128(
+              __builtin_bit_cast(u32x4, f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]}), ro,
+              off + 16u * h, 0, 0);
+      }
+    }
+}
+
 // DH: g and u come and dg, du, w h go as such lines.  dh0, h and the products
 // stay float32; dg, du and w h are rounded once to bf16, the type of the MFMA
 // that reads them next.  The row sums of dh0 h over 64 columns go to
@@ -194,11 +225,12 @@ __device__ __forceinline__ void store_dh(const f32x16 (&acc)[TM][TN], const Grad
 }
 
 // A set of tiles: BM x BN of the products over pile rows and of the weight
-// gradients, waves per block, K step, and waves per SIMD asked of the
-// register allocator.
-template <int RBM_, int RBN_, int WBM_, int WBN_, int NW_, int BK_, int OCC_>
+// gradients, waves per block, K step, waves per SIMD asked of the register
+// allocator, and the blocks per CU that da's split K aims at.
+template <int RBM_, int RBN_, int WBM_, int WBN_, int NW_, int BK_, int OCC_, int HOLD_>
 struct Cfg {
   static constexpr int RBM = RBM_, RBN = RBN_, WBM = WBM_, WBN = WBN_, NW = NW_, BK = BK_, OCC = OCC_;
+  static constexpr int HOLD = HOLD_;
   static constexpr int NT = NW * 64;
   static constexpr int max(int a, int b) { return a > b ? a : b; }
   // stages, or the epilogue's pieces (and the rows' combine weights)
@@ -224,10 +256,13 @@ __device__ __forceinline__ void grad_tile(const GradParams &p, int block, uint8_
   int e, nt, m0, rows;  // output rows m0 .. m0 + rows (pile rows, or weight rows of the expert)
   int nk;               // K steps
   int kcount;           // K of one range
+  int kt0 = 0;          // first step of this block's K range (DX)
+  int split = 0;
   bool second = false;  // DW13: the tile is dW3's
   int pile0 = 0;        // weight gradients: the pile's first row
   if constexpr (!WEIGHT) {
-    if (wave == 0) map_block<BM, false, true>(p.offsets, p.E, p.n_nt, 1, lane, &s_t, 1, 4);
+    const int S = MODE == DX ? p.splits : 1;
+    if (wave == 0) map_block<BM, false, true>(p.offsets, p.E, p.n_nt, S, lane, &s_t, S, 4);
     __syncthreads();
     e = s_t.e;
     if (e < 0) return;
@@ -236,6 +271,11 @@ __device__ __forceinline__ void grad_tile(const GradParams &p, int block, uint8_
     rows = s_t.rows;
     kcount = MODE == DH ? p.d : p.f;
     nk = (kcount + BK - 1) / BK * (MODE == DX ? 2 : 1);
+    if (MODE == DX && S > 1) {
+      split = s_t.split;
+      kt0 = (int)((long long)split * nk / S);
+      nk = (int)((long long)(split + 1) * nk / S) - kt0;
+    }
   } else {
     // Every XCD (block b runs on XCD b mod 8) takes an eighth of each
     // expert's tiles, so that all have the same share of large and small
@@ -329,11 +369,12 @@ __device__ __forceinline__ void grad_tile(const GradParams &p, int block, uint8_
         tok[j] = p.perm[pile0 + min(kt * BK + g_kr + j * G_ROWS, kcount - 1)];
   };
 
-  // Copies of K step kt into LDS stage `stage`; a step past the end copies zeros.
-  const int nk_range = MODE == DX ? nk / 2 : nk;
+  // Copies of K step kt into LDS stage `stage` (a step past the end is copied
+  // and not used, or copies zeros).
+  const int nk_range = (kcount + BK - 1) / BK;
   auto issue = [&](int kt, int stage) {
-    const bool sec = MODE == DX && kt >= nk_range;
-    const int k0 = (sec ? kt - nk_range : kt) * BK;
+    const bool sec = MODE == DX && kt0 + kt >= nk_range;
+    const int k0 = (kt0 + kt - (sec ? nk_range : 0)) * BK;
     uint8_t *sa = smem + stage * STAGE, *sb = sa + A_BYTES;
     if constexpr (!WEIGHT) {
       const uint32_t pen = k0 + c * 8 < kcount ? 0u : kOOB;
@@ -483,6 +524,10 @@ __device__ __forceinline__ void grad_tile(const GradParams &p, int block, uint8_
       s_w[r] = GATHER && r < rows ? pair_weight(p.inv, p.topk_w, p.k, p.perm[m0 + r], m0 + r) : 1.f;
     __syncthreads();
     store_dh<TM, TN, WM, WN>(acc, p, s_w, m0, rows, n0, wm, wn, piece);
+  } else if (MODE == DX && p.splits > 1) {
+    float *out = p.dx_part + ((size_t)split * p.R + m0) * N;
+    store_lines_f32<TM, TN, WM, WN>(acc, rsrc(out, (uint32_t)rows * (uint32_t)N * 4u), N, rows, n0, wm, wn,
+                                    piece);
   } else {
     // da: the tile's pile rows; weight gradients: rows m0 .. of expert e
     uint16_t *out = (uint16_t *)(MODE == DW13 && second ? p.c1 : p.c0) +
@@ -536,12 +581,24 @@ hipError_t allow_lds(Kern kern, int lds, std::atomic<uint64_t> &done) {
   return hipSuccess;
 }
 
-// Blocks of a product over pile rows (at most one ragged tile per pile) and
-// of a weight gradient (E experts, each an eighth of its tiles per XCD).
-int row_blocks(const GradParams &p, int bm) {
-  return ((p.R + bm - 1) / bm + (p.E < p.R ? p.E : p.R)) * p.n_nt;
+int tiles(int v, int b) { return (v + b - 1) / b; }
+
+// Row tiles of the piles at most (one ragged tile per pile), and blocks of a
+// weight gradient (E experts, each an eighth of its tiles per XCD).
+int row_tiles(int R, int E, int bm) { return tiles(R, bm) + (E < R ? E : R); }
+int weight_blocks(const GradParams &p) { return p.E * 8 * tiles(p.n_mt * p.n_nt, 8); }
+
+// K ranges of da's product: its K is 2 d_ff, so with few row tiles its blocks
+// would outlast everything that runs beside them.  With fewer blocks than
+// HOLD per CU, K is split until there are as many, each range 512 deep at
+// least (Switch-shaped, 8 tokens: 165 -> 71 us; 4096 tokens: 347 -> 311).
+template <typename C>
+int dx_splits(int R, int E, int d, int f) {
+  const int blocks = row_tiles(R, E, C::RBM) * tiles(d, C::RBN), hold = 256 * C::HOLD;
+  int S = blocks < hold ? hold / blocks : 1;
+  if (S > 2 * f / 512) S = 2 * f / 512;
+  return S < 1 ? 1 : S;
 }
-int weight_blocks(const GradParams &p) { return p.E * 8 * ((p.n_mt * p.n_nt + 7) / 8); }
 
 template <bool GATHER, typename C>
 hipError_t launch_both(GradParams dh, RestParams q, hipStream_t st) {
@@ -553,15 +610,15 @@ hipError_t launch_both(GradParams dh, RestParams q, hipStream_t st) {
   if (err == hipSuccess) err = allow_lds(k2, rest_lds, allowed2);
   if (err != hipSuccess) return err;
   const int f = dh.f, d = dh.d;
-  auto tiles = [](int v, int b) { return (v + b - 1) / b; };
   dh.n_nt = tiles(f, C::RBN);
   q.dx.n_nt = tiles(d, C::RBN);
   q.dw13.n_mt = 2 * tiles(f, C::WBM);
   q.dw13.n_nt = tiles(d, C::WBN);
   q.dw2.n_mt = tiles(d, C::WBM);
   q.dw2.n_nt = tiles(f, C::WBN);
-  k1<<<row_blocks(dh, C::RBM), C::NT, C::ROW_LDS, st>>>(dh);
-  q.end_dx = (row_blocks(q.dx, C::RBM) + 7) / 8 * 8;
+  const int rt = row_tiles(dh.R, dh.E, C::RBM);
+  k1<<<rt * dh.n_nt, C::NT, C::ROW_LDS, st>>>(dh);
+  q.end_dx = tiles(rt * q.dx.n_nt * q.dx.splits, 8) * 8;
   q.end_dw13 = q.end_dx + weight_blocks(q.dw13);
   q.end_dw2 = q.end_dw13 + weight_blocks(q.dw2);
   k2<<<q.end_dw2, C::NT, rest_lds, st>>>(q);
@@ -570,9 +627,39 @@ hipError_t launch_both(GradParams dh, RestParams q, hipStream_t st) {
 
 }  // namespace
 
-int grad_planes_bf16(int d_ff) { return (d_ff + 63) / 64; }
+namespace {
 
-hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, int *planes, hipStream_t st) {
+// One block of 8 waves per CU; or four blocks of 4 waves, which overlap each
+// other's first loads and last stores but move 1.6 times the bytes through L2
+// per product.
+using Big = Cfg<320, 256, 256, 256, 8, 64, 1, 1>;
+using Small = Cfg<128, 128, 128, 128, 4, 32, 4, 2>;
+
+// Small tiles where blocks are short, few, or mostly padding (measured, Big
+// against Small, us):
+//   at most 128 rows per expert: 128 experts, d = d_ff = 2880, 256 tokens top-4
+//     2838 against 2154, 4096 tokens Zipf-skewed 4237 against 3642 (uniform
+//     3843 against 4039); at 256 rows (8 experts, 1024 x 4096) 199 against 234
+//   the dh product under half a round of the CUs: 1 expert, 2048 x 8192, 500
+//     tokens 168 against 155; 1024 tokens (160 blocks) 268 against 260
+//   padding: d = 264, d_ff = 520, 8000 tokens 116 against 88.  Without padding
+//     Small takes 1.2 times as long (Mixtral-shaped 11.7 against 14.1 ms).
+bool use_small(const FfnGradArgs &a) {
+  auto area = [&](int b) { return (double)(tiles(a.d, b) * b) * (tiles(a.d_ff, b) * b); };
+  return a.R <= 128ll * a.E || row_tiles(a.R, a.E, Big::RBM) * tiles(a.d_ff, Big::RBN) < 128 ||
+         1.2 * area(128) < area(256);
+}
+
+}  // namespace
+
+GradPlan grad_plan_bf16(const FfnGradArgs &a) {
+  GradPlan p{};
+  p.dw_planes = tiles(a.d_ff, 64);
+  p.dx_splits = use_small(a) ? dx_splits<Small>(a.R, a.E, a.d, a.d_ff) : dx_splits<Big>(a.R, a.E, a.d, a.d_ff);
+  return p;
+}
+
+hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t st) {
   GradParams b{};
   b.offsets = a.offsets;
   b.slot = a.slot;
@@ -582,6 +669,7 @@ hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, int *plane
   b.d = a.d;
   b.f = a.d_ff;
   b.src_bytes = (uint32_t)((size_t)(a.perm ? a.n : a.R) * a.d * 2);
+  b.splits = 1;
 
   GradParams p = b;
   p.a0 = (const uint16_t *)a.dy;
@@ -603,6 +691,8 @@ hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, int *plane
   q.dx.b0 = (const uint16_t *)a.w1;
   q.dx.b1 = (const uint16_t *)a.w3;
   q.dx.c0 = a.da;
+  q.dx.splits = w.plan.dx_splits;
+  q.dx.dx_part = w.dx_part;
   q.dw13.b0 = (const uint16_t *)a.a;
   q.dw13.perm = q.dw2.perm = a.perm;
   q.dw13.c0 = a.dw1;
@@ -610,11 +700,8 @@ hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, int *plane
   q.dw2.a0 = (const uint16_t *)a.dy;
   q.dw2.b0 = (const uint16_t *)w.hs;
   q.dw2.c0 = a.dw2;
-#ifndef CFG
-#define CFG 320, 256, 256, 256, 8, 64, 1
-#endif
-  using Big = Cfg<CFG>;
-  *planes = grad_planes_bf16(a.d_ff);
+  if (use_small(a))
+    return a.perm ? launch_both<true, Small>(p, q, st) : launch_both<false, Small>(p, q, st);
   return a.perm ? launch_both<true, Big>(p, q, st) : launch_both<false, Big>(p, q, st);
 }
 
