@@ -19,8 +19,8 @@ struct FinishParams {
   const int32_t *offsets, *perm, *inv;
   float *dw;
   const float *dx_part;
-  int S;
-  uint16_t *da;
+  int S, bf16;
+  void *da;
   int w_blocks;  // blocks of the weights' gradient (0 without a combine)
 };
 
@@ -29,8 +29,7 @@ struct FinishParams {
 // w + 16, ... of each; the 16 sums are added in wave order, so the result
 // does not depend on scheduling.  The sum of row r goes to the pair whose row
 // it is; pairs without a row (inv outside [0, R)) get 0.  The other blocks:
-// the piled rows of da, eight columns a thread, as the sum of their S planes
-// in order (d % 8 == 0).
+// the piled rows of da, eight elements a thread, as the sum of their S planes in order.
 __global__ __launch_bounds__(1024) void ffn_grad_finish_kernel(FinishParams p) {
   __shared__ float s_p[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -52,16 +51,28 @@ __global__ __launch_bounds__(1024) void ffn_grad_finish_kernel(FinishParams p) {
     if (wave == 1 && r < p.R && (unsigned)p.inv[r] >= (unsigned)p.R) p.dw[r] = 0.f;  // pair r
     return;
   }
-  const size_t at = ((size_t)(blockIdx.x - p.w_blocks) * 1024 + threadIdx.x) * 8;
-  if (at >= (size_t)p.offsets[p.E] * p.d) return;
-  const size_t plane = (size_t)p.R * p.d;
-  f32x4 a = *(const f32x4 *)(p.dx_part + at), b = *(const f32x4 *)(p.dx_part + at + 4);
-  for (int s = 1; s < p.S; ++s) {
-    a += *(const f32x4 *)(p.dx_part + s * plane + at);
-    b += *(const f32x4 *)(p.dx_part + s * plane + at + 4);
+  const size_t total = (size_t)p.offsets[p.E] * p.d, plane = (size_t)p.R * p.d;
+  const size_t first = (size_t)(blockIdx.x - p.w_blocks) * 8192;
+  if (p.bf16) {
+    const size_t at = first + threadIdx.x * 8;
+    if (at >= total) return;
+    f32x4 a = *(const f32x4 *)(p.dx_part + at), b = *(const f32x4 *)(p.dx_part + at + 4);
+    for (int s = 1; s < p.S; ++s) {
+      a += *(const f32x4 *)(p.dx_part + s * plane + at);
+      b += *(const f32x4 *)(p.dx_part + s * plane + at + 4);
+    }
+    *(u32x4 *)((uint16_t *)p.da + at) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                              pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const size_t at = first + threadIdx.x + 1024 * i;
+      if (at >= total) return;
+      float v = p.dx_part[at];
+      for (int s = 1; s < p.S; ++s) v += p.dx_part[s * plane + at];
+      ((float *)p.da)[at] = v;
+    }
   }
-  *(u32x4 *)(p.da + at) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]),
-                                pack_bf16x2(b[2], b[3])};
 }
 
 struct Layout {
@@ -105,9 +116,10 @@ hipError_t launch_ffn_grad(const FfnGradArgs &a, hipStream_t st) {
   p.dw = a.dtopk_w;
   p.dx_part = w.dx_part;
   p.S = L.plan.dx_splits;
-  p.da = (uint16_t *)a.da;
+  p.da = a.da;
+  p.bf16 = a.bf16;
   p.w_blocks = a.perm ? (a.R + 63) / 64 : 0;
-  const size_t sums = p.S > 1 ? ((size_t)a.R * a.d / 8 + 1023) / 1024 : 0;
+  const size_t sums = p.S > 1 ? ((size_t)a.R * a.d + 8191) / 8192 : 0;
   if (p.w_blocks + sums == 0) return hipSuccess;
   ffn_grad_finish_kernel<<<(unsigned)(p.w_blocks + sums), 1024, 0, st>>>(p);
   return hipGetLastError();

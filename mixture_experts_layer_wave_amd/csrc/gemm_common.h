@@ -115,11 +115,13 @@ struct TileSlot {
 // column tiles) and each column tile's weights (across the group's row
 // tiles) in L2; without it a large pile's rows are streamed again for every
 // column tile.
+// b: the block's index among the list's blocks (the whole grid's, unless the
+// grid holds other work too).
 template <bool LPT = false, typename RowTile, bool BAL = false>
 __device__ __forceinline__ void map_block_fn(const int32_t *offsets, int E, int n_tiles, int S,
                                              int lane, TileSlot *out, RowTile bm_of,
                                              std::integral_constant<bool, BAL> = {}, int S1 = 0,
-                                             int RG = 0) {
+                                             int RG = 0, int b = blockIdx.x) {
   if (S1 <= 0) S1 = S;
   const int per = (E + MOE_WAVE - 1) / MOE_WAVE;
   const int eb = lane * per, ee = min(E, eb + per);
@@ -146,7 +148,6 @@ __device__ __forceinline__ void map_block_fn(const int32_t *offsets, int E, int 
   const int incl0 = wave_incl_scan(loc0), incl1 = LPT ? wave_incl_scan(loc1) : 0;
   const int tot0 = __builtin_amdgcn_readlane(incl0, MOE_WAVE - 1) * n_tiles * S;
   const int tot1 = LPT ? __builtin_amdgcn_readlane(incl1, MOE_WAVE - 1) * n_tiles * S1 : 0;
-  const int b = blockIdx.x;
   const int xcd = b & 7, slot = b >> 3;
   int base0 = 0, base1 = 0;
   for (int x = 0; x < xcd; ++x) {
@@ -205,9 +206,10 @@ __device__ __forceinline__ void map_block_fn(const int32_t *offsets, int E, int 
 
 template <int BM, bool LPT = false, bool BAL = false>
 __device__ __forceinline__ void map_block(const int32_t *offsets, int E, int n_tiles, int S,
-                                          int lane, TileSlot *out, int S1 = 0, int RG = 0) {
+                                          int lane, TileSlot *out, int S1 = 0, int RG = 0,
+                                          int b = blockIdx.x) {
   map_block_fn<LPT>(offsets, E, n_tiles, S, lane, out, [](int) { return BM; },
-                    std::integral_constant<bool, BAL>{}, S1, RG);
+                    std::integral_constant<bool, BAL>{}, S1, RG, b);
 }
 
 // f32 stores of a block's accumulators: acc[tm][tn] of wave (wm, wn) holds

@@ -3,13 +3,17 @@
 //
 // Block of 256 threads (4 waves, 2 x 2), output tile 64 x 64 (each wave
 // 32 x 32 on v_mfma_f32_32x32x2_f32), K steps of 32.  Both operands lie in
-// LDS K row by K row, 65 floats apart, so that the stores of operands that
-// are contiguous along K (32 K of one row by 32 lanes) and the fragment
-// reads (32 rows of one K) both meet 64 different banks.  Elements come
-// through a function of (k, row), zero outside the operand, so every size,
-// gather and layout runs through the same loop; the next step's elements are
-// fetched while this step is multiplied.
+// LDS K row by K row, 65 floats apart, in two stages with one barrier a step;
+// a thread fetches four consecutive elements at a time, two steps ahead
+// (these products are small, so the trip to memory is most of a step).  A
+// 16-byte fetch needs 4-byte alignment only, so every size and layout takes
+// it; pieces cut by an edge are read element by element, zero outside.
+//
+// A sum over K is taken in runs of 256, each from zero, added to a total:
+// the error of a long sum then grows with the runs, not with K.
 #pragma once
+
+#include <type_traits>
 
 #include "common.h"
 
@@ -17,60 +21,109 @@ namespace moe {
 namespace f32gemm {
 
 constexpr int kT = 64, kK = 32, kPitch = kT + 1, kThreads = 256;
-constexpr int kPer = kT * kK / kThreads;  // elements a thread fetches per operand and step
+constexpr int kFour = kT * kK / 4 / kThreads;  // pieces a thread fetches per operand and step
+constexpr int kStage = 2 * kK * kPitch;        // floats of both tiles of a stage
+constexpr int kSmem = 2 * kStage;
 
-// (k, row) of element i of this thread in a step: lanes run along K for
-// operands contiguous along K, along the rows otherwise.
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+// Four consecutive elements, of which the first `n` (<= 0: none, >= 4: all)
+// are inside the operand.
+struct Piece {
+  const float *p;
+  int n;
+};
+__device__ __forceinline__ f32x4 fetch4(Piece q) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (q.n >= 4) {
+    v = *(const f32x4_any *)q.p;
+  } else if (q.n > 0) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (j < q.n) v[j] = q.p[j];
+  }
+  return v;
+}
+
+// (k, row) of the first element of piece i of this thread in a step: pieces
+// run along the rows' index for K-major operands, along K otherwise.
 template <bool KMAJ>
 __device__ __forceinline__ void place(int i, int &k, int &r) {
   const int t = threadIdx.x;
   if constexpr (KMAJ) {
-    r = t & (kT - 1);
-    k = (t >> 6) + i * (kThreads / kT);
+    r = (t & 15) * 4;
+    k = (t >> 4) + i * 16;
   } else {
-    k = t & (kK - 1);
-    r = (t >> 5) + i * (kThreads / kK);
+    k = (t & 7) * 4;
+    r = (t >> 3) + i * 32;
   }
 }
+template <bool KMAJ>
+__device__ __forceinline__ void put(float *tile, int i, f32x4 v) {
+  int k, r;
+  place<KMAJ>(i, k, r);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) tile[KMAJ ? k * kPitch + r + j : (k + j) * kPitch + r] = v[j];
+}
 
-// acc += sum over k < K of A(k, m) B(k, n): lane l of wave (wm, wn) holds row
-// m = 32 wm + l % 32 and columns n = 32 wn + (i / 4) 8 + (l / 32) 4 + i % 4.
-// fa(i, k, m) and fb(i, k, n) give element i of the thread at tile rows m, n;
-// they are called with k < K only.  smem: 2 * kK * kPitch floats.
+// total += sum over k < K of A(k, m) B(k, n): lane l of wave (wm, wn) holds
+// row m = 32 wm + l % 32 and columns n = 32 wn + (i / 4) 8 + (l / 32) 4 + i % 4.
+// fa(i, k, m) and fb(i, k, n) give the thread's piece i at tile row m or
+// column n; for K-major operands they are called with k < K only, else the
+// piece is cut at K here.  smem: kSmem floats.
 template <bool A_KMAJ, bool B_KMAJ, typename FA, typename FB>
-__device__ __forceinline__ void product(f32x16 &acc, float *smem, int K, FA fa, FB fb) {
-  float *sa = smem, *sb = smem + kK * kPitch;
+__device__ __forceinline__ void product(f32x16 &total, float *smem, int K, FA fa, FB fb) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int am = (wave >> 1) * 32 + (lane & 31), bn = (wave & 1) * 32 + (lane & 31), kh = lane >> 5;
-  float ra[kPer], rb[kPer];
-  auto fetch = [&](int k0) {
+  auto get = [&](auto kmaj, auto f, int i, int k0) {
+    constexpr bool KMAJ = decltype(kmaj)::value;
+    int k, r;
+    place<KMAJ>(i, k, r);
+    Piece q = {nullptr, 0};
+    if (k0 + k < K) {
+      q = f(i, k0 + k, r);
+      if (!KMAJ && q.n > 0) q.n = K - k0 - k;
+    }
+    return fetch4(q);
+  };
+  f32x4 ra[2][kFour], rb[2][kFour];
+  auto fetch = [&](f32x4 *a, f32x4 *b, int k0) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      int k, r;
-      place<A_KMAJ>(i, k, r);
-      ra[i] = k0 + k < K ? fa(i, k0 + k, r) : 0.f;
-      place<B_KMAJ>(i, k, r);
-      rb[i] = k0 + k < K ? fb(i, k0 + k, r) : 0.f;
+    for (int i = 0; i < kFour; ++i) {
+      a[i] = get(std::integral_constant<bool, A_KMAJ>{}, fa, i, k0);
+      b[i] = get(std::integral_constant<bool, B_KMAJ>{}, fb, i, k0);
     }
   };
-  fetch(0);
-  for (int k0 = 0; k0 < K; k0 += kK) {
-    __syncthreads();  // the tiles of the step before have been read
+  f32x16 acc = {};
+  const int steps = (K + kK - 1) / kK;
+  fetch(ra[0], rb[0], 0);
+  fetch(ra[1], rb[1], kK);
+  __syncthreads();  // smem's readers before this call are done
+  auto step = [&](int s, auto odd) {
+    constexpr int P = decltype(odd)::value;
+    // (stage P was last read in step s - 2, before the barrier of s - 1)
+    float *sa = smem + P * kStage, *sb = sa + kK * kPitch;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      int k, r;
-      place<A_KMAJ>(i, k, r);
-      sa[k * kPitch + r] = ra[i];
-      place<B_KMAJ>(i, k, r);
-      sb[k * kPitch + r] = rb[i];
+    for (int i = 0; i < kFour; ++i) {
+      put<A_KMAJ>(sa, i, ra[P][i]);
+      put<B_KMAJ>(sb, i, rb[P][i]);
     }
+    fetch(ra[P], rb[P], (s + 2) * kK);
     __syncthreads();
-    if (k0 + kK < K) fetch(k0 + kK);
 #pragma unroll
     for (int k = 0; k < kK; k += 2)
       acc = __builtin_amdgcn_mfma_f32_32x32x2f32(sb[(k + kh) * kPitch + bn], sa[(k + kh) * kPitch + am],
                                                  acc, 0, 0, 0);
+    if ((s & 7) == 7) {
+      total += acc;
+      acc = f32x16{};
+    }
+  };
+  for (int s = 0; s < steps; s += 2) {
+    step(s, std::integral_constant<int, 0>{});
+    if (s + 1 < steps) step(s + 1, std::integral_constant<int, 1>{});
   }
+  total += acc;
 }
 
 // Tile-relative row and column of accumulator element i.

@@ -22,23 +22,26 @@ struct F32Params {
   int n_slots, n, k, E, R, d, f, n_nt;
   const float *w1, *w3, *w2, *g, *u;
   float *dg, *du, *hs, *part;  // gradient
-  float *o0, *o1, *o2;         // outputs of the product
+  float *o0, *o1, *o2, *o3;    // up: h, g, u; gradient: da's planes, dW1, dW3, dW2
+  int splits;                  // da's planes
 };
 
 __device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + expf(-g)); }
 
-// The tile's pile, first row, rows and column tile, from the pile sizes.
-__device__ __forceinline__ bool row_tile(const F32Params &p, TileSlot &s_t) {
-  if (threadIdx.x < 64) gemm::map_block<kT>(p.offsets, p.E, p.n_nt, 1, threadIdx.x, &s_t);
+// The tile's pile, first row, rows, column tile and K range, from the pile
+// sizes; false for a block without work.
+__device__ __forceinline__ bool row_tile(const F32Params &p, TileSlot &s_t, int block, int splits) {
+  if (threadIdx.x < 64)
+    gemm::map_block<kT>(p.offsets, p.E, p.n_nt, splits, threadIdx.x, &s_t, splits, 0, block);
   __syncthreads();
   return s_t.e >= 0;
 }
 
-// Rows of this thread's elements of an operand contiguous along K, gathered
-// or not (past the tile's rows: -1).
-__device__ __forceinline__ void source_rows(int (&src)[kPer], const int32_t *perm, int row0, int rows) {
+// Rows of this thread's pieces of an operand contiguous along K, gathered or
+// not (past the tile's rows: -1).
+__device__ __forceinline__ void source_rows(int (&src)[kFour], const int32_t *perm, int row0, int rows) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+  for (int i = 0; i < kFour; ++i) {
     int k, r;
     place<false>(i, k, r);
     src[i] = r < rows ? (perm ? perm[row0 + r] : row0 + r) : -1;
@@ -47,16 +50,16 @@ __device__ __forceinline__ void source_rows(int (&src)[kPer], const int32_t *per
 
 // g = a W1^T, u = a W3^T, h = silu(g) u.
 __global__ __launch_bounds__(kThreads) void up_save_f32_kernel(F32Params p) {
-  __shared__ float smem[2 * kK * kPitch];
+  __shared__ float smem[kSmem];
   __shared__ TileSlot s_t;
-  if (!row_tile(p, s_t)) return;
+  if (!row_tile(p, s_t, blockIdx.x, 1)) return;
   const int row0 = s_t.row0, rows = s_t.rows, n0 = s_t.nt * kT;
   const size_t mat = (size_t)phys_slot(p.slot, p.n_slots, s_t.e) * p.f * p.d;
-  int src[kPer];
+  int src[kFour];
   source_rows(src, p.perm, row0, rows);
-  auto fa = [&](int i, int k, int) { return src[i] >= 0 ? p.a[(size_t)src[i] * p.d + k] : 0.f; };
+  auto fa = [&](int i, int k, int) { return Piece{p.a + (size_t)src[i] * p.d + k, src[i] >= 0 ? 4 : 0}; };
   auto weights = [&](const float *w) {
-    return [=](int, int k, int c) { return n0 + c < p.f ? w[mat + (size_t)(n0 + c) * p.d + k] : 0.f; };
+    return [=](int, int k, int c) { return Piece{w + mat + (size_t)(n0 + c) * p.d + k, n0 + c < p.f ? 4 : 0}; };
   };
   f32x16 ga = {}, ua = {};
   product<false, false>(ga, smem, p.d, fa, weights(p.w1));
@@ -77,17 +80,18 @@ __global__ __launch_bounds__(kThreads) void up_save_f32_kernel(F32Params p) {
 // dh0 = dy W2 and what follows from it; row sums of dh0 h over each wave's 32
 // columns go to part[plane][row].
 __global__ __launch_bounds__(kThreads) void dh_f32_kernel(F32Params p) {
-  __shared__ float smem[2 * kK * kPitch];
+  __shared__ float smem[kSmem];
   __shared__ TileSlot s_t;
-  if (!row_tile(p, s_t)) return;
+  if (!row_tile(p, s_t, blockIdx.x, 1)) return;
   const int row0 = s_t.row0, rows = s_t.rows, n0 = s_t.nt * kT;
   const float *w2 = p.w2 + (size_t)phys_slot(p.slot, p.n_slots, s_t.e) * p.d * p.f;
-  int src[kPer];
+  int src[kFour];
   source_rows(src, p.perm, row0, rows);
   f32x16 acc = {};
   product<false, true>(
-      acc, smem, p.d, [&](int i, int k, int) { return src[i] >= 0 ? p.dy[(size_t)src[i] * p.d + k] : 0.f; },
-      [&](int, int k, int c) { return n0 + c < p.f ? w2[(size_t)k * p.f + n0 + c] : 0.f; });
+      acc, smem, p.d,
+      [&](int i, int k, int) { return Piece{p.dy + (size_t)src[i] * p.d + k, src[i] >= 0 ? 4 : 0}; },
+      [&](int, int k, int c) { return Piece{w2 + (size_t)k * p.f + n0 + c, p.f - n0 - c}; });
   const int r = out_row();
   float wr = 1.f, sum = 0.f;
   if (p.perm && r < rows) {
@@ -114,37 +118,40 @@ __global__ __launch_bounds__(kThreads) void dh_f32_kernel(F32Params p) {
   if (p.perm && (threadIdx.x & 63) < 32 && r < rows) p.part[(size_t)plane * p.R + row0 + r] = sum;
 }
 
-// da = dg W1 + du W3.
-__global__ __launch_bounds__(kThreads) void dx_f32_kernel(F32Params p) {
-  __shared__ float smem[2 * kK * kPitch];
-  __shared__ TileSlot s_t;
-  if (!row_tile(p, s_t)) return;
+// One K range of da = dg W1 + du W3: split 2 s + h of 2 S is range s of half
+// h (0: dg W1, 1: du W3); its sums go to plane dx_part[split][R][d].
+__device__ __forceinline__ void dx_tile(const F32Params &p, int block, float *smem, TileSlot &s_t) {
+  if (!row_tile(p, s_t, block, p.splits)) return;
   const int row0 = s_t.row0, rows = s_t.rows, n0 = s_t.nt * kT;
   const size_t mat = (size_t)phys_slot(p.slot, p.n_slots, s_t.e) * p.f * p.d;
+  const int half = s_t.split & 1, S = p.splits / 2, steps = (p.f + kK - 1) / kK;
+  const int k0 = (int)((long long)(s_t.split / 2) * steps / S) * kK;
+  const int k1 = min(p.f, (int)((long long)(s_t.split / 2 + 1) * steps / S) * kK);
+  const float *dz = (half ? p.du : p.dg) + (size_t)row0 * p.f + k0;
+  const float *w = (half ? p.w3 : p.w1) + mat + (size_t)k0 * p.d;
   f32x16 acc = {};
-  for (int half = 0; half < 2; ++half) {
-    const float *dz = half ? p.du : p.dg, *w = (half ? p.w3 : p.w1) + mat;
-    product<false, true>(
-        acc, smem, p.f, [&](int, int k, int m) { return m < rows ? dz[(size_t)(row0 + m) * p.f + k] : 0.f; },
-        [&](int, int k, int c) { return n0 + c < p.d ? w[(size_t)k * p.d + n0 + c] : 0.f; });
-  }
+  product<false, true>(
+      acc, smem, k1 - k0,
+      [&](int, int k, int m) { return Piece{dz + (size_t)m * p.f + k, m < rows ? 4 : 0}; },
+      [&](int, int k, int c) { return Piece{w + (size_t)k * p.d + n0 + c, p.d - n0 - c}; });
+  float *out = p.o0 + ((size_t)s_t.split * p.R + row0) * p.d;
   const int r = out_row();
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int c = n0 + out_col(i);
-    if (r < rows && c < p.d) p.o0[(size_t)(row0 + r) * p.d + c] = acc[i];
+    if (r < rows && c < p.d) out[(size_t)r * p.d + c] = acc[i];
   }
 }
 
-// Weight gradients of expert blockIdx.z: dW1 and dW3 (f x d; blockIdx.y runs
-// over the row tiles of dW1, then of dW3), or dW2 (d x f).
+// Weight gradients: dW1 and dW3 (f x d; row tiles of dW1, then of dW3), or
+// dW2 (d x f).  Blocks run over an expert's column tiles, then its row tiles.
 template <bool W2>
-__global__ __launch_bounds__(kThreads) void dw_f32_kernel(F32Params p) {
-  __shared__ float smem[2 * kK * kPitch];
-  const int e = blockIdx.z, n0 = blockIdx.x * kT;
-  const int M = W2 ? p.d : p.f, N = W2 ? p.f : p.d, mt = (M + kT - 1) / kT;
-  const bool second = !W2 && (int)blockIdx.y >= mt;
-  const int m0 = ((int)blockIdx.y - (second ? mt : 0)) * kT;
+__device__ __forceinline__ void dw_tile(const F32Params &p, int block, float *smem) {
+  const int M = W2 ? p.d : p.f, N = W2 ? p.f : p.d, mt = (M + kT - 1) / kT, nt = (N + kT - 1) / kT;
+  const int per = (W2 ? mt : 2 * mt) * nt, e = block / per, tile = block % per;
+  const int n0 = tile % nt * kT;
+  const bool second = !W2 && tile / nt >= mt;
+  const int m0 = (tile / nt - (second ? mt : 0)) * kT;
   const int row0 = p.offsets[e], rows = p.offsets[e + 1] - row0;
   const float *dz = second ? p.du : p.dg;
   auto token = [&](int k) { return (size_t)(p.perm ? p.perm[row0 + k] : row0 + k); };
@@ -152,14 +159,12 @@ __global__ __launch_bounds__(kThreads) void dw_f32_kernel(F32Params p) {
   product<true, true>(
       acc, smem, rows,
       [&](int, int k, int m) {
-        if (m0 + m >= M) return 0.f;
-        return W2 ? p.dy[token(k) * p.d + m0 + m] : dz[(size_t)(row0 + k) * p.f + m0 + m];
+        return Piece{(W2 ? p.dy + token(k) * p.d : dz + (size_t)(row0 + k) * p.f) + m0 + m, M - m0 - m};
       },
       [&](int, int k, int c) {
-        if (n0 + c >= N) return 0.f;
-        return W2 ? p.hs[(size_t)(row0 + k) * p.f + n0 + c] : p.a[token(k) * p.d + n0 + c];
+        return Piece{(W2 ? p.hs + (size_t)(row0 + k) * p.f : p.a + token(k) * p.d) + n0 + c, N - n0 - c};
       });
-  float *out = (second ? p.o1 : p.o0) + (size_t)e * M * N;
+  float *out = (W2 ? p.o3 : second ? p.o2 : p.o1) + (size_t)e * M * N;
   const int r = m0 + out_row();
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -168,11 +173,32 @@ __global__ __launch_bounds__(kThreads) void dw_f32_kernel(F32Params p) {
   }
 }
 
+// Everything that waits for dg, du and w h, in one grid: da, then dW1 and
+// dW3, then dW2.
+__global__ __launch_bounds__(kThreads) void rest_f32_kernel(F32Params p, int end_dx, int end_dw13) {
+  __shared__ float smem[kSmem];
+  __shared__ TileSlot s_t;
+  const int b = blockIdx.x;
+  if (b < end_dx)
+    dx_tile(p, b, smem, s_t);
+  else if (b < end_dw13)
+    dw_tile<false>(p, b - end_dx, smem);
+  else
+    dw_tile<true>(p, b - end_dw13, smem);
+}
+
 int row_tiles(int R, int E) { return (R + kT - 1) / kT + (E < R ? E : R); }
 
 }  // namespace
 
-GradPlan grad_plan_f32(const FfnGradArgs &a) { return {(a.d_ff + kT - 1) / kT * 2, 1}; }
+// da's K ranges, two at least (one for each of its two products), more until
+// its blocks fill the chip four to a CU, each range 128 deep at least.
+GradPlan grad_plan_f32(const FfnGradArgs &a) {
+  const int blocks = row_tiles(a.R, a.E) * ((a.d + kT - 1) / kT) * 2;
+  int S = blocks < 1024 ? 1024 / blocks : 1;
+  if (S > a.d_ff / 128) S = a.d_ff / 128;
+  return {(a.d_ff + kT - 1) / kT * 2, 2 * (S < 1 ? 1 : S)};
+}
 
 hipError_t launch_up_save_f32(const FfnArgs &a, void *g, void *u, hipStream_t st) {
   F32Params p{};
@@ -221,17 +247,17 @@ hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t
   p.hs = (float *)w.hs;
   p.part = w.part;
   const int ft = (p.f + kT - 1) / kT, dt = (p.d + kT - 1) / kT;
-  const int tiles = row_tiles(p.R, p.E);
+  const int rt = row_tiles(p.R, p.E);
   p.n_nt = ft;
-  dh_f32_kernel<<<tiles * ft, kThreads, 0, st>>>(p);
+  dh_f32_kernel<<<rt * ft, kThreads, 0, st>>>(p);
   p.n_nt = dt;
-  p.o0 = (float *)a.da;
-  dx_f32_kernel<<<tiles * dt, kThreads, 0, st>>>(p);
-  p.o0 = (float *)a.dw1;
-  p.o1 = (float *)a.dw3;
-  dw_f32_kernel<false><<<dim3(dt, 2 * ft, p.E), kThreads, 0, st>>>(p);
-  p.o0 = (float *)a.dw2;
-  dw_f32_kernel<true><<<dim3(ft, dt, p.E), kThreads, 0, st>>>(p);
+  p.splits = w.plan.dx_splits;
+  p.o0 = w.dx_part;
+  p.o1 = (float *)a.dw1;
+  p.o2 = (float *)a.dw3;
+  p.o3 = (float *)a.dw2;
+  const int end_dx = (rt * dt * p.splits + 7) / 8 * 8, dw = p.E * ft * dt;
+  rest_f32_kernel<<<end_dx + 3 * dw, kThreads, 0, st>>>(p, end_dx, end_dx + 2 * dw);
   return hipGetLastError();
 }
 

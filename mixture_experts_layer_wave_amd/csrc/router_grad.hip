@@ -288,12 +288,12 @@ using namespace f32gemm;
 __global__ __launch_bounds__(kThreads) void router_dx_f32_kernel(
     const float *__restrict__ dz, const float *__restrict__ wg, const float *__restrict__ da,
     const int32_t *__restrict__ inv, int n, int d, int E, int k, float *__restrict__ dx) {
-  __shared__ float smem[2 * kK * kPitch];
+  __shared__ float smem[kSmem];
   const int t0 = blockIdx.x * kT, c0 = blockIdx.y * kT;
   f32x16 acc = {};
   product<false, true>(
-      acc, smem, E, [&](int, int e, int t) { return t0 + t < n ? dz[(size_t)(t0 + t) * E + e] : 0.f; },
-      [&](int, int e, int c) { return c0 + c < d ? wg[(size_t)e * d + c0 + c] : 0.f; });
+      acc, smem, E, [&](int, int e, int t) { return Piece{dz + (size_t)(t0 + t) * E + e, t0 + t < n ? 4 : 0}; },
+      [&](int, int e, int c) { return Piece{wg + (size_t)e * d + c0 + c, d - c0 - c}; });
   const int t = t0 + out_row();
   const unsigned R = (unsigned)n * (unsigned)k;
   if (t >= n) return;
@@ -318,15 +318,15 @@ __global__ __launch_bounds__(kThreads) void router_dw_f32_kernel(const float *__
                                                                  const float *__restrict__ x, int n, int d,
                                                                  int E, int range, float *__restrict__ part,
                                                                  float *__restrict__ bias_part) {
-  __shared__ float smem[2 * kK * kPitch];
+  __shared__ float smem[kSmem];
   __shared__ float s_b[kThreads];
   const int c0 = blockIdx.x * kT, e0 = blockIdx.z * kT;
   const int tb = blockIdx.y * range, te = min(n, tb + range);
   f32x16 acc = {};
   product<true, true>(
       acc, smem, te - tb,
-      [&](int, int t, int e) { return e0 + e < E ? dz[(size_t)(tb + t) * E + e0 + e] : 0.f; },
-      [&](int, int t, int c) { return c0 + c < d ? x[(size_t)(tb + t) * d + c0 + c] : 0.f; });
+      [&](int, int t, int e) { return Piece{dz + (size_t)(tb + t) * E + e0 + e, E - e0 - e}; },
+      [&](int, int t, int c) { return Piece{x + (size_t)(tb + t) * d + c0 + c, d - c0 - c}; });
   const int e = e0 + out_row();
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
