@@ -349,7 +349,9 @@ int moe_layer_norm_backward(int32_t n, int32_t d, const void *dy, const void *x,
  * float32 value), f32 for F32 weights.  The other arguments and src(r) as in
  * moe_expert_up; h goes to moe_expert_down.  Rows outside the piles are left
  * as they were.  F32 and BF16 weights only (MOE_ERR_DTYPE otherwise); d and
- * d_ff below 2^20; with BF16 weights a, h, g and u 16-byte aligned.
+ * d_ff below 2^20, and operands under 2^31 bytes: n*k*max(d, d_ff) and
+ * d*d_ff below 2^30 with BF16 and 2^29 with F32 weights (MOE_ERR_SHAPE);
+ * with BF16 weights a, h, g and u 16-byte aligned.
  * A dense gated feed-forward block is the case E = 1, k = 1, perm = NULL,
  * offsets = {0, n}. */
 int moe_expert_up_save(const moe_shape *s, const void *a, int act, const int32_t *perm,
@@ -383,8 +385,8 @@ int moe_expert_up_save(const moe_shape *s, const void *a, int act, const int32_t
  * Matrices have the type of act and the weights, F32 or BF16 (MOE_ERR_DTYPE
  * otherwise).  Products accumulate in float32 and outputs are rounded once;
  * with BF16 weights dg, du and w silu(g) u are rounded to bf16 in between
- * (the matrix cores' input type) and pointers are 16-byte aligned.  d and
- * d_ff below 2^20.  Deterministic.  The size helper returns 0 for an invalid
+ * (the matrix cores' input type) and pointers are 16-byte aligned.  Sizes as
+ * in moe_expert_up_save.  Deterministic.  The size helper returns 0 for an invalid
  * shape or weight dtype. */
 size_t moe_grouped_ffn_backward_workspace_bytes(const moe_shape *s, int w_dtype);
 int moe_grouped_ffn_backward(const moe_shape *s, const void *dy, const void *a, int act,
@@ -415,8 +417,8 @@ int moe_grouped_ffn_backward(const moe_shape *s, const void *dy, const void *a, 
  * ws       at least moe_router_backward_workspace_bytes(s), 16-byte aligned
  * Sums are float32; with MOE_BF16 dlogits enters the two products with 16 of
  * its 24 bits, and dx and dwg are rounded once.  A token whose logits are
- * all -inf has dlogits 0; one with a NaN logit has NaN.  n < 2^24, d < 2^20;
- * MOE_BF16 needs d % 8 == 0 and 16-byte aligned x, wg, da_perm, dx and dwg.
+ * all -inf has dlogits 0; one with a NaN logit has NaN.  n < 2^24, d < 2^20,
+ * E*d < 2^29; MOE_BF16 needs d % 8 == 0 and 16-byte aligned x, wg, da_perm, dx and dwg.
  * Deterministic.  The size helper returns 0 for an invalid shape. */
 size_t moe_router_backward_workspace_bytes(const moe_shape *s);
 int moe_router_backward(const moe_shape *s, const float *logits, const int32_t *topk_idx,

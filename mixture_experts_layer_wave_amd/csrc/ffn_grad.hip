@@ -29,7 +29,8 @@ struct FinishParams {
 // w + 16, ... of each; the 16 sums are added in wave order, so the result
 // does not depend on scheduling.  The sum of row r goes to the pair whose row
 // it is; pairs without a row (inv outside [0, R)) get 0.  The other blocks:
-// the piled rows of da, eight elements a thread, as the sum of their S planes in order.
+// the piled rows of da, four elements a thread (bf16) or one, as the sum of their S planes in
+// order.
 __global__ __launch_bounds__(1024) void ffn_grad_finish_kernel(FinishParams p) {
   __shared__ float s_p[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -52,26 +53,19 @@ __global__ __launch_bounds__(1024) void ffn_grad_finish_kernel(FinishParams p) {
     return;
   }
   const size_t total = (size_t)p.offsets[p.E] * p.d, plane = (size_t)p.R * p.d;
-  const size_t first = (size_t)(blockIdx.x - p.w_blocks) * 8192;
+  const size_t i = (size_t)(blockIdx.x - p.w_blocks) * 1024 + threadIdx.x;
   if (p.bf16) {
-    const size_t at = first + threadIdx.x * 8;
-    if (at >= total) return;
-    f32x4 a = *(const f32x4 *)(p.dx_part + at), b = *(const f32x4 *)(p.dx_part + at + 4);
-    for (int s = 1; s < p.S; ++s) {
-      a += *(const f32x4 *)(p.dx_part + s * plane + at);
-      b += *(const f32x4 *)(p.dx_part + s * plane + at + 4);
-    }
-    *(u32x4 *)((uint16_t *)p.da + at) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
-                                              pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+    if (i * 4 >= total) return;
+    f32x4 v = *(const f32x4 *)(p.dx_part + i * 4);
+#pragma unroll 4
+    for (int s = 1; s < p.S; ++s) v += *(const f32x4 *)(p.dx_part + s * plane + i * 4);
+    *(u32x2 *)((uint16_t *)p.da + i * 4) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const size_t at = first + threadIdx.x + 1024 * i;
-      if (at >= total) return;
-      float v = p.dx_part[at];
-      for (int s = 1; s < p.S; ++s) v += p.dx_part[s * plane + at];
-      ((float *)p.da)[at] = v;
-    }
+    if (i >= total) return;
+    float v = p.dx_part[i];
+#pragma unroll 8
+    for (int s = 1; s < p.S; ++s) v += p.dx_part[s * plane + i];
+    ((float *)p.da)[i] = v;
   }
 }
 
@@ -119,7 +113,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs &a, hipStream_t st) {
   p.da = a.da;
   p.bf16 = a.bf16;
   p.w_blocks = a.perm ? (a.R + 63) / 64 : 0;
-  const size_t sums = p.S > 1 ? ((size_t)a.R * a.d + 8191) / 8192 : 0;
+  const size_t sums = p.S > 1 ? ((size_t)a.R * a.d / (a.bf16 ? 4 : 1) + 1023) / 1024 : 0;
   if (p.w_blocks + sums == 0) return hipSuccess;
   ffn_grad_finish_kernel<<<(unsigned)(p.w_blocks + sums), 1024, 0, st>>>(p);
   return hipGetLastError();

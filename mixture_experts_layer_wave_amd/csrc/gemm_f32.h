@@ -7,7 +7,7 @@
 // a thread fetches four consecutive elements at a time, two steps ahead
 // (these products are small, so the trip to memory is most of a step).  A
 // 16-byte fetch needs 4-byte alignment only, so every size and layout takes
-// it; pieces cut by an edge are read element by element, zero outside.
+// it.
 //
 // A sum over K is taken in runs of 256, each from zero, added to a total:
 // the error of a long sum then grows with the runs, not with K.
@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "gemm_common.h"
 
 namespace moe {
 namespace f32gemm {
@@ -25,23 +26,21 @@ constexpr int kFour = kT * kK / 4 / kThreads;  // pieces a thread fetches per op
 constexpr int kStage = 2 * kK * kPitch;        // floats of both tiles of a stage
 constexpr int kSmem = 2 * kStage;
 
-typedef f32x4 f32x4_any __attribute__((aligned(4)));
-
-// Four consecutive elements, of which the first `n` (<= 0: none, >= 4: all)
-// are inside the operand.
+// Four consecutive elements at byte offset `off` of a buffer, of which the
+// first `n` (<= 0: none, >= 4: all) belong to the operand.  Dwords past the
+// buffer's record count read as zero one by one; elements past n (the next
+// row's) are replaced by zero.  No branch: the fetches in flight stay
+// countable.
 struct Piece {
-  const float *p;
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t off;
   int n;
 };
 __device__ __forceinline__ f32x4 fetch4(Piece q) {
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if (q.n >= 4) {
-    v = *(const f32x4_any *)q.p;
-  } else if (q.n > 0) {
+  f32x4 v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                          q.r, q.n > 0 ? q.off : gemm::kOOB, 0, 0));
 #pragma unroll
-    for (int j = 0; j < 3; ++j)
-      if (j < q.n) v[j] = q.p[j];
-  }
+  for (int j = 1; j < 4; ++j) v[j] = j < q.n ? v[j] : 0.f;
   return v;
 }
 
@@ -69,8 +68,7 @@ __device__ __forceinline__ void put(float *tile, int i, f32x4 v) {
 // total += sum over k < K of A(k, m) B(k, n): lane l of wave (wm, wn) holds
 // row m = 32 wm + l % 32 and columns n = 32 wn + (i / 4) 8 + (l / 32) 4 + i % 4.
 // fa(i, k, m) and fb(i, k, n) give the thread's piece i at tile row m or
-// column n; for K-major operands they are called with k < K only, else the
-// piece is cut at K here.  smem: kSmem floats.
+// column n; k may be past K (the piece is cut here).  smem: kSmem floats.
 template <bool A_KMAJ, bool B_KMAJ, typename FA, typename FB>
 __device__ __forceinline__ void product(f32x16 &total, float *smem, int K, FA fa, FB fb) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -79,11 +77,11 @@ __device__ __forceinline__ void product(f32x16 &total, float *smem, int K, FA fa
     constexpr bool KMAJ = decltype(kmaj)::value;
     int k, r;
     place<KMAJ>(i, k, r);
-    Piece q = {nullptr, 0};
-    if (k0 + k < K) {
-      q = f(i, k0 + k, r);
-      if (!KMAJ && q.n > 0) q.n = K - k0 - k;
-    }
+    Piece q = f(i, k0 + k, r);
+    if (KMAJ)
+      q.n = k0 + k < K ? q.n : 0;
+    else
+      q.n = q.n > 0 ? K - k0 - k : 0;
     return fetch4(q);
   };
   f32x4 ra[2][kFour], rb[2][kFour];

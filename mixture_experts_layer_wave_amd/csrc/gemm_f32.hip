@@ -19,12 +19,21 @@ struct F32Params {
   const float *a, *dy;
   const int32_t *perm, *inv, *offsets, *slot;
   const float *topk_w;
-  int n_slots, n, k, E, R, d, f, n_nt;
+  int n_slots, src_rows, k, E, R, d, f, n_nt;  // src_rows: rows of a and dy
   const float *w1, *w3, *w2, *g, *u;
   float *dg, *du, *hs, *part;  // gradient
   float *o0, *o1, *o2, *o3;    // up: h, g, u; gradient: da's planes, dW1, dW3, dW2
   int splits;                  // da's planes
 };
+
+// A row-major matrix as a buffer (under 2^31 bytes, checked on the host), and
+// the byte offset of an element.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t f32_rsrc(const float *p, int rows, int cols) {
+  return gemm::rsrc(p, (uint32_t)rows * (uint32_t)cols * 4u);
+}
+__device__ __forceinline__ uint32_t at(int row, int cols, int col) {
+  return ((uint32_t)row * (uint32_t)cols + (uint32_t)col) * 4u;
+}
 
 __device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + expf(-g)); }
 
@@ -57,9 +66,11 @@ __global__ __launch_bounds__(kThreads) void up_save_f32_kernel(F32Params p) {
   const size_t mat = (size_t)phys_slot(p.slot, p.n_slots, s_t.e) * p.f * p.d;
   int src[kFour];
   source_rows(src, p.perm, row0, rows);
-  auto fa = [&](int i, int k, int) { return Piece{p.a + (size_t)src[i] * p.d + k, src[i] >= 0 ? 4 : 0}; };
+  const auto ra = f32_rsrc(p.a, p.src_rows, p.d);
+  auto fa = [&](int i, int k, int) { return Piece{ra, at(src[i], p.d, k), src[i] >= 0 ? 4 : 0}; };
   auto weights = [&](const float *w) {
-    return [=](int, int k, int c) { return Piece{w + mat + (size_t)(n0 + c) * p.d + k, n0 + c < p.f ? 4 : 0}; };
+    const auto rw = f32_rsrc(w + mat, p.f, p.d);
+    return [=](int, int k, int c) { return Piece{rw, at(n0 + c, p.d, k), n0 + c < p.f ? 4 : 0}; };
   };
   f32x16 ga = {}, ua = {};
   product<false, false>(ga, smem, p.d, fa, weights(p.w1));
@@ -69,10 +80,10 @@ __global__ __launch_bounds__(kThreads) void up_save_f32_kernel(F32Params p) {
   for (int i = 0; i < 16; ++i) {
     const int c = n0 + out_col(i);
     if (r < rows && c < p.f) {
-      const size_t at = (size_t)(row0 + r) * p.f + c;
-      p.o1[at] = ga[i];
-      p.o2[at] = ua[i];
-      p.o0[at] = ga[i] * sigmoid_f32(ga[i]) * ua[i];
+      const size_t o = (size_t)(row0 + r) * p.f + c;
+      p.o1[o] = ga[i];
+      p.o2[o] = ua[i];
+      p.o0[o] = ga[i] * sigmoid_f32(ga[i]) * ua[i];
     }
   }
 }
@@ -87,11 +98,11 @@ __global__ __launch_bounds__(kThreads) void dh_f32_kernel(F32Params p) {
   const float *w2 = p.w2 + (size_t)phys_slot(p.slot, p.n_slots, s_t.e) * p.d * p.f;
   int src[kFour];
   source_rows(src, p.perm, row0, rows);
+  const auto ra = f32_rsrc(p.dy, p.src_rows, p.d), rw = f32_rsrc(w2, p.d, p.f);
   f32x16 acc = {};
   product<false, true>(
-      acc, smem, p.d,
-      [&](int i, int k, int) { return Piece{p.dy + (size_t)src[i] * p.d + k, src[i] >= 0 ? 4 : 0}; },
-      [&](int, int k, int c) { return Piece{w2 + (size_t)k * p.f + n0 + c, p.f - n0 - c}; });
+      acc, smem, p.d, [&](int i, int k, int) { return Piece{ra, at(src[i], p.d, k), src[i] >= 0 ? 4 : 0}; },
+      [&](int, int k, int c) { return Piece{rw, at(k, p.f, n0 + c), p.f - n0 - c}; });
   const int r = out_row();
   float wr = 1.f, sum = 0.f;
   if (p.perm && r < rows) {
@@ -104,13 +115,13 @@ __global__ __launch_bounds__(kThreads) void dh_f32_kernel(F32Params p) {
   for (int i = 0; i < 16; ++i) {
     const int c = n0 + out_col(i);
     if (r < rows && c < p.f) {
-      const size_t at = (size_t)(row0 + r) * p.f + c;
-      const float g = p.g[at], u = p.u[at], s = sigmoid_f32(g), a = g * s, h = a * u;
+      const size_t o = (size_t)(row0 + r) * p.f + c;
+      const float g = p.g[o], u = p.u[o], s = sigmoid_f32(g), a = g * s, h = a * u;
       sum = fmaf(acc[i], h, sum);
       const float dh = acc[i] * wr;
-      p.dg[at] = dh * u * fmaf(a, 1.0f - s, s);
-      p.du[at] = dh * a;
-      p.hs[at] = wr * h;
+      p.dg[o] = dh * u * fmaf(a, 1.0f - s, s);
+      p.du[o] = dh * a;
+      p.hs[o] = wr * h;
     }
   }
   sum += __shfl_xor(sum, 32, 64);
@@ -127,13 +138,12 @@ __device__ __forceinline__ void dx_tile(const F32Params &p, int block, float *sm
   const int half = s_t.split & 1, S = p.splits / 2, steps = (p.f + kK - 1) / kK;
   const int k0 = (int)((long long)(s_t.split / 2) * steps / S) * kK;
   const int k1 = min(p.f, (int)((long long)(s_t.split / 2 + 1) * steps / S) * kK);
-  const float *dz = (half ? p.du : p.dg) + (size_t)row0 * p.f + k0;
-  const float *w = (half ? p.w3 : p.w1) + mat + (size_t)k0 * p.d;
+  const auto rz = f32_rsrc((half ? p.du : p.dg) + (size_t)row0 * p.f, rows, p.f);
+  const auto rw = f32_rsrc((half ? p.w3 : p.w1) + mat, p.f, p.d);
   f32x16 acc = {};
   product<false, true>(
-      acc, smem, k1 - k0,
-      [&](int, int k, int m) { return Piece{dz + (size_t)m * p.f + k, m < rows ? 4 : 0}; },
-      [&](int, int k, int c) { return Piece{w + (size_t)k * p.d + n0 + c, p.d - n0 - c}; });
+      acc, smem, k1 - k0, [&](int, int k, int m) { return Piece{rz, at(m, p.f, k0 + k), m < rows ? 4 : 0}; },
+      [&](int, int k, int c) { return Piece{rw, at(k0 + k, p.d, n0 + c), p.d - n0 - c}; });
   float *out = p.o0 + ((size_t)s_t.split * p.R + row0) * p.d;
   const int r = out_row();
 #pragma unroll
@@ -143,27 +153,39 @@ __device__ __forceinline__ void dx_tile(const F32Params &p, int block, float *sm
   }
 }
 
+constexpr int kTokens = 1024;
+
 // Weight gradients: dW1 and dW3 (f x d; row tiles of dW1, then of dW3), or
 // dW2 (d x f).  Blocks run over an expert's column tiles, then its row tiles.
 template <bool W2>
-__device__ __forceinline__ void dw_tile(const F32Params &p, int block, float *smem) {
+__device__ __forceinline__ void dw_tile(const F32Params &p, int block, float *smem, int32_t *s_tok) {
   const int M = W2 ? p.d : p.f, N = W2 ? p.f : p.d, mt = (M + kT - 1) / kT, nt = (N + kT - 1) / kT;
   const int per = (W2 ? mt : 2 * mt) * nt, e = block / per, tile = block % per;
   const int n0 = tile % nt * kT;
   const bool second = !W2 && tile / nt >= mt;
   const int m0 = (tile / nt - (second ? mt : 0)) * kT;
   const int row0 = p.offsets[e], rows = p.offsets[e + 1] - row0;
-  const float *dz = second ? p.du : p.dg;
-  auto token = [&](int k) { return (size_t)(p.perm ? p.perm[row0 + k] : row0 + k); };
   f32x16 acc = {};
-  product<true, true>(
-      acc, smem, rows,
-      [&](int, int k, int m) {
-        return Piece{(W2 ? p.dy + token(k) * p.d : dz + (size_t)(row0 + k) * p.f) + m0 + m, M - m0 - m};
-      },
-      [&](int, int k, int c) {
-        return Piece{(W2 ? p.hs + (size_t)(row0 + k) * p.f : p.a + token(k) * p.d) + n0 + c, N - n0 - c};
-      });
+  // 1024 of the pile's rows at a time, their tokens in LDS (a fetch that
+  // waited for a token from memory would drain the fetches before it); an
+  // empty pile's weight gradients are zeros.
+  for (int q0 = 0; q0 < rows; q0 += kTokens) {
+    const int q = min(kTokens, rows - q0), first = row0 + q0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < q; i += kThreads) s_tok[i] = p.perm ? p.perm[first + i] : first + i;
+    __syncthreads();
+    const auto rf = f32_rsrc((W2 ? p.hs : second ? p.du : p.dg) + (size_t)first * p.f, q, p.f);
+    const auto rd = f32_rsrc(W2 ? p.dy : p.a, p.src_rows, p.d);
+    auto token = [&](int k) { return s_tok[min(k, q - 1)]; };
+    product<true, true>(
+        acc, smem, q,
+        [&](int, int k, int m) {
+          return W2 ? Piece{rd, at(token(k), p.d, m0 + m), M - m0 - m} : Piece{rf, at(k, p.f, m0 + m), M - m0 - m};
+        },
+        [&](int, int k, int c) {
+          return W2 ? Piece{rf, at(k, p.f, n0 + c), N - n0 - c} : Piece{rd, at(token(k), p.d, n0 + c), N - n0 - c};
+        });
+  }
   float *out = (W2 ? p.o3 : second ? p.o2 : p.o1) + (size_t)e * M * N;
   const int r = m0 + out_row();
 #pragma unroll
@@ -177,14 +199,15 @@ __device__ __forceinline__ void dw_tile(const F32Params &p, int block, float *sm
 // dW3, then dW2.
 __global__ __launch_bounds__(kThreads) void rest_f32_kernel(F32Params p, int end_dx, int end_dw13) {
   __shared__ float smem[kSmem];
+  __shared__ int32_t s_tok[kTokens];
   __shared__ TileSlot s_t;
   const int b = blockIdx.x;
   if (b < end_dx)
     dx_tile(p, b, smem, s_t);
   else if (b < end_dw13)
-    dw_tile<false>(p, b - end_dx, smem);
+    dw_tile<false>(p, b - end_dx, smem, s_tok);
   else
-    dw_tile<true>(p, b - end_dw13, smem);
+    dw_tile<true>(p, b - end_dw13, smem, s_tok);
 }
 
 int row_tiles(int R, int E) { return (R + kT - 1) / kT + (E < R ? E : R); }
@@ -203,6 +226,7 @@ GradPlan grad_plan_f32(const FfnGradArgs &a) {
 hipError_t launch_up_save_f32(const FfnArgs &a, void *g, void *u, hipStream_t st) {
   F32Params p{};
   p.a = (const float *)a.a;
+  p.src_rows = a.perm ? a.n : a.R;
   p.perm = a.perm;
   p.offsets = a.offsets;
   p.slot = a.slot;
@@ -224,6 +248,7 @@ hipError_t launch_up_save_f32(const FfnArgs &a, void *g, void *u, hipStream_t st
 hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t st) {
   F32Params p{};
   p.a = (const float *)a.a;
+  p.src_rows = a.perm ? a.n : a.R;
   p.dy = (const float *)a.dy;
   p.perm = a.perm;
   p.inv = a.inv;
@@ -231,7 +256,6 @@ hipError_t launch_grad_f32(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t
   p.offsets = a.offsets;
   p.slot = a.slot;
   p.n_slots = a.n_slots;
-  p.n = a.n;
   p.k = a.k;
   p.E = a.E;
   p.R = a.R;

@@ -290,10 +290,13 @@ __global__ __launch_bounds__(kThreads) void router_dx_f32_kernel(
     const int32_t *__restrict__ inv, int n, int d, int E, int k, float *__restrict__ dx) {
   __shared__ float smem[kSmem];
   const int t0 = blockIdx.x * kT, c0 = blockIdx.y * kT;
+  const auto rz = gemm::rsrc(dz + (size_t)t0 * E, (uint32_t)min(kT, n - t0) * (uint32_t)E * 4u);
+  const auto rw = gemm::rsrc(wg, (uint32_t)E * (uint32_t)d * 4u);
   f32x16 acc = {};
   product<false, true>(
-      acc, smem, E, [&](int, int e, int t) { return Piece{dz + (size_t)(t0 + t) * E + e, t0 + t < n ? 4 : 0}; },
-      [&](int, int e, int c) { return Piece{wg + (size_t)e * d + c0 + c, d - c0 - c}; });
+      acc, smem, E,
+      [&](int, int e, int t) { return Piece{rz, ((uint32_t)t * E + e) * 4u, t0 + t < n ? 4 : 0}; },
+      [&](int, int e, int c) { return Piece{rw, ((uint32_t)e * d + c0 + c) * 4u, d - c0 - c}; });
   const int t = t0 + out_row();
   const unsigned R = (unsigned)n * (unsigned)k;
   if (t >= n) return;
@@ -322,11 +325,13 @@ __global__ __launch_bounds__(kThreads) void router_dw_f32_kernel(const float *__
   __shared__ float s_b[kThreads];
   const int c0 = blockIdx.x * kT, e0 = blockIdx.z * kT;
   const int tb = blockIdx.y * range, te = min(n, tb + range);
+  const auto rz = gemm::rsrc(dz + (size_t)tb * E, (uint32_t)(te - tb) * (uint32_t)E * 4u);
+  const auto rx = gemm::rsrc(x + (size_t)tb * d, (uint32_t)(te - tb) * (uint32_t)d * 4u);
   f32x16 acc = {};
   product<true, true>(
       acc, smem, te - tb,
-      [&](int, int t, int e) { return Piece{dz + (size_t)(tb + t) * E + e0 + e, E - e0 - e}; },
-      [&](int, int t, int c) { return Piece{x + (size_t)(tb + t) * d + c0 + c, d - c0 - c}; });
+      [&](int, int t, int e) { return Piece{rz, ((uint32_t)t * E + e0 + e) * 4u, E - e0 - e}; },
+      [&](int, int t, int c) { return Piece{rx, ((uint32_t)t * d + c0 + c) * 4u, d - c0 - c}; });
   const int e = e0 + out_row();
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -347,7 +352,8 @@ __global__ __launch_bounds__(kThreads) void router_dw_f32_kernel(const float *__
 }
 
 // Token ranges of the dW_g product: about two blocks per CU, but planes of
-// at most the bytes of x (S E 4 <= n 2), and whole steps.
+// at most the bytes of x (S E 4 <= n 2), and whole steps; a range's rows of x
+// and dz stay under 2^30 bytes (32-bit buffer offsets).
 struct Ranges {
   int S, range;
 };
@@ -356,6 +362,8 @@ Ranges dw_ranges(int n, int d, int E) {
   int S = (512 + tiles - 1) / tiles;
   const int most = n / (2 * E) > 1 ? n / (2 * E) : 1;
   if (S > most) S = most;
+  const long long bytes = (long long)n * (d > E ? d : E) * 4;
+  if (S < (bytes >> 29)) S = (int)(bytes >> 29);
   int range = (n + S - 1) / S;
   range = (range + kWT - 1) / kWT * kWT;
   return {(n + range - 1) / range, range};

@@ -5,6 +5,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "api_internal.h"
 #include "gemm_grad.h"
 #include "kernels.h"
@@ -28,7 +30,12 @@ int check_ffn_shape(const moe_shape *s, int act, int wdt) {
   if (wdt != MOE_F32 && wdt != MOE_BF16) return MOE_ERR_DTYPE;
   st = check_dtypes(s, act, wdt);
   if (st != MOE_OK) return st;
-  return s->d < (1 << 20) && s->d_ff < (1 << 20) ? MOE_OK : MOE_ERR_SHAPE;
+  if (s->d >= (1 << 20) || s->d_ff >= (1 << 20)) return MOE_ERR_SHAPE;
+  // 32-bit byte offsets, as check_dtypes asks of bf16
+  const long long R = (long long)s->n * s->k, bytes = wdt == MOE_F32 ? 4 : 2;
+  if (R * std::max(s->d, s->d_ff) * bytes >= (1ll << 31) || (long long)s->d * s->d_ff * bytes >= (1ll << 31))
+    return MOE_ERR_SHAPE;
+  return MOE_OK;
 }
 
 int check_ffn(const moe_shape *s, int act, const moe_expert_weights *w) {
@@ -52,7 +59,8 @@ FfnGradArgs grad_args(const moe_shape *s, int wdt) {
 int check_router(const moe_shape *s) {
   const int st = check_shape(s);
   if (st != MOE_OK) return st;
-  return s->n < (1 << 24) && s->d < (1 << 20) ? MOE_OK : MOE_ERR_SHAPE;
+  if (s->n >= (1 << 24) || s->d >= (1 << 20) || (long long)s->E * s->d >= (1ll << 29)) return MOE_ERR_SHAPE;
+  return MOE_OK;
 }
 
 }  // namespace

@@ -85,6 +85,7 @@ def test_ffn_training_refuses_shapes_and_types(call):
     assert call(shape=(4, 1 << 20, 4, 2, 64)) == -2 and call(shape=(4, 64, 4, 2, 1 << 20), act=F32) == -2
     # bf16 operands are addressed with 32-bit offsets, as in the forward pass
     assert call(shape=(65536, 4096, 8, 2, 14336)) == -2
+    assert call(shape=(32768, 4096, 8, 2, 8192), act=F32) == -2 and call(shape=(4, 32768, 4, 2, 16384), act=F32) == -2
     assert call(act=MXFP8) == -3 and call(act=MXFP4) == -3
     assert call(act=F32, w=_weights(BF16)) == -3 and call(act=BF16, w=_weights(F32)) == -3
     # MXFP4 weights are not trained
@@ -130,6 +131,7 @@ def _router(shape=(4, 64, 4, 2, 64), act=BF16, nb=1 << 40, **kw):
 def test_router_backward_refusals():
     assert _router(shape=None) == -1
     assert _router(shape=(4, 64, 4, 5, 64)) == -2 and _router(shape=(1 << 24, 64, 4, 1, 64)) == -2
+    assert _router(shape=(4, 1 << 19, 1024, 2, 64)) == -2
     assert _router(shape=(4, 1 << 20, 4, 2, 64)) == -2 and _router(shape=(4, 60, 4, 2, 64)) == -2
     assert _router(act=MXFP4) == -3 and _router(act=MXFP8) == -3
     for name in ("z", "idx", "w", "dw", "x", "wg", "dz", "dx", "dwg", "da", "inv"):
