@@ -1,16 +1,19 @@
 // A float32 product tile on the matrix cores, shared by the float32 kernels
 // of the training operators (gemm_f32.hip, router_grad.hip).
 //
-// Block of 256 threads (4 waves, 2 x 2), output tile 64 x 64 (each wave
-// 32 x 32 on v_mfma_f32_32x32x2_f32), K steps of 32.  Both operands lie in
-// LDS K row by K row, 65 floats apart, in two stages with one barrier a step;
-// a thread fetches four consecutive elements at a time, two steps ahead
-// (these products are small, so the trip to memory is most of a step).  A
-// 16-byte fetch needs 4-byte alignment only, so every size and layout takes
-// it.
+// Block of 512 threads: two groups of 4 waves (2 x 2, each 32 x 32 on
+// v_mfma_f32_32x32x2_f32) compute the same 64 x 64 output tile over the even
+// and the odd K steps of 32, so that a small grid still has two waves per
+// SIMD (one group's LDS and barrier waits lie under the other's products).
+// Both operands lie in LDS K row by K row, 66 floats apart: the stores of
+// operands contiguous along K (8 pieces of four K, 8 rows) and the fragment
+// reads (32 rows of K rows k and k + 16) meet 64 different banks.  Two stages
+// a group, one barrier a step; a thread fetches four consecutive elements at
+// a time, two steps ahead.  A 16-byte fetch needs 4-byte alignment only, so
+// every size and layout takes it.
 //
-// A sum over K is taken in runs of 256, each from zero, added to a total:
-// the error of a long sum then grows with the runs, not with K.
+// A sum over K is taken in runs of eight steps, each from zero, added to a
+// total: the error of a long sum then grows with the runs, not with K.
 #pragma once
 
 #include <type_traits>
@@ -21,10 +24,12 @@
 namespace moe {
 namespace f32gemm {
 
-constexpr int kT = 64, kK = 32, kPitch = kT + 1, kThreads = 256;
-constexpr int kFour = kT * kK / 4 / kThreads;  // pieces a thread fetches per operand and step
+constexpr int kT = 64, kK = 32, kPitch = kT + 2, kThreads = 512;
+constexpr int kFour = kT * kK / 4 / 256;       // pieces a thread fetches per operand and step
 constexpr int kStage = 2 * kK * kPitch;        // floats of both tiles of a stage
-constexpr int kSmem = 2 * kStage;
+constexpr int kSmem = 4 * kStage;              // two groups, two stages
+constexpr int kOutPitch = kT + 4;
+constexpr int kLines = kT * kT / 4 / kThreads;  // pieces of the result a thread holds
 
 // Four consecutive elements at byte offset `off` of a buffer, of which the
 // first `n` (<= 0: none, >= 4: all) belong to the operand.  Dwords past the
@@ -43,12 +48,24 @@ __device__ __forceinline__ f32x4 fetch4(Piece q) {
   for (int j = 1; j < 4; ++j) v[j] = j < q.n ? v[j] : 0.f;
   return v;
 }
+// The first n of four elements to dst (4-byte aligned).
+__device__ __forceinline__ void store4(float *dst, int n, f32x4 v) {
+  typedef f32x4 f32x4_any __attribute__((aligned(4)));
+  if (n >= 4) {
+    *(f32x4_any *)dst = v;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (j < n) dst[j] = v[j];
+  }
+}
 
-// (k, row) of the first element of piece i of this thread in a step: pieces
-// run along the rows' index for K-major operands, along K otherwise.
+// (k, row) of the first element of piece i of this thread (of its group) in a
+// step: pieces run along the rows' index for K-major operands, along K
+// otherwise.
 template <bool KMAJ>
 __device__ __forceinline__ void place(int i, int &k, int &r) {
-  const int t = threadIdx.x;
+  const int t = threadIdx.x & 255;
   if constexpr (KMAJ) {
     r = (t & 15) * 4;
     k = (t >> 4) + i * 16;
@@ -65,13 +82,18 @@ __device__ __forceinline__ void put(float *tile, int i, f32x4 v) {
   for (int j = 0; j < 4; ++j) tile[KMAJ ? k * kPitch + r + j : (k + j) * kPitch + r] = v[j];
 }
 
-// total += sum over k < K of A(k, m) B(k, n): lane l of wave (wm, wn) holds
-// row m = 32 wm + l % 32 and columns n = 32 wn + (i / 4) 8 + (l / 32) 4 + i % 4.
-// fa(i, k, m) and fb(i, k, n) give the thread's piece i at tile row m or
-// column n; k may be past K (the piece is cut here).  smem: kSmem floats.
+// Row and first column (in the tile) of the result's piece i of this thread:
+// 16 lanes hold a row.
+__device__ __forceinline__ int line_row(int i) { return (threadIdx.x >> 4) + i * (kThreads / 16); }
+__device__ __forceinline__ int line_col() { return (threadIdx.x & 15) * 4; }
+
+// out += sum over k < K of A(k, m) B(k, n), as pieces of four columns
+// (line_row, line_col).  piece_a(i, k, m) and piece_b(i, k, n) give the
+// thread's piece i at tile row m or column n; k may be past K (the piece is
+// cut here).  smem: kSmem floats.  Every thread of the block calls it.
 template <bool A_KMAJ, bool B_KMAJ, typename FA, typename FB>
-__device__ __forceinline__ void product(f32x16 &total, float *smem, int K, FA fa, FB fb) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__device__ __forceinline__ void product(f32x4 (&out)[kLines], float *smem, int K, FA piece_a, FB piece_b) {
+  const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) & 3, kg = threadIdx.x >> 8;
   const int am = (wave >> 1) * 32 + (lane & 31), bn = (wave & 1) * 32 + (lane & 31), kh = lane >> 5;
   auto get = [&](auto kmaj, auto f, int i, int k0) {
     constexpr bool KMAJ = decltype(kmaj)::value;
@@ -85,33 +107,43 @@ __device__ __forceinline__ void product(f32x16 &total, float *smem, int K, FA fa
     return fetch4(q);
   };
   f32x4 ra[2][kFour], rb[2][kFour];
-  auto fetch = [&](f32x4 *a, f32x4 *b, int k0) {
+  // step s of this group
+  auto fetch = [&](f32x4 *a, f32x4 *b, int s) {
+    const int k0 = (2 * s + kg) * kK;
 #pragma unroll
     for (int i = 0; i < kFour; ++i) {
-      a[i] = get(std::integral_constant<bool, A_KMAJ>{}, fa, i, k0);
-      b[i] = get(std::integral_constant<bool, B_KMAJ>{}, fb, i, k0);
+      a[i] = get(std::integral_constant<bool, A_KMAJ>{}, piece_a, i, k0);
+      b[i] = get(std::integral_constant<bool, B_KMAJ>{}, piece_b, i, k0);
     }
   };
-  f32x16 acc = {};
-  const int steps = (K + kK - 1) / kK;
+  f32x16 acc = {}, total = {};
+  const int steps = (K + 2 * kK - 1) / (2 * kK);  // of either group
   fetch(ra[0], rb[0], 0);
-  fetch(ra[1], rb[1], kK);
+  fetch(ra[1], rb[1], 1);
   __syncthreads();  // smem's readers before this call are done
   auto step = [&](int s, auto odd) {
     constexpr int P = decltype(odd)::value;
     // (stage P was last read in step s - 2, before the barrier of s - 1)
-    float *sa = smem + P * kStage, *sb = sa + kK * kPitch;
+    float *sa = smem + (2 * kg + P) * kStage, *sb = sa + kK * kPitch;
 #pragma unroll
     for (int i = 0; i < kFour; ++i) {
       put<A_KMAJ>(sa, i, ra[P][i]);
       put<B_KMAJ>(sb, i, rb[P][i]);
     }
-    fetch(ra[P], rb[P], (s + 2) * kK);
+    fetch(ra[P], rb[P], s + 2);
     __syncthreads();
+    // all of the step's fragments first, so that the products wait for the
+    // first of them only
+    float fa[kK / 2], fb[kK / 2];
 #pragma unroll
-    for (int k = 0; k < kK; k += 2)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(sb[(k + kh) * kPitch + bn], sa[(k + kh) * kPitch + am],
-                                                 acc, 0, 0, 0);
+    for (int k = 0; k < kK / 2; ++k) {
+      fa[k] = sa[(k + 16 * kh) * kPitch + am];
+      fb[k] = sb[(k + 16 * kh) * kPitch + bn];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < kK / 2; ++k)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[k], fa[k], acc, 0, 0, 0);
     if ((s & 7) == 7) {
       total += acc;
       acc = f32x16{};
@@ -122,15 +154,23 @@ __device__ __forceinline__ void product(f32x16 &total, float *smem, int K, FA fa
     if (s + 1 < steps) step(s + 1, std::integral_constant<int, 1>{});
   }
   total += acc;
-}
-
-// Tile-relative row and column of accumulator element i.
-__device__ __forceinline__ int out_row() {
-  return ((threadIdx.x >> 6) >> 1) * 32 + (threadIdx.x & 31);
-}
-__device__ __forceinline__ int out_col(int i) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  return (wave & 1) * 32 + (i >> 2) * 8 + (lane >> 5) * 4 + (i & 3);
+  // Lane l of wave (wm, wn) holds row 32 wm + l % 32 and columns 32 wn +
+  // 8 g + 4 (l / 32) + 0 .. 3: the even steps' sums, then the odd steps'.
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    __syncthreads();
+    if (kg == half)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float *q = smem + am * kOutPitch + (wave & 1) * 32 + g * 8 + kh * 4;
+        f32x4 v = {total[g * 4], total[g * 4 + 1], total[g * 4 + 2], total[g * 4 + 3]};
+        if (half) v += *(const f32x4 *)q;
+        *(f32x4 *)q = v;
+      }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kLines; ++i) out[i] += *(const f32x4 *)(smem + line_row(i) * kOutPitch + line_col());
 }
 
 }  // namespace f32gemm

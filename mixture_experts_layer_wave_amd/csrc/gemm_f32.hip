@@ -8,6 +8,7 @@
 #include "gemm_f32.h"
 #include "gemm_grad.h"
 #include "kernels.h"
+#include "route_dev.h"
 
 namespace moe {
 namespace {
@@ -58,8 +59,8 @@ __device__ __forceinline__ void source_rows(int (&src)[kFour], const int32_t *pe
 }
 
 // g = a W1^T, u = a W3^T, h = silu(g) u.
-__global__ __launch_bounds__(kThreads) void up_save_f32_kernel(F32Params p) {
-  __shared__ float smem[kSmem];
+__global__ __launch_bounds__(kThreads, 4) void up_save_f32_kernel(F32Params p) {
+  __shared__ __attribute__((aligned(16))) float smem[kSmem];
   __shared__ TileSlot s_t;
   if (!row_tile(p, s_t, blockIdx.x, 1)) return;
   const int row0 = s_t.row0, rows = s_t.rows, n0 = s_t.nt * kT;
@@ -72,26 +73,27 @@ __global__ __launch_bounds__(kThreads) void up_save_f32_kernel(F32Params p) {
     const auto rw = f32_rsrc(w + mat, p.f, p.d);
     return [=](int, int k, int c) { return Piece{rw, at(n0 + c, p.d, k), n0 + c < p.f ? 4 : 0}; };
   };
-  f32x16 ga = {}, ua = {};
-  product<false, false>(ga, smem, p.d, fa, weights(p.w1));
-  product<false, false>(ua, smem, p.d, fa, weights(p.w3));
-  const int r = out_row();
+  f32x4 g[kLines] = {}, u[kLines] = {};
+  product<false, false>(g, smem, p.d, fa, weights(p.w1));
+  product<false, false>(u, smem, p.d, fa, weights(p.w3));
+  const int c = n0 + line_col();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = n0 + out_col(i);
-    if (r < rows && c < p.f) {
-      const size_t o = (size_t)(row0 + r) * p.f + c;
-      p.o1[o] = ga[i];
-      p.o2[o] = ua[i];
-      p.o0[o] = ga[i] * sigmoid_f32(ga[i]) * ua[i];
-    }
+  for (int i = 0; i < kLines; ++i) {
+    if (line_row(i) >= rows) continue;
+    const size_t o = (size_t)(row0 + line_row(i)) * p.f + c;
+    f32x4 h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = g[i][j] * sigmoid_f32(g[i][j]) * u[i][j];
+    store4(p.o0 + o, p.f - c, h);
+    store4(p.o1 + o, p.f - c, g[i]);
+    store4(p.o2 + o, p.f - c, u[i]);
   }
 }
 
-// dh0 = dy W2 and what follows from it; row sums of dh0 h over each wave's 32
-// columns go to part[plane][row].
-__global__ __launch_bounds__(kThreads) void dh_f32_kernel(F32Params p) {
-  __shared__ float smem[kSmem];
+// dh0 = dy W2 and what follows from it; row sums of dh0 h over the tile's 64
+// columns go to part[column tile][row].
+__global__ __launch_bounds__(kThreads, 4) void dh_f32_kernel(F32Params p) {
+  __shared__ __attribute__((aligned(16))) float smem[kSmem];
   __shared__ TileSlot s_t;
   if (!row_tile(p, s_t, blockIdx.x, 1)) return;
   const int row0 = s_t.row0, rows = s_t.rows, n0 = s_t.nt * kT;
@@ -99,34 +101,49 @@ __global__ __launch_bounds__(kThreads) void dh_f32_kernel(F32Params p) {
   int src[kFour];
   source_rows(src, p.perm, row0, rows);
   const auto ra = f32_rsrc(p.dy, p.src_rows, p.d), rw = f32_rsrc(w2, p.d, p.f);
-  f32x16 acc = {};
+  f32x4 acc[kLines] = {};
   product<false, true>(
       acc, smem, p.d, [&](int i, int k, int) { return Piece{ra, at(src[i], p.d, k), src[i] >= 0 ? 4 : 0}; },
       [&](int, int k, int c) { return Piece{rw, at(k, p.f, n0 + c), p.f - n0 - c}; });
-  const int r = out_row();
-  float wr = 1.f, sum = 0.f;
-  if (p.perm && r < rows) {
-    const int t = p.perm[row0 + r];
-    wr = 0.f;
-    for (int j = 0; j < p.k; ++j)
-      if (p.inv[(size_t)t * p.k + j] == row0 + r) wr = p.topk_w[(size_t)t * p.k + j];
-  }
+  const int c = n0 + line_col();
+  const size_t base = (size_t)row0 * p.f;
+  const auto rg = f32_rsrc(p.g + base, rows, p.f), ru = f32_rsrc(p.u + base, rows, p.f);
+  f32x4 g[kLines], u[kLines];
+  float wr[kLines];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = n0 + out_col(i);
-    if (r < rows && c < p.f) {
-      const size_t o = (size_t)(row0 + r) * p.f + c;
-      const float g = p.g[o], u = p.u[o], s = sigmoid_f32(g), a = g * s, h = a * u;
-      sum = fmaf(acc[i], h, sum);
-      const float dh = acc[i] * wr;
-      p.dg[o] = dh * u * fmaf(a, 1.0f - s, s);
-      p.du[o] = dh * a;
-      p.hs[o] = wr * h;
+  for (int i = 0; i < kLines; ++i) {
+    const int r = line_row(i), n = r < rows ? p.f - c : 0;
+    g[i] = fetch4(Piece{rg, at(r, p.f, c), n});
+    u[i] = fetch4(Piece{ru, at(r, p.f, c), n});
+    wr[i] = 1.f;  // combine weight of the row
+    if (p.perm && r < rows) {
+      const int t = p.perm[row0 + r];
+      wr[i] = 0.f;
+      for (int j = 0; j < p.k; ++j)
+        if (p.inv[(size_t)t * p.k + j] == row0 + r) wr[i] = p.topk_w[(size_t)t * p.k + j];
     }
   }
-  sum += __shfl_xor(sum, 32, 64);
-  const int plane = s_t.nt * 2 + ((threadIdx.x >> 6) & 1);
-  if (p.perm && (threadIdx.x & 63) < 32 && r < rows) p.part[(size_t)plane * p.R + row0 + r] = sum;
+#pragma unroll
+  for (int i = 0; i < kLines; ++i) {
+    const int r = line_row(i);
+    f32x4 dg, du, hs;
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float s = sigmoid_f32(g[i][j]), a = g[i][j] * s, h = a * u[i][j], dh = acc[i][j] * wr[i];
+      sum = fmaf(acc[i][j], h, sum);
+      dg[j] = dh * u[i][j] * fmaf(a, 1.0f - s, s);
+      du[j] = dh * a;
+      hs[j] = wr[i] * h;
+    }
+    sum = group_sum(sum, 16);
+    if (r >= rows) continue;
+    const size_t o = base + (size_t)r * p.f + c;
+    store4(p.dg + o, p.f - c, dg);
+    store4(p.du + o, p.f - c, du);
+    store4(p.hs + o, p.f - c, hs);
+    if (p.perm && (threadIdx.x & 15) == 0) p.part[(size_t)s_t.nt * p.R + row0 + r] = sum;
+  }
 }
 
 // One K range of da = dg W1 + du W3: split 2 s + h of 2 S is range s of half
@@ -140,17 +157,15 @@ __device__ __forceinline__ void dx_tile(const F32Params &p, int block, float *sm
   const int k1 = min(p.f, (int)((long long)(s_t.split / 2 + 1) * steps / S) * kK);
   const auto rz = f32_rsrc((half ? p.du : p.dg) + (size_t)row0 * p.f, rows, p.f);
   const auto rw = f32_rsrc((half ? p.w3 : p.w1) + mat, p.f, p.d);
-  f32x16 acc = {};
+  f32x4 acc[kLines] = {};
   product<false, true>(
       acc, smem, k1 - k0, [&](int, int k, int m) { return Piece{rz, at(m, p.f, k0 + k), m < rows ? 4 : 0}; },
       [&](int, int k, int c) { return Piece{rw, at(k0 + k, p.d, n0 + c), p.d - n0 - c}; });
   float *out = p.o0 + ((size_t)s_t.split * p.R + row0) * p.d;
-  const int r = out_row();
+  const int c = n0 + line_col();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = n0 + out_col(i);
-    if (r < rows && c < p.d) out[(size_t)r * p.d + c] = acc[i];
-  }
+  for (int i = 0; i < kLines; ++i)
+    if (line_row(i) < rows) store4(out + (size_t)line_row(i) * p.d + c, p.d - c, acc[i]);
 }
 
 constexpr int kTokens = 1024;
@@ -165,7 +180,7 @@ __device__ __forceinline__ void dw_tile(const F32Params &p, int block, float *sm
   const bool second = !W2 && tile / nt >= mt;
   const int m0 = (tile / nt - (second ? mt : 0)) * kT;
   const int row0 = p.offsets[e], rows = p.offsets[e + 1] - row0;
-  f32x16 acc = {};
+  f32x4 acc[kLines] = {};
   // 1024 of the pile's rows at a time, their tokens in LDS (a fetch that
   // waited for a token from memory would drain the fetches before it); an
   // empty pile's weight gradients are zeros.
@@ -187,18 +202,18 @@ __device__ __forceinline__ void dw_tile(const F32Params &p, int block, float *sm
         });
   }
   float *out = (W2 ? p.o3 : second ? p.o2 : p.o1) + (size_t)e * M * N;
-  const int r = m0 + out_row();
+  const int c = n0 + line_col();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = n0 + out_col(i);
-    if (r < M && c < N) out[(size_t)r * N + c] = acc[i];
+  for (int i = 0; i < kLines; ++i) {
+    const int r = m0 + line_row(i);
+    if (r < M) store4(out + (size_t)r * N + c, N - c, acc[i]);
   }
 }
 
 // Everything that waits for dg, du and w h, in one grid: da, then dW1 and
 // dW3, then dW2.
-__global__ __launch_bounds__(kThreads) void rest_f32_kernel(F32Params p, int end_dx, int end_dw13) {
-  __shared__ float smem[kSmem];
+__global__ __launch_bounds__(kThreads, 4) void rest_f32_kernel(F32Params p, int end_dx, int end_dw13) {
+  __shared__ __attribute__((aligned(16))) float smem[kSmem];
   __shared__ int32_t s_tok[kTokens];
   __shared__ TileSlot s_t;
   const int b = blockIdx.x;
@@ -215,12 +230,12 @@ int row_tiles(int R, int E) { return (R + kT - 1) / kT + (E < R ? E : R); }
 }  // namespace
 
 // da's K ranges, two at least (one for each of its two products), more until
-// its blocks fill the chip four to a CU, each range 128 deep at least.
+// its blocks fill the chip two to a CU, each range 128 deep at least.
 GradPlan grad_plan_f32(const FfnGradArgs &a) {
   const int blocks = row_tiles(a.R, a.E) * ((a.d + kT - 1) / kT) * 2;
-  int S = blocks < 1024 ? 1024 / blocks : 1;
+  int S = blocks < 512 ? 512 / blocks : 1;
   if (S > a.d_ff / 128) S = a.d_ff / 128;
-  return {(a.d_ff + kT - 1) / kT * 2, 2 * (S < 1 ? 1 : S)};
+  return {(a.d_ff + kT - 1) / kT, 2 * (S < 1 ? 1 : S)};
 }
 
 hipError_t launch_up_save_f32(const FfnArgs &a, void *g, void *u, hipStream_t st) {

@@ -285,69 +285,69 @@ __global__ __launch_bounds__(256) void router_sum_kernel(const float *__restrict
 // ---- float32 ----------------------------------------------------------------------
 using namespace f32gemm;
 
-__global__ __launch_bounds__(kThreads) void router_dx_f32_kernel(
+__global__ __launch_bounds__(kThreads, 4) void router_dx_f32_kernel(
     const float *__restrict__ dz, const float *__restrict__ wg, const float *__restrict__ da,
     const int32_t *__restrict__ inv, int n, int d, int E, int k, float *__restrict__ dx) {
-  __shared__ float smem[kSmem];
+  __shared__ __attribute__((aligned(16))) float smem[kSmem];
   const int t0 = blockIdx.x * kT, c0 = blockIdx.y * kT;
   const auto rz = gemm::rsrc(dz + (size_t)t0 * E, (uint32_t)min(kT, n - t0) * (uint32_t)E * 4u);
   const auto rw = gemm::rsrc(wg, (uint32_t)E * (uint32_t)d * 4u);
-  f32x16 acc = {};
+  f32x4 acc[kLines] = {};
   product<false, true>(
       acc, smem, E,
       [&](int, int e, int t) { return Piece{rz, ((uint32_t)t * E + e) * 4u, t0 + t < n ? 4 : 0}; },
       [&](int, int e, int c) { return Piece{rw, ((uint32_t)e * d + c0 + c) * 4u, d - c0 - c}; });
-  const int t = t0 + out_row();
   const unsigned R = (unsigned)n * (unsigned)k;
-  if (t >= n) return;
-  if (da)
-    for (int j = 0; j < k; ++j) {
-      const int pr = inv[(size_t)t * k + j];
-      if ((unsigned)pr >= R) continue;
+  const int c = c0 + line_col();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int c = c0 + out_col(i);
-        if (c < d) acc[i] += da[(size_t)pr * d + c];
+  for (int i = 0; i < kLines; ++i) {
+    const int t = t0 + line_row(i);
+    if (t >= n) continue;
+    if (da)
+      for (int j = 0; j < k; ++j) {
+        const int pr = inv[(size_t)t * k + j];
+        if ((unsigned)pr >= R) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c + q < d) acc[i][q] += da[(size_t)pr * d + c + q];
       }
-    }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = c0 + out_col(i);
-    if (c < d) dx[(size_t)t * d + c] = acc[i];
+    store4(dx + (size_t)t * d + c, d - c, acc[i]);
   }
 }
 
-__global__ __launch_bounds__(kThreads) void router_dw_f32_kernel(const float *__restrict__ dz,
+__global__ __launch_bounds__(kThreads, 4) void router_dw_f32_kernel(const float *__restrict__ dz,
                                                                  const float *__restrict__ x, int n, int d,
                                                                  int E, int range, float *__restrict__ part,
                                                                  float *__restrict__ bias_part) {
-  __shared__ float smem[kSmem];
+  __shared__ __attribute__((aligned(16))) float smem[kSmem];
   __shared__ float s_b[kThreads];
   const int c0 = blockIdx.x * kT, e0 = blockIdx.z * kT;
   const int tb = blockIdx.y * range, te = min(n, tb + range);
   const auto rz = gemm::rsrc(dz + (size_t)tb * E, (uint32_t)(te - tb) * (uint32_t)E * 4u);
   const auto rx = gemm::rsrc(x + (size_t)tb * d, (uint32_t)(te - tb) * (uint32_t)d * 4u);
-  f32x16 acc = {};
+  f32x4 acc[kLines] = {};
   product<true, true>(
       acc, smem, te - tb,
       [&](int, int t, int e) { return Piece{rz, ((uint32_t)t * E + e0 + e) * 4u, E - e0 - e}; },
       [&](int, int t, int c) { return Piece{rx, ((uint32_t)t * d + c0 + c) * 4u, d - c0 - c}; });
-  const int e = e0 + out_row();
+  const int c = c0 + line_col();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = c0 + out_col(i);
-    if (e < E && c < d) part[((size_t)blockIdx.y * E + e) * d + c] = acc[i];
+  for (int i = 0; i < kLines; ++i) {
+    const int e = e0 + line_row(i);
+    if (e < E) store4(part + ((size_t)blockIdx.y * E + e) * d + c, d - c, acc[i]);
   }
   if (blockIdx.x == 0) {
+    constexpr int W = kThreads / 64;
     const int be = e0 + (threadIdx.x & 63), s = threadIdx.x >> 6;
     float v = 0.f;
     if (be < E)
-      for (int t = tb + s; t < te; t += 4) v += dz[(size_t)t * E + be];
+      for (int t = tb + s; t < te; t += W) v += dz[(size_t)t * E + be];
     s_b[threadIdx.x] = v;
     __syncthreads();
-    if (s == 0 && be < E)
-      bias_part[(size_t)blockIdx.y * E + be] =
-          s_b[threadIdx.x] + s_b[threadIdx.x + 64] + s_b[threadIdx.x + 128] + s_b[threadIdx.x + 192];
+    if (s == 0 && be < E) {
+      for (int i = 1; i < W; ++i) v += s_b[i * 64 + threadIdx.x];
+      bias_part[(size_t)blockIdx.y * E + be] = v;
+    }
   }
 }
 
