@@ -17,6 +17,8 @@
 // of one: the operand keeps 16 of float32's 24 bits, so dx and dW_g are
 // rounded only on their way out.  Both products are too narrow (E) to matter
 // beside their traffic: dx reads n k + writes n rows of d, dW_g reads n.
+#include <atomic>
+
 #include "common.h"
 #include "gemm_f32.h"
 #include "kernels.h"
@@ -85,12 +87,16 @@ __device__ __forceinline__ void split_bf16(float x, uint16_t &hi, uint16_t &lo) 
 }
 
 // ---- dx, bf16 -------------------------------------------------------------------
-// Block: 4 waves, 32 tokens x 256 columns (each wave 64), 32 experts a step.
-// The router's part goes through LDS as float32, so that the gathered rows
-// and dx itself are read and written as whole 512-B row pieces.
-constexpr int kXT = 32, kXC = 256, kXE = 32, kXPitch = kXC + 4, kZPitch = kXE + 8;
+// Block: 8 waves, 32 tokens x 512 columns (64 a wave), 32 experts a step; the
+// products go through LDS as float32, after which a wave takes four whole
+// row pieces of 1 KB.  Which rows those are is known from the start: their
+// tokens are uniform (the pile rows come by scalar loads) and the gathered
+// rows of the first two slots are already on their way during the products.
+// (Waves that each keep to 32 x 128 and meet nowhere were slower: 89 against
+// 72 us on 8 experts, each wave's chain of loads being its own.)
+constexpr int kXT = 32, kXC = 512, kXE = 32, kXPitch = kXC + 4, kZPitch = kXE + 8, kXRows = kXT / 8;
 
-__global__ __launch_bounds__(256) void router_dx_bf16_kernel(
+__global__ __launch_bounds__(512, 4) void router_dx_bf16_kernel(
     const float *__restrict__ dz, const uint16_t *__restrict__ wg, const uint16_t *__restrict__ da,
     const int32_t *__restrict__ inv, int n, int d, int E, int k, uint16_t *__restrict__ dx) {
   union Lds {
@@ -100,9 +106,49 @@ __global__ __launch_bounds__(256) void router_dx_bf16_kernel(
     } in;
     float out[kXT * kXPitch];
   };
-  __shared__ __attribute__((aligned(16))) Lds s;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  Lds &s = *(Lds *)smem;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int t0 = blockIdx.x * kXT, c0 = blockIdx.y * kXC;
+  const int col = c0 + lane * 8, safe = col < d ? col : 0;
+  const unsigned R = (unsigned)n * (unsigned)k;
+  const int first = t0 + wave * kXRows;  // this wave's tokens first .. first + 3
+
+  // The rows of slots j and j + 1 of the wave's tokens; slots past k and pairs
+  // without a row read row 0 and give zeros.
+  auto gather = [&](u32x4 (&q)[2][kXRows], int j) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < kXRows; ++i) {
+        const int t = min(first + i, n - 1);
+        const unsigned r = j + b < k ? (unsigned)inv[(size_t)t * k + j + b] : ~0u;
+        const uint32_t keep = r < R ? ~0u : 0u;
+        q[b][i] = *(const u32x4 *)(da + (size_t)(r & keep) * d + safe) & u32x4{keep, keep, keep, keep};
+      }
+  };
+  // This thread's pieces of a step's rows of W_g and values of dz.
+  u32x4 wr[kXE / 8];
+  float zr[kXT * kXE / 512];
+  auto fetch = [&](int e0) {
+#pragma unroll
+    for (int i = 0; i < kXE / 8; ++i) {
+      const int e = e0 + wave + 8 * i;
+      wr[i] = *(const u32x4 *)(wg + (size_t)min(e, E - 1) * d + safe);
+      if (e >= E || col >= d) wr[i] = u32x4{};
+    }
+#pragma unroll
+    for (int i = 0; i < kXT * kXE / 512; ++i) {
+      const int e = e0 + (tid & 31), t = t0 + (tid >> 5) + 16 * i;
+      zr[i] = dz[(size_t)min(t, n - 1) * E + min(e, E - 1)];
+      if (e >= E || t >= n) zr[i] = 0.f;
+    }
+  };
+  fetch(0);
+  u32x4 q[2][kXRows] = {};
+  if (da) gather(q, 0);
+
   f32x16 acc[2] = {};
   int b_lane[2];
 #pragma unroll
@@ -110,19 +156,17 @@ __global__ __launch_bounds__(256) void router_dx_bf16_kernel(
   for (int e0 = 0; e0 < E; e0 += kXE) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kXE * kXC / 8 / 256; ++i) {
-      const int e = (tid >> 5) + 8 * i, ch = tid & 31;
-      u32x4 v = {};
-      if (e0 + e < E && c0 + ch * 8 < d) v = *(const u32x4 *)(wg + (size_t)(e0 + e) * d + c0 + ch * 8);
-      *(u32x4 *)(s.in.w + e * kXC * 2 + ((ch ^ kmaj_key<kXC>(e)) << 4)) = v;
+    for (int i = 0; i < kXE / 8; ++i) {
+      const int e = wave + 8 * i;
+      *(u32x4 *)(s.in.w + e * kXC * 2 + ((lane ^ kmaj_key<kXC>(e)) << 4)) = wr[i];
     }
 #pragma unroll
-    for (int i = 0; i < kXT * kXE / 256; ++i) {
-      const int e = tid & 31, t = (tid >> 5) + 8 * i;
-      const float v = e0 + e < E && t0 + t < n ? dz[(size_t)(t0 + t) * E + e0 + e] : 0.f;
-      split_bf16(v, s.in.hi[t * kZPitch + e], s.in.lo[t * kZPitch + e]);
+    for (int i = 0; i < kXT * kXE / 512; ++i) {
+      const int at = ((tid >> 5) + 16 * i) * kZPitch + (tid & 31);
+      split_bf16(zr[i], s.in.hi[at], s.in.lo[at]);
     }
     __syncthreads();
+    if (e0 + kXE < E) fetch(e0 + kXE);
 #pragma unroll
     for (int kk = 0; kk < kXE / 16; ++kk) {
       if (e0 + kk * 16 >= E) break;
@@ -144,30 +188,38 @@ __global__ __launch_bounds__(256) void router_dx_bf16_kernel(
       *(f32x4 *)(s.out + (lane & 31) * kXPitch + wave * 64 + j * 32 + g * 8 + (lane >> 5) * 4) =
           f32x4{acc[j][g * 4], acc[j][g * 4 + 1], acc[j][g * 4 + 2], acc[j][g * 4 + 3]};
   __syncthreads();
-  const int ch = tid & 31, col = c0 + ch * 8;
-  const unsigned R = (unsigned)n * (unsigned)k;
+  f32x4 v[kXRows][2];
+#pragma unroll
+  for (int i = 0; i < kXRows; ++i) {
+    const float *p = s.out + (wave * kXRows + i) * kXPitch + lane * 8;
+    v[i][0] = *(const f32x4 *)p;
+    v[i][1] = *(const f32x4 *)(p + 4);
+  }
+  // the slots' rows are added in slot order
+  auto add = [&](const u32x4 (&q)[2][kXRows]) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < kXRows; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          v[i][x >> 1][(2 * x) & 3] += __uint_as_float(q[b][i][x] << 16);
+          v[i][x >> 1][(2 * x + 1) & 3] += __uint_as_float(q[b][i][x] & 0xffff0000u);
+        }
+  };
+  add(q);
+  if (da)
+    for (int j = 2; j < k; j += 2) {
+      gather(q, j);
+      add(q);
+    }
   if (col >= d) return;
 #pragma unroll
-  for (int i = 0; i < kXT / 8; ++i) {
-    const int r = (tid >> 5) + 8 * i, t = t0 + r;
-    if (t >= n) break;
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = s.out[r * kXPitch + ch * 8 + j];
-    if (da)
-      for (int j = 0; j < k; ++j) {
-        const int pr = inv[(size_t)t * k + j];
-        if ((unsigned)pr >= R) continue;
-        const u32x4 q = *(const u32x4 *)(da + (size_t)pr * d + col);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          v[2 * b] += __uint_as_float(q[b] << 16);
-          v[2 * b + 1] += __uint_as_float(q[b] & 0xffff0000u);
-        }
-      }
-    *(u32x4 *)(dx + (size_t)t * d + col) =
-        u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-  }
+  for (int i = 0; i < kXRows; ++i)
+    if (first + i < n)
+      *(u32x4 *)(dx + (size_t)(first + i) * d + col) =
+          u32x4{pack_bf16x2(v[i][0][0], v[i][0][1]), pack_bf16x2(v[i][0][2], v[i][0][3]),
+                pack_bf16x2(v[i][1][0], v[i][1][1]), pack_bf16x2(v[i][1][2], v[i][1][3])};
 }
 
 // ---- dW_g, bf16 -----------------------------------------------------------------
@@ -369,6 +421,25 @@ Ranges dw_ranges(int n, int d, int E) {
   return {(n + range - 1) / range, range};
 }
 
+hipError_t launch_dx(const RouterGradArgs &a, hipStream_t st) {
+  constexpr int lds = kXT * kXPitch * 4;  // the larger of its two uses
+  static_assert(lds >= kXE * kXC * 2 + 2 * kXT * kZPitch * 2, "both uses fit");
+  static std::atomic<uint64_t> allowed{0};  // devices on which LDS above 64 KB is allowed
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(allowed.load(std::memory_order_acquire) & bit)) {
+    err = hipFuncSetAttribute((const void *)router_dx_bf16_kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                              lds);
+    if (err != hipSuccess) return err;
+    allowed.fetch_or(bit, std::memory_order_release);
+  }
+  router_dx_bf16_kernel<<<dim3((a.n + kXT - 1) / kXT, (a.d + kXC - 1) / kXC), 512, lds, st>>>(
+      a.dlogits, (const uint16_t *)a.wg, (const uint16_t *)a.da, a.inv, a.n, a.d, a.E, a.k, (uint16_t *)a.dx);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 size_t router_grad_bytes(int n, int d, int E) {
@@ -383,9 +454,8 @@ hipError_t launch_router_grad(const RouterGradArgs &a, hipStream_t st) {
   const Ranges q = dw_ranges(a.n, a.d, a.E);
   float *part = (float *)a.ws, *bias_part = part + (size_t)q.S * a.E * a.d;
   if (a.bf16) {
-    router_dx_bf16_kernel<<<dim3((a.n + kXT - 1) / kXT, (a.d + kXC - 1) / kXC), 256, 0, st>>>(
-        a.dlogits, (const uint16_t *)a.wg, (const uint16_t *)a.da, a.inv, a.n, a.d, a.E, a.k,
-        (uint16_t *)a.dx);
+    const hipError_t e = launch_dx(a, st);
+    if (e != hipSuccess) return e;
     // experts of a block: as many 32-wide groups as there are, up to 128
     const int EW = a.E <= 32 ? 32 : (a.E <= 64 ? 64 : 128);
     const dim3 grid((a.d + kWC - 1) / kWC, q.S, (a.E + EW - 1) / EW);
