@@ -28,16 +28,30 @@
 namespace moe {
 namespace {
 
+// x = hi + lo + rest, the rest below 2^-16 of x.
+__device__ __forceinline__ void split_bf16(float x, uint16_t &hi, uint16_t &lo) {
+  hi = (uint16_t)f32_to_bf16_bits(x);
+  const float r = x - bf16_bits_to_f32(hi);
+  // (an infinite or NaN x keeps its value in hi; the rest would be NaN)
+  lo = __builtin_isfinite(x) ? (uint16_t)f32_to_bf16_bits(r) : 0;
+}
+
+// Experts of dz's bf16 halves, padded with zeros.
+__host__ __device__ constexpr int padded(int E) { return (E + 31) & ~31; }
+
 // ---- dz: one group of G = topk_group(E) lanes per token -----------------------
+// split (bf16 rows): dz's two halves too, hi [n][padded(E)], then lo, which
+// the dW_g product reads once per column tile.
 __global__ __launch_bounds__(256) void router_dz_kernel(
     const float *__restrict__ logits, const int32_t *__restrict__ idx, const float *__restrict__ w,
     const float *__restrict__ dw, const float *__restrict__ f, float aux, int n, int E, int k, int renorm,
-    float *__restrict__ dz) {
+    float *__restrict__ dz, uint16_t *__restrict__ split) {
   const int G = topk_group(E);
   const int gl = (threadIdx.x & 63) & (G - 1);
   const int t = (blockIdx.x * 256 + threadIdx.x) / G;
   if ((blockIdx.x * 256 + (threadIdx.x & ~63)) / G >= n) return;  // whole wave idle
   const bool live = t < n;
+  const int Ep = padded(E);
   const size_t row = live ? t : 0;
   const float *z = logits + row * E;
   idx += row * k;
@@ -75,15 +89,10 @@ __global__ __launch_bounds__(256) void router_dz_kernel(
       if (f) v = fmaf(aux * p, f[e] - fp, v);
     }
     dz[row * E + e] = v;
+    if (split) split_bf16(v, split[row * Ep + e], split[(size_t)n * Ep + row * Ep + e]);
   }
-}
-
-// x = hi + lo + rest, the rest below 2^-16 of x.
-__device__ __forceinline__ void split_bf16(float x, uint16_t &hi, uint16_t &lo) {
-  hi = (uint16_t)f32_to_bf16_bits(x);
-  const float r = x - bf16_bits_to_f32(hi);
-  // (an infinite or NaN x keeps its value in hi; the rest would be NaN)
-  lo = __builtin_isfinite(x) ? (uint16_t)f32_to_bf16_bits(r) : 0;
+  if (split)
+    for (int e = E + gl; e < Ep; e += G) split[row * Ep + e] = split[(size_t)n * Ep + row * Ep + e] = 0;
 }
 
 // ---- dx, bf16 -------------------------------------------------------------------
@@ -224,38 +233,57 @@ __global__ __launch_bounds__(512, 4) void router_dx_bf16_kernel(
 
 // ---- dW_g, bf16 -----------------------------------------------------------------
 // Block: 4 waves, EW experts x 128 columns (each wave 32) over a range of the
-// tokens, 64 at a step; the ranges' float32 planes part[s][E][d] (and the
-// bias's, after them) are added in order by router_sum_kernel.
+// tokens, 64 at a step, the next step's pieces of x and of dz's halves on
+// their way; the ranges' float32 planes part[s][E][d] are added in order by
+// router_sum_kernel.  The last column tile's blocks take the bias's sums
+// bias_part[s][E] instead, from the float32 dz.
 constexpr int kWC = 128, kWT = 64;
 
 template <int EW>
 __global__ __launch_bounds__(256) void router_dw_bf16_kernel(const float *__restrict__ dz,
+                                                             const uint16_t *__restrict__ split,
                                                              const uint16_t *__restrict__ x, int n, int d,
                                                              int E, int range, float *__restrict__ part,
                                                              float *__restrict__ bias_part) {
-  constexpr int TM = EW / 32;
-  constexpr int ZR = 256 / EW, ZN = kWT / ZR;  // dz: rows per pass, passes
+  constexpr int TM = EW / 32, ZC = EW / 8, ZN = kWT * ZC / 256;  // 16-B pieces of a dz row; per thread
   __shared__ __attribute__((aligned(16))) uint8_t s_x[kWT * kWC * 2];
-  __shared__ __attribute__((aligned(16))) uint8_t s_hi[kWT * EW * 2], s_lo[kWT * EW * 2];
-  __shared__ float s_b[256];
+  __shared__ __attribute__((aligned(16))) uint8_t s_z[2][kWT * EW * 2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int c0 = blockIdx.x * kWC, e0 = blockIdx.z * EW;
+  const int c0 = blockIdx.x * kWC, e0 = blockIdx.z * EW, Ep = padded(E);
   const int tb = blockIdx.y * range, te = min(n, tb + range);
-  const int ze = tid % EW, zt = tid / EW;
+  if (c0 >= d) {
+    constexpr int ZR = 256 / EW;
+    float *s_b = (float *)s_x;
+    const int e = e0 + tid % EW;
+    float v = 0.f;
+    if (e < E)
+#pragma unroll 16
+      for (int t = tb + tid / EW; t < te; t += ZR) v += dz[(size_t)t * E + e];
+    s_b[tid] = v;
+    __syncthreads();
+    if (tid < EW && e < E) {
+      for (int i = 1; i < ZR; ++i) v += s_b[i * EW + tid];
+      bias_part[(size_t)blockIdx.y * E + e] = v;
+    }
+    return;
+  }
   const int xch = tid & 15, xt = tid >> 4;
-  u32x4 xr[4];
-  float zr[ZN], bias = 0.f;
+  u32x4 xr[4], zr[2][ZN];
   auto fetch = [&](int t0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = t0 + xt + 16 * i;
-      xr[i] = u32x4{};
-      if (t < te && c0 + xch * 8 < d) xr[i] = *(const u32x4 *)(x + (size_t)t * d + c0 + xch * 8);
+      xr[i] = *(const u32x4 *)(x + (size_t)min(t, te - 1) * d + (c0 + xch * 8 < d ? c0 + xch * 8 : 0));
+      if (t >= te || c0 + xch * 8 >= d) xr[i] = u32x4{};
     }
 #pragma unroll
     for (int i = 0; i < ZN; ++i) {
-      const int t = t0 + zt + ZR * i;
-      zr[i] = t < te && e0 + ze < E ? dz[(size_t)t * E + e0 + ze] : 0.f;
+      const int t = t0 + tid / ZC + (256 / ZC) * i, e = e0 + tid % ZC * 8;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        zr[h][i] = *(const u32x4 *)(split + ((size_t)h * n + min(t, te - 1)) * Ep + (e < Ep ? e : 0));
+        if (t >= te || e >= Ep) zr[h][i] = u32x4{};
+      }
     }
   };
   f32x16 acc[TM] = {};
@@ -273,10 +301,10 @@ __global__ __launch_bounds__(256) void router_dw_bf16_kernel(const float *__rest
     }
 #pragma unroll
     for (int i = 0; i < ZN; ++i) {
-      const int t = zt + ZR * i;
-      const int at = t * EW * 2 + (((ze >> 3) ^ kmaj_key<EW>(t)) << 4) + (ze & 7) * 2;
-      split_bf16(zr[i], *(uint16_t *)(s_hi + at), *(uint16_t *)(s_lo + at));
-      bias += zr[i];
+      const int t = tid / ZC + (256 / ZC) * i;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *(u32x4 *)(s_z[h] + t * EW * 2 + (((tid % ZC) ^ kmaj_key<EW>(t)) << 4)) = zr[h][i];
     }
     __syncthreads();
     if (t0 + kWT < te) fetch(t0 + kWT);
@@ -284,10 +312,10 @@ __global__ __launch_bounds__(256) void router_dw_bf16_kernel(const float *__rest
     for (int kk = 0; kk < kWT / 16; ++kk) {
       const bf16x8 b = kmaj_frag<kWC>(s_x, b_lane, kk);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, kmaj_frag<EW>(s_hi, a_lane[i], kk), acc[i], 0, 0, 0);
-        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, kmaj_frag<EW>(s_lo, a_lane[i], kk), acc[i], 0, 0, 0);
-      }
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, kmaj_frag<EW>(s_z[h], a_lane[i], kk), acc[i], 0, 0, 0);
     }
   }
   float *out = part + (size_t)blockIdx.y * E * d;
@@ -300,15 +328,6 @@ __global__ __launch_bounds__(256) void router_dw_bf16_kernel(const float *__rest
       if (e < E && col < d)
         *(f32x4 *)(out + (size_t)e * d + col) =
             f32x4{acc[i][g * 4], acc[i][g * 4 + 1], acc[i][g * 4 + 2], acc[i][g * 4 + 3]};
-    }
-  }
-  if (blockIdx.x == 0) {  // the bias's sum over this range, in row order
-    s_b[tid] = bias;
-    __syncthreads();
-    if (zt == 0 && e0 + ze < E) {
-      float v = 0.f;
-      for (int i = 0; i < ZR; ++i) v += s_b[i * EW + ze];
-      bias_part[(size_t)blockIdx.y * E + e0 + ze] = v;
     }
   }
 }
@@ -403,7 +422,8 @@ __global__ __launch_bounds__(kThreads, 4) void router_dw_f32_kernel(const float 
   }
 }
 
-// Token ranges of the dW_g product: about two blocks per CU, but planes of
+// Token ranges of the dW_g product: about two blocks per CU (four when a
+// block has few experts, and so little LDS), but planes of
 // at most the bytes of x (S E 4 <= n 2), and whole steps; a range's rows of x
 // and dz stay under 2^30 bytes (32-bit buffer offsets).
 struct Ranges {
@@ -411,7 +431,7 @@ struct Ranges {
 };
 Ranges dw_ranges(int n, int d, int E) {
   const int tiles = ((d + kWC - 1) / kWC) * ((E + 127) / 128);
-  int S = (512 + tiles - 1) / tiles;
+  int S = ((E <= 32 ? 1024 : 512) + tiles - 1) / tiles;
   const int most = n / (2 * E) > 1 ? n / (2 * E) : 1;
   if (S > most) S = most;
   const long long bytes = (long long)n * (d > E ? d : E) * 4;
@@ -442,15 +462,23 @@ hipError_t launch_dx(const RouterGradArgs &a, hipStream_t st) {
 
 }  // namespace
 
+namespace {
+size_t plane_bytes(int n, int d, int E) {
+  return ((size_t)dw_ranges(n, d, E).S * ((size_t)E * d + E) * sizeof(float) + 255) / 256 * 256;
+}
+}  // namespace
+
 size_t router_grad_bytes(int n, int d, int E) {
-  return (size_t)dw_ranges(n, d, E).S * ((size_t)E * d + E) * sizeof(float);
+  // the planes, then (bf16 rows) dz's two halves
+  return plane_bytes(n, d, E) + (size_t)2 * n * padded(E) * sizeof(uint16_t);
 }
 
 hipError_t launch_router_grad(const RouterGradArgs &a, hipStream_t st) {
+  uint16_t *split = a.bf16 ? (uint16_t *)((char *)a.ws + plane_bytes(a.n, a.d, a.E)) : nullptr;
   const int per_block = 256 / topk_group(a.E);
   router_dz_kernel<<<(a.n + per_block - 1) / per_block, 256, 0, st>>>(
       a.logits, a.idx, a.topk_w, a.dtopk_w, a.f, a.alpha * (float)a.E / (float)a.n, a.n, a.E, a.k,
-      a.renorm ? 1 : 0, a.dlogits);
+      a.renorm ? 1 : 0, a.dlogits, split);
   const Ranges q = dw_ranges(a.n, a.d, a.E);
   float *part = (float *)a.ws, *bias_part = part + (size_t)q.S * a.E * a.d;
   if (a.bf16) {
@@ -458,9 +486,9 @@ hipError_t launch_router_grad(const RouterGradArgs &a, hipStream_t st) {
     if (e != hipSuccess) return e;
     // experts of a block: as many 32-wide groups as there are, up to 128
     const int EW = a.E <= 32 ? 32 : (a.E <= 64 ? 64 : 128);
-    const dim3 grid((a.d + kWC - 1) / kWC, q.S, (a.E + EW - 1) / EW);
+    const dim3 grid((a.d + kWC - 1) / kWC + 1, q.S, (a.E + EW - 1) / EW);
     auto go = [&](auto kern) {
-      kern<<<grid, 256, 0, st>>>(a.dlogits, (const uint16_t *)a.x, a.n, a.d, a.E, q.range, part, bias_part);
+      kern<<<grid, 256, 0, st>>>(a.dlogits, split, (const uint16_t *)a.x, a.n, a.d, a.E, q.range, part, bias_part);
     };
     if (EW == 32)
       go(router_dw_bf16_kernel<32>);

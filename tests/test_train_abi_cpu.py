@@ -143,6 +143,8 @@ def test_router_backward_refusals():
     assert need % 256 == 0 and need >= 4 * (64 + 1) * 4
     assert _router(nb=need - 1) == -5 and _router(ws=None) == -5 and _router(ws=FAKE + 4) == -4
     assert B.moe_router_backward_workspace_bytes((0, 64, 4, 2, 64)) == 0
-    # the partial planes of W_g's gradient stay within the bytes of x
+    # the partial planes of W_g's gradient stay within the bytes of x; two
+    # bf16 halves of dlogits, 32 experts wide at least, follow them
     for n, d, E in ((8192, 4096, 8), (4096, 2880, 128), (65536, 256, 64)):
-        assert B.moe_router_backward_workspace_bytes((n, d, E, 1, 8)) <= max(n * 2, 4 * E) * (d + 1) + 256
+        most = max(n * 2, 4 * E) * (d + 1) + 4 * n * -(-E // 32) * 32 + 512
+        assert B.moe_router_backward_workspace_bytes((n, d, E, 1, 8)) <= most
