@@ -105,9 +105,10 @@ __global__ __launch_bounds__(256) void router_dz_kernel(
 // 72 us on 8 experts, each wave's chain of loads being its own.)
 constexpr int kXT = 32, kXC = 512, kXE = 32, kXPitch = kXC + 4, kZPitch = kXE + 8, kXRows = kXT / 8;
 
-__global__ __launch_bounds__(512, 4) void router_dx_bf16_kernel(
+__device__ __forceinline__ void router_dx_tile(
     const float *__restrict__ dz, const uint16_t *__restrict__ wg, const uint16_t *__restrict__ da,
-    const int32_t *__restrict__ inv, int n, int d, int E, int k, uint16_t *__restrict__ dx) {
+    const int32_t *__restrict__ inv, int n, int d, int E, int k, uint16_t *__restrict__ dx, int tx, int ty,
+    uint8_t *smem) {
   union Lds {
     struct {
       uint8_t w[kXE * kXC * 2];
@@ -115,11 +116,10 @@ __global__ __launch_bounds__(512, 4) void router_dx_bf16_kernel(
     } in;
     float out[kXT * kXPitch];
   };
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   Lds &s = *(Lds *)smem;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int t0 = blockIdx.x * kXT, c0 = blockIdx.y * kXC;
+  const int t0 = tx * kXT, c0 = ty * kXC;
   const int col = c0 + lane * 8, safe = col < d ? col : 0;
   const unsigned R = (unsigned)n * (unsigned)k;
   const int first = t0 + wave * kXRows;  // this wave's tokens first .. first + 3
@@ -232,28 +232,35 @@ __global__ __launch_bounds__(512, 4) void router_dx_bf16_kernel(
 }
 
 // ---- dW_g, bf16 -----------------------------------------------------------------
-// Block: 4 waves, EW experts x 128 columns (each wave 32) over a range of the
-// tokens, 64 at a step, the next step's pieces of x and of dz's halves on
-// their way; the ranges' float32 planes part[s][E][d] are added in order by
-// router_sum_kernel.  The last column tile's blocks take the bias's sums
-// bias_part[s][E] instead, from the float32 dz.
-constexpr int kWC = 128, kWT = 64;
+// Block: 8 waves, EW experts x WC columns over a range of the tokens, 64 at a
+// step, the next step's pieces of x and of dz's halves on their way.  A wave
+// takes 32 columns and up to 64 experts (EW = 128: four waves each for the
+// lower and the upper half).  The ranges' float32 planes part[s][E][d] are
+// added in order by router_sum_kernel.  The blocks past the last column tile
+// take the bias's sums bias_part[s][E] instead, from the float32 dz.
+constexpr int kWT = 64;
+template <int EW>
+struct DwTile {
+  static constexpr int TM = EW < 64 ? 1 : 2, NE = EW / (32 * TM), WC = 32 * (8 / NE);
+  static constexpr int LDS = kWT * WC * 2 + 2 * kWT * EW * 2;
+};
 
 template <int EW>
-__global__ __launch_bounds__(256) void router_dw_bf16_kernel(const float *__restrict__ dz,
-                                                             const uint16_t *__restrict__ split,
-                                                             const uint16_t *__restrict__ x, int n, int d,
-                                                             int E, int range, float *__restrict__ part,
-                                                             float *__restrict__ bias_part) {
-  constexpr int TM = EW / 32, ZC = EW / 8, ZN = kWT * ZC / 256;  // 16-B pieces of a dz row; per thread
-  __shared__ __attribute__((aligned(16))) uint8_t s_x[kWT * kWC * 2];
-  __shared__ __attribute__((aligned(16))) uint8_t s_z[2][kWT * EW * 2];
+__device__ __forceinline__ void router_dw_tile(const float *__restrict__ dz, const uint16_t *__restrict__ split,
+                                               const uint16_t *__restrict__ x, int n, int d, int E, int range,
+                                               float *__restrict__ part, float *__restrict__ bias_part, int bx,
+                                               int by, int bz, uint8_t *smem) {
+  using T = DwTile<EW>;
+  constexpr int TM = T::TM, WC = T::WC, NT = 512;
+  constexpr int ZC = EW / 8, ZN = kWT * ZC / NT > 0 ? kWT * ZC / NT : 1;  // 16-B pieces of a dz row; per thread
+  constexpr int XC = WC / 8, XN = kWT * XC / NT;
+  uint8_t *s_x = smem, *s_z = smem + kWT * WC * 2;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int c0 = blockIdx.x * kWC, e0 = blockIdx.z * EW, Ep = padded(E);
-  const int tb = blockIdx.y * range, te = min(n, tb + range);
+  const int c0 = bx * WC, e0 = bz * EW, Ep = padded(E);
+  const int tb = by * range, te = min(n, tb + range);
   if (c0 >= d) {
-    constexpr int ZR = 256 / EW;
-    float *s_b = (float *)s_x;
+    constexpr int ZR = NT / EW;
+    float *s_b = (float *)smem;
     const int e = e0 + tid % EW;
     float v = 0.f;
     if (e < E)
@@ -263,72 +270,104 @@ __global__ __launch_bounds__(256) void router_dw_bf16_kernel(const float *__rest
     __syncthreads();
     if (tid < EW && e < E) {
       for (int i = 1; i < ZR; ++i) v += s_b[i * EW + tid];
-      bias_part[(size_t)blockIdx.y * E + e] = v;
+      bias_part[(size_t)by * E + e] = v;
     }
     return;
   }
-  const int xch = tid & 15, xt = tid >> 4;
-  u32x4 xr[4], zr[2][ZN];
+  const int xcol = c0 + tid % XC * 8, zt = tid / ZC, ze = e0 + tid % ZC * 8;
+  const bool zin = ZC * kWT >= NT || zt < kWT;  // (EW = 32: half of the threads hold pieces of dz)
+  u32x4 xr[XN], zr[2][ZN];
   auto fetch = [&](int t0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = t0 + xt + 16 * i;
-      xr[i] = *(const u32x4 *)(x + (size_t)min(t, te - 1) * d + (c0 + xch * 8 < d ? c0 + xch * 8 : 0));
-      if (t >= te || c0 + xch * 8 >= d) xr[i] = u32x4{};
+    for (int i = 0; i < XN; ++i) {
+      const int t = t0 + tid / XC + (NT / XC) * i;
+      xr[i] = *(const u32x4 *)(x + (size_t)min(t, te - 1) * d + (xcol < d ? xcol : 0));
+      if (t >= te || xcol >= d) xr[i] = u32x4{};
     }
+    if (zin)
 #pragma unroll
-    for (int i = 0; i < ZN; ++i) {
-      const int t = t0 + tid / ZC + (256 / ZC) * i, e = e0 + tid % ZC * 8;
+      for (int i = 0; i < ZN; ++i) {
+        const int t = t0 + zt + (NT / ZC) * i;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        zr[h][i] = *(const u32x4 *)(split + ((size_t)h * n + min(t, te - 1)) * Ep + (e < Ep ? e : 0));
-        if (t >= te || e >= Ep) zr[h][i] = u32x4{};
+        for (int h = 0; h < 2; ++h) {
+          zr[h][i] = *(const u32x4 *)(split + ((size_t)h * n + min(t, te - 1)) * Ep + (ze < Ep ? ze : 0));
+          if (t >= te || ze >= Ep) zr[h][i] = u32x4{};
+        }
       }
-    }
   };
+  const int half = wave % T::NE, cg = wave / T::NE;  // this wave's experts and columns
   f32x16 acc[TM] = {};
   int a_lane[TM];
 #pragma unroll
-  for (int i = 0; i < TM; ++i) a_lane[i] = kmaj_lane<EW>(i * 32, lane);
-  const int b_lane = kmaj_lane<kWC>(wave * 32, lane);
+  for (int i = 0; i < TM; ++i) a_lane[i] = kmaj_lane<EW>(half * 64 + i * 32, lane);
+  const int b_lane = kmaj_lane<WC>(cg * 32, lane);
   fetch(tb);
   for (int t0 = tb; t0 < te; t0 += kWT) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = xt + 16 * i;
-      *(u32x4 *)(s_x + t * kWC * 2 + ((xch ^ kmaj_key<kWC>(t)) << 4)) = xr[i];
+    for (int i = 0; i < XN; ++i) {
+      const int t = tid / XC + (NT / XC) * i;
+      *(u32x4 *)(s_x + t * WC * 2 + (((tid % XC) ^ kmaj_key<WC>(t)) << 4)) = xr[i];
     }
+    if (zin)
 #pragma unroll
-    for (int i = 0; i < ZN; ++i) {
-      const int t = tid / ZC + (256 / ZC) * i;
+      for (int i = 0; i < ZN; ++i) {
+        const int t = zt + (NT / ZC) * i;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *(u32x4 *)(s_z[h] + t * EW * 2 + (((tid % ZC) ^ kmaj_key<EW>(t)) << 4)) = zr[h][i];
-    }
+        for (int h = 0; h < 2; ++h)
+          *(u32x4 *)(s_z + (h * kWT + t) * EW * 2 + (((tid % ZC) ^ kmaj_key<EW>(t)) << 4)) = zr[h][i];
+      }
     __syncthreads();
     if (t0 + kWT < te) fetch(t0 + kWT);
 #pragma unroll
     for (int kk = 0; kk < kWT / 16; ++kk) {
-      const bf16x8 b = kmaj_frag<kWC>(s_x, b_lane, kk);
+      const bf16x8 b = kmaj_frag<WC>(s_x, b_lane, kk);
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, kmaj_frag<EW>(s_z[h], a_lane[i], kk), acc[i], 0, 0, 0);
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              b, kmaj_frag<EW>(s_z + h * kWT * EW * 2, a_lane[i], kk), acc[i], 0, 0, 0);
     }
   }
-  float *out = part + (size_t)blockIdx.y * E * d;
+  float *out = part + (size_t)by * E * d;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int e = e0 + i * 32 + (lane & 31);
+    const int e = e0 + half * 64 + i * 32 + (lane & 31);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const int col = c0 + wave * 32 + g * 8 + (lane >> 5) * 4;
+      const int col = c0 + cg * 32 + g * 8 + (lane >> 5) * 4;
       if (e < E && col < d)
         *(f32x4 *)(out + (size_t)e * d + col) =
             f32x4{acc[i][g * 4], acc[i][g * 4 + 1], acc[i][g * 4 + 2], acc[i][g * 4 + 3]};
     }
+  }
+}
+
+// Both products in one grid: they read different things, and the few long
+// blocks of dW_g start first and end under dx's many short ones.
+struct BothParams {
+  const float *dz;
+  const uint16_t *split, *x, *wg, *da;
+  const int32_t *inv;
+  uint16_t *dx;
+  float *part, *bias_part;
+  int n, d, E, k, range;
+  int dw_cols, dw_S, dw_blocks;  // column tiles (with the bias's), token ranges, all blocks
+  int dx_rows;                   // token tiles
+};
+
+template <int EW>
+__global__ __launch_bounds__(512, 4) void router_both_kernel(BothParams p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  int b = blockIdx.x;
+  if (b < p.dw_blocks) {
+    const int bx = b % p.dw_cols, q = b / p.dw_cols;
+    router_dw_tile<EW>(p.dz, p.split, p.x, p.n, p.d, p.E, p.range, p.part, p.bias_part, bx, q % p.dw_S,
+                       q / p.dw_S, smem);
+  } else {
+    b -= p.dw_blocks;
+    router_dx_tile(p.dz, p.wg, p.da, p.inv, p.n, p.d, p.E, p.k, p.dx, b % p.dx_rows, b / p.dx_rows, smem);
   }
 }
 
@@ -341,6 +380,7 @@ __global__ __launch_bounds__(256) void router_sum_kernel(const float *__restrict
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, ed = (size_t)E * d;
   if (i < ed) {
     float v = 0.f;
+#pragma unroll 8
     for (int s = 0; s < S; ++s) v += part[(size_t)s * ed + i];
     if constexpr (BF)
       ((uint16_t *)dwg)[i] = (uint16_t)f32_to_bf16_bits(v);
@@ -422,16 +462,15 @@ __global__ __launch_bounds__(kThreads, 4) void router_dw_f32_kernel(const float 
   }
 }
 
-// Token ranges of the dW_g product: about two blocks per CU (four when a
-// block has few experts, and so little LDS), but planes of
-// at most the bytes of x (S E 4 <= n 2), and whole steps; a range's rows of x
-// and dz stay under 2^30 bytes (32-bit buffer offsets).
+// Token ranges of the dW_g product: one block per CU beside dx's, but planes
+// of at most the bytes of x (S E 4 <= n 2), and whole steps; a range's rows
+// of x and dz stay under 2^30 bytes (32-bit buffer offsets, float32).
 struct Ranges {
   int S, range;
 };
 Ranges dw_ranges(int n, int d, int E) {
-  const int tiles = ((d + kWC - 1) / kWC) * ((E + 127) / 128);
-  int S = ((E <= 32 ? 1024 : 512) + tiles - 1) / tiles;
+  const int cols = E <= 64 ? 256 : 128, tiles = ((d + cols - 1) / cols) * ((E + 127) / 128);
+  int S = (256 + tiles - 1) / tiles;
   const int most = n / (2 * E) > 1 ? n / (2 * E) : 1;
   if (S > most) S = most;
   const long long bytes = (long long)n * (d > E ? d : E) * 4;
@@ -441,22 +480,43 @@ Ranges dw_ranges(int n, int d, int E) {
   return {(n + range - 1) / range, range};
 }
 
-hipError_t launch_dx(const RouterGradArgs &a, hipStream_t st) {
-  constexpr int lds = kXT * kXPitch * 4;  // the larger of its two uses
-  static_assert(lds >= kXE * kXC * 2 + 2 * kXT * kZPitch * 2, "both uses fit");
+template <int EW>
+hipError_t launch_both(const RouterGradArgs &a, const uint16_t *split, const Ranges &q, float *part,
+                       float *bias_part, hipStream_t st) {
+  using T = DwTile<EW>;
+  constexpr int dx_lds = kXT * kXPitch * 4, lds = dx_lds > T::LDS ? dx_lds : T::LDS;
+  static_assert(dx_lds >= kXE * kXC * 2 + 2 * kXT * kZPitch * 2, "both uses of dx's LDS fit");
   static std::atomic<uint64_t> allowed{0};  // devices on which LDS above 64 KB is allowed
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
   if (err != hipSuccess) return err;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(allowed.load(std::memory_order_acquire) & bit)) {
-    err = hipFuncSetAttribute((const void *)router_dx_bf16_kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+    err = hipFuncSetAttribute((const void *)router_both_kernel<EW>, hipFuncAttributeMaxDynamicSharedMemorySize,
                               lds);
     if (err != hipSuccess) return err;
     allowed.fetch_or(bit, std::memory_order_release);
   }
-  router_dx_bf16_kernel<<<dim3((a.n + kXT - 1) / kXT, (a.d + kXC - 1) / kXC), 512, lds, st>>>(
-      a.dlogits, (const uint16_t *)a.wg, (const uint16_t *)a.da, a.inv, a.n, a.d, a.E, a.k, (uint16_t *)a.dx);
+  BothParams p{};
+  p.dz = a.dlogits;
+  p.split = split;
+  p.x = (const uint16_t *)a.x;
+  p.wg = (const uint16_t *)a.wg;
+  p.da = (const uint16_t *)a.da;
+  p.inv = a.inv;
+  p.dx = (uint16_t *)a.dx;
+  p.part = part;
+  p.bias_part = bias_part;
+  p.n = a.n;
+  p.d = a.d;
+  p.E = a.E;
+  p.k = a.k;
+  p.range = q.range;
+  p.dw_cols = (a.d + T::WC - 1) / T::WC + 1;
+  p.dw_S = q.S;
+  p.dw_blocks = p.dw_cols * q.S * ((a.E + EW - 1) / EW);
+  p.dx_rows = (a.n + kXT - 1) / kXT;
+  router_both_kernel<EW><<<p.dw_blocks + p.dx_rows * ((a.d + kXC - 1) / kXC), 512, lds, st>>>(p);
   return hipGetLastError();
 }
 
@@ -482,20 +542,11 @@ hipError_t launch_router_grad(const RouterGradArgs &a, hipStream_t st) {
   const Ranges q = dw_ranges(a.n, a.d, a.E);
   float *part = (float *)a.ws, *bias_part = part + (size_t)q.S * a.E * a.d;
   if (a.bf16) {
-    const hipError_t e = launch_dx(a, st);
+    // experts of a dW_g block: as many 32-wide groups as there are, up to 128
+    const hipError_t e = a.E <= 32   ? launch_both<32>(a, split, q, part, bias_part, st)
+                         : a.E <= 64 ? launch_both<64>(a, split, q, part, bias_part, st)
+                                     : launch_both<128>(a, split, q, part, bias_part, st);
     if (e != hipSuccess) return e;
-    // experts of a block: as many 32-wide groups as there are, up to 128
-    const int EW = a.E <= 32 ? 32 : (a.E <= 64 ? 64 : 128);
-    const dim3 grid((a.d + kWC - 1) / kWC + 1, q.S, (a.E + EW - 1) / EW);
-    auto go = [&](auto kern) {
-      kern<<<grid, 256, 0, st>>>(a.dlogits, split, (const uint16_t *)a.x, a.n, a.d, a.E, q.range, part, bias_part);
-    };
-    if (EW == 32)
-      go(router_dw_bf16_kernel<32>);
-    else if (EW == 64)
-      go(router_dw_bf16_kernel<64>);
-    else
-      go(router_dw_bf16_kernel<128>);
   } else {
     router_dx_f32_kernel<<<dim3((a.n + kT - 1) / kT, (a.d + kT - 1) / kT), kThreads, 0, st>>>(
         a.dlogits, (const float *)a.wg, (const float *)a.da, a.inv, a.n, a.d, a.E, a.k, (float *)a.dx);
