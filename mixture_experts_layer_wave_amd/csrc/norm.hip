@@ -130,11 +130,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void layer_norm_kernel(
       wv[c][j] = col < d ? w[col] : 0.f;
       bv[c][j] = b && col < d ? b[col] : 0.f;
     }
-  K cur[C];
+  K next[C];  // the row to come
   auto load_row = [&](int row) {
     if (row < n)
 #pragma unroll
-      for (int c = 0; c < C; ++c) cur[c].load(x, row, (c * TPR + gl) * V, d);
+      for (int c = 0; c < C; ++c) next[c].load(x, row, (c * TPR + gl) * V, d);
   };
   load_row(blockIdx.x * G + grp);
   // (every thread of a block takes the same number of turns: the sums of a
@@ -146,10 +146,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void layer_norm_kernel(
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        v[c][j] = cur[c].get(j);  // 0 past the row's end
+        v[c][j] = next[c].get(j);  // 0 past the row's end
         s[0] += v[c][j];
       }
-    load_row(row + stride);  // the next row's loads run under this row's sums
+    load_row(row + stride);  // runs under this row's sums
     row_sum(s);
     // (divided, not multiplied by 1 / d: the mean of equal values is that value)
     const float mu = s[0] / (float)d;
@@ -290,46 +290,61 @@ __global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(
 }
 
 // dw | db [2 d] = the sum of P partial rows [P][2 d], in a fixed order: a
-// block takes 64 columns, 16 threads each, thread s the rows s, s + 16, ...
+// block takes 64 columns, 16 threads of four columns for each of 64 slabs of
+// the rows (slab s: rows s, s + 64, ...), then the slabs' sums in order.
 __global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restrict__ part, int P,
                                                           int d, float *__restrict__ dw,
                                                           float *__restrict__ db) {
-  __shared__ float s_p[16][64];
-  const int lane = threadIdx.x & 63, s = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
-  float v = 0.f;
-  if (col < 2 * d)
-    for (int p = s; p < P; p += 16) v += part[(size_t)p * 2 * d + col];
-  s_p[s][lane] = v;
+  __shared__ __attribute__((aligned(16))) float s_p[64][64];
+  __shared__ float s_q[4][64];
+  const int tid = threadIdx.x, slab = tid >> 4, c4 = (tid & 15) * 4;
+  const int base = blockIdx.x * 64, left = 2 * d - base - c4;  // columns from this thread's first on
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int p = slab; p < P; p += 64) {
+    const float *q = part + (size_t)p * 2 * d + base + c4;
+    if (left >= 4) {
+      v += *(const f32x4_any *)q;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (j < left) v[j] += q[j];
+    }
+  }
+  *(f32x4 *)&s_p[slab][c4] = v;
   __syncthreads();
-  if (s == 0 && col < 2 * d) {
-    v = 0.f;
-    for (int i = 0; i < 16; ++i) v += s_p[i][lane];
-    if (col < d) {
-      if (dw) dw[col] = v;
+  const int col = tid & 63;
+  if (tid < 256) {
+    float a = 0.f;
+    for (int i = 0; i < 16; ++i) a += s_p[(tid >> 6) * 16 + i][col];
+    s_q[tid >> 6][col] = a;
+  }
+  __syncthreads();
+  const int c = base + col;
+  if (tid < 64 && c < 2 * d) {
+    const float a = s_q[0][col] + s_q[1][col] + s_q[2][col] + s_q[3][col];
+    if (c < d) {
+      if (dw) dw[c] = a;
     } else if (db) {
-      db[col - d] = v;
+      db[c - d] = a;
     }
   }
 }
 
 // Threads per row and chunks per thread for rows of d: the fewest threads
-// that hold a row in at most two 16-B chunks each (the gradient: one, up to
-// 1024 threads; float32 above 8192: four), so narrow rows share a block.
-template <bool BF, bool TAIL, bool GRAD, typename Launch>
+// that hold a row in one 16-B chunk each (two above 1024 threads, four for
+// float32 above 8192), so narrow rows share a block.  (Rows of 4096 bf16 in
+// two chunks by 256 threads: 46 us against 36 for 8192 of them.)
+template <bool BF, bool TAIL, typename Launch>
 hipError_t with_layout(int d, Launch go) {
   constexpr int V = Chunk<BF, TAIL>::V;
 #define MOE_LN(C_, T_) \
   if (d <= V * C_ * T_) return go(std::integral_constant<int, C_>{}, std::integral_constant<int, T_>{});
   MOE_LN(1, 16)
   MOE_LN(1, 64)
+  MOE_LN(1, 128)
   MOE_LN(1, 256)
-  if constexpr (GRAD) {
-    MOE_LN(1, 512)
-    MOE_LN(1, 1024)
-  } else {
-    MOE_LN(2, 256)
-  }
+  MOE_LN(1, 512)
+  MOE_LN(1, 1024)
   MOE_LN(2, 1024)
   if constexpr (!BF) MOE_LN(4, 1024)
 #undef MOE_LN
@@ -340,13 +355,18 @@ hipError_t with_layout(int d, Launch go) {
 // fewer for few rows; each writes one partial row of 2 d floats.
 int grad_blocks(int n) { return n < 256 ? n : 256; }
 
+// Threads per CU of the forward pass: more rows at once repeat more of w and
+// b's loads, fewer leave HBM idle (8192 rows of 4096 bf16: 512 threads 37.6,
+// 1024 33.8, 2048 36.4, 4096 48.3 us).
+constexpr int kRowThreads = 1024;
+
 template <bool BF, bool TAIL>
 hipError_t launch_fwd(const void *x, const float *w, const float *b, float eps, int n, int d, void *y,
                       float *mean, float *rstd, hipStream_t st) {
-  return with_layout<BF, TAIL, false>(d, [&](auto cc, auto tt) {
+  return with_layout<BF, TAIL>(d, [&](auto cc, auto tt) {
     constexpr int C = decltype(cc)::value, TPR = decltype(tt)::value;
     constexpr int NT = TPR > 256 ? TPR : 256, G = NT / TPR;
-    const int want = (n + G - 1) / G, cap = 256 * 2048 / NT;  // every CU full
+    const int want = (n + G - 1) / G, cap = 256 * kRowThreads / NT;
     layer_norm_kernel<BF, TAIL, C, TPR><<<want < cap ? want : cap, NT, 0, st>>>(x, w, b, eps, n, d, y,
                                                                              mean, rstd);
     return hipGetLastError();
@@ -358,7 +378,7 @@ hipError_t launch_grad(const void *dy, const void *x, const float *w, const floa
                        const float *rstd, int n, int d, void *dx, float *dw, float *db, float *part,
                        hipStream_t st) {
   int P = 0;
-  const hipError_t e = with_layout<BF, TAIL, true>(d, [&](auto cc, auto tt) {
+  const hipError_t e = with_layout<BF, TAIL>(d, [&](auto cc, auto tt) {
     constexpr int C = decltype(cc)::value, TPR = decltype(tt)::value;
     constexpr int G = kGradThreads / TPR;
     P = grad_blocks((n + G - 1) / G);

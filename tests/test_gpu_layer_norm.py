@@ -19,9 +19,9 @@ pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 SIZES = {
-    "bf16": [(1, 8), (3, 16), (7, 136), (65, 512), (33, 520), (2, 2048), (1, 4096), (300, 4096), (5, 4104),
+    "bf16": [(2, 1024), (1, 8), (3, 16), (7, 136), (65, 512), (33, 520), (2, 2048), (1, 4096), (300, 4096), (5, 4104),
              (9, 8192), (3, 8200), (2, 16384), (5000, 64), (2600, 1024)],
-    "f32": [(1, 1), (2, 3), (5, 17), (6, 64), (7, 65), (9, 255), (4, 257), (33, 1021), (5, 1024), (3, 2047),
+    "f32": [(4, 511), (1, 1), (2, 3), (5, 17), (6, 64), (7, 65), (9, 255), (4, 257), (33, 1021), (5, 1024), (3, 2047),
             (9, 2049), (3, 4097), (2, 8193), (2, 16383), (1, 16384), (5000, 33), (2600, 500)],
 }
 CASES = [(t, n, d) for t in SIZES for n, d in SIZES[t]]
