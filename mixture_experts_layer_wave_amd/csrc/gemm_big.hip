@@ -87,13 +87,9 @@ __device__ __forceinline__ void lgkm_wait0() {
 
 // Up: H rows [row0, row0 + rows) in ro (row pitch N bf16) = silu(gate) * value,
 // gate = acc[tm][j], value = acc[tm][j + TN/2].  TM * TN stores per wave.
-// SAVE: gate and value, each rounded once, go to rg and ru too (H is formed
-// from the float32 values).
-template <int TM, int TN, int WM, int WN, bool SAVE>
+template <int TM, int TN, int WM, int WN>
 __device__ __forceinline__ void store_swiglu_regs(const f32x16 (&acc)[TM][TN],
-                                                  __amdgpu_buffer_rsrc_t ro,
-                                                  __amdgpu_buffer_rsrc_t rg,
-                                                  __amdgpu_buffer_rsrc_t ru, int N, int rows,
+                                                  __amdgpu_buffer_rsrc_t ro, int N, int rows,
                                                   int n0, int wm, int wn) {
   // (the lane id is read afresh: lane-derived values of the K loop are
   // not kept live across it for the epilogue)
@@ -121,18 +117,54 @@ __device__ __forceinline__ void store_swiglu_regs(const f32x16 (&acc)[TM][TN],
         const uint32_t off =
             (r < rows && col < N) ? (rowoff + (uint32_t)(tm * 32 * N) + col) * 2u : kOOB;
         __builtin_amdgcn_raw_buffer_store_b128(o, ro, off, 0, 0);
-        if constexpr (SAVE) {
+      }
+    }
+  }
+}
+
+// Up, keeping the pre-activations: gate to rg, value to ru, H to ro, each
+// rounded once (H is formed from the float32 values).  Three matrices make
+// the way of the stores matter: gate and value pass through the wave's own
+// piece of LDS (float32, 32 rows x 32 columns each, rows 144 bytes apart), so
+// that an instruction writes 64 bytes of each of 16 rows instead of 32 bytes
+// of each of 32 (Switch layer: 94 -> 88 us).  The caller has made the
+// stages free (barrier).
+constexpr int kSavePitch = 36;                        // floats per row
+constexpr int kSavePiece = 2 * 32 * kSavePitch;       // floats per wave
+template <int TM, int TN, int WM, int WN>
+__device__ __forceinline__ void store_swiglu_save(const f32x16 (&acc)[TM][TN], __amdgpu_buffer_rsrc_t ro,
+                                                  __amdgpu_buffer_rsrc_t rg, __amdgpu_buffer_rsrc_t ru,
+                                                  int N, int rows, int n0, int wm, int wn, float *piece) {
+  static_assert(TN == 2, "one gate and one value column group per wave");
+  const int lane = __lane_id();
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const f32x16 &x = acc[tm][v ? j + TN / 2 : j];
-            const u32x4 q = swap_halves(pack_bf16x2(x[8 * h], x[8 * h + 1]),
-                                        pack_bf16x2(x[8 * h + 2], x[8 * h + 3]),
-                                        pack_bf16x2(x[8 * h + 4], x[8 * h + 5]),
-                                        pack_bf16x2(x[8 * h + 6], x[8 * h + 7]));
-            __builtin_amdgcn_raw_buffer_store_b128(q, v ? ru : rg, off, 0, 0);
-          }
+  for (int tm = 0; tm < TM; ++tm) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *(f32x4 *)(piece + (v * 32 + (lane & 31)) * kSavePitch + g * 8 + (lane >> 5) * 4) =
+            f32x4{acc[tm][v][g * 4], acc[tm][v][g * 4 + 1], acc[tm][v][g * 4 + 2], acc[tm][v][g * 4 + 3]};
+    const int col = n0 + wn * (WN / 2) + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = 16 * i + (lane >> 2), r = wm * WM + tm * 32 + row;
+      const float *p = piece + row * kSavePitch + (lane & 3) * 8;
+      u32x4 h, g, u;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const f32x4 gv = *(const f32x4 *)(p + 4 * q), uv = *(const f32x4 *)(p + 32 * kSavePitch + 4 * q);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          g[2 * q + x] = pack_bf16x2(gv[2 * x], gv[2 * x + 1]);
+          u[2 * q + x] = pack_bf16x2(uv[2 * x], uv[2 * x + 1]);
+          h[2 * q + x] = pack_bf16x2(silu(gv[2 * x]) * uv[2 * x], silu(gv[2 * x + 1]) * uv[2 * x + 1]);
         }
       }
+      const uint32_t off = (r < rows && col < N) ? ((uint32_t)r * (uint32_t)N + (uint32_t)col) * 2u : kOOB;
+      __builtin_amdgcn_raw_buffer_store_b128(h, ro, off, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(g, rg, off, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(u, ru, off, 0, 0);
     }
   }
 }
@@ -432,9 +464,17 @@ __global__ __launch_bounds__(kNT, 1) void big_gemm_kernel(BigGemmParams p) {
   if constexpr (UP) {
     const uint32_t bytes = (uint32_t)rows * (uint32_t)N * 2u;
     const __amdgpu_buffer_rsrc_t ro = rsrc((uint16_t *)p.out + (size_t)row0 * N, bytes);
-    store_swiglu_regs<T::TM, T::TN, T::WM, T::WN, SAVE>(
-        acc, ro, SAVE ? rsrc((uint16_t *)p.out_g + (size_t)row0 * N, bytes) : ro,
-        SAVE ? rsrc((uint16_t *)p.out_u + (size_t)row0 * N, bytes) : ro, N, rows, n0, wm, wn);
+    if constexpr (SAVE) {
+      static_assert(kNW * kSavePiece * 4 <= 2 * T::STAGE, "the pieces fit the stages");
+      wait_vmcnt<0>();  // (the last step's copies, which nobody reads)
+      __syncthreads();
+      store_swiglu_save<T::TM, T::TN, T::WM, T::WN>(
+          acc, ro, rsrc((uint16_t *)p.out_g + (size_t)row0 * N, bytes),
+          rsrc((uint16_t *)p.out_u + (size_t)row0 * N, bytes), N, rows, n0, wm, wn,
+          (float *)smem + wave * kSavePiece);
+    } else {
+      store_swiglu_regs<T::TM, T::TN, T::WM, T::WN>(acc, ro, N, rows, n0, wm, wn);
+    }
   } else if constexpr (FUSE) {
     store_scaled_rows_regs<T::TM, T::TN, T::WM, T::WN>(
         acc, rsrc(p.out, (uint32_t)p.fuse_rows * (uint32_t)N * 2u), N, p.perm_out, p.comb_w, row0,
@@ -684,7 +724,7 @@ __global__ __launch_bounds__(kNT, 1) void mxdq_gemm_kernel(BigGemmParams p) {
   }
   if constexpr (UP) {
     const __amdgpu_buffer_rsrc_t ro = rsrc((uint16_t *)p.out + (size_t)row0 * N, (uint32_t)rows * N * 2u);
-    store_swiglu_regs<T::TM, T::TN, T::WM, T::WN, false>(acc, ro, ro, ro, N, rows, n0, wm, wn);
+    store_swiglu_regs<T::TM, T::TN, T::WM, T::WN>(acc, ro, N, rows, n0, wm, wn);
   } else if constexpr (FUSE) {
     store_scaled_rows_regs<T::TM, T::TN, T::WM, T::WN>(
         acc, rsrc(p.out, (uint32_t)p.fuse_rows * (uint32_t)N * 2u), N, p.perm_out, p.comb_w, row0, rows,
