@@ -1,10 +1,9 @@
 // Grouped bf16 products of the expert FFN's gradient (gemm_grad.h has the
 // formulas).
 //
-//   DH   dh0 = dy W2            rows x d_ff, K = d       (and the epilogue's dg, du, w h)
-//   DX   da  = dg W1 + du W3    rows x d,    K = 2 d_ff  (two ranges of d_ff)
-//   DW13 dW1 = dg^T a, dW3 = du^T a   d_ff x d, K = the pile's rows
-//   DW2  dW2 = dy^T (w h)             d x d_ff, K = the pile's rows
+//   DH  dh0 = dy W2            rows x d_ff, K = d       (and the epilogue's dg, du, w h)
+//   DX  da  = dg W1 + du W3    rows x d,    K = 2 d_ff  (two ranges of d_ff)
+//   weight gradients  dW1 = dg^T a, dW3 = du^T a, dW2 = dy^T (w h),  K = the pile's rows
 //
 // In the forward products both operands are contiguous along K.  Here the
 // weights of DH and DX and both operands of the weight gradients are
@@ -14,12 +13,13 @@
 // which transposes a 4 x 16 block of 16-bit values among 16 lanes.  No
 // operand is ever transposed in memory.
 //
-// Block: 8 waves arranged 2 x 4, tile BM x BN, K steps of 64 through two LDS
-// stages filled by direct-to-LDS copies, MFMA 32x32x16, f32 accumulators,
-// the K loop rotated by one slice against its barriers as in the forward
-// GEMM (gemm_big.hip).  Loads past a buffer's record count return zero:
+// Block: 8 waves arranged 2 x 4 (or 4 waves 2 x 2), K steps of 64 (32) through
+// two LDS stages filled by direct-to-LDS copies, MFMA 32x32x16, f32
+// accumulators, the K loop rotated by one slice against its barriers as in
+// the forward GEMM (gemm_big.hip).  Loads past a buffer's record count return zero:
 // that fills ragged rows, columns and the K tail.
 #include <atomic>
+#include <type_traits>
 
 #include "common.h"
 #include "gemm_common.h"
@@ -33,19 +33,20 @@ namespace {
 
 using namespace gemm;
 
-enum Mode { DH, DX, DW13, DW2 };
+enum Mode { DH, DX };
 
-struct GradParams {
-  const uint16_t *a0, *a1;  // DH dy; DX dg, du; DW13 dg, du; DW2 dy
-  const uint16_t *b0, *b1;  // DH W2; DX W1, W3; DW13 a; DW2 w h
-  uint32_t src_bytes;       // bytes of the gathered matrix (dy or a)
-  const int32_t *perm;      // gather of dy / a, or NULL
+// The products over pile rows.
+struct RowParams {
+  const uint16_t *a0, *a1;  // DH dy; DX dg, du
+  const uint16_t *b0, *b1;  // DH W2; DX W1, W3
+  uint32_t src_bytes;       // bytes of the gathered matrix (dy)
+  const int32_t *perm;      // gather of dy, or NULL
   const int32_t *offsets;
   const int32_t *slot;
   int n_slots;
   int E, R, d, f;
-  int n_mt, n_nt;           // tiles along the output's rows (weight gradients) and columns
-  void *c0, *c1;            // DX da; DW13 dW1, dW3; DW2 dW2
+  int n_nt;                 // column tiles
+  uint16_t *c;              // DX: da
   // DX with few blocks: K in `splits` ranges, range s of every tile to the
   // float32 plane dx_part[s][R][d]; the planes are added later, in order.
   int splits;
@@ -57,6 +58,18 @@ struct GradParams {
   const int32_t *inv;
   const float *topk_w;
   int k;
+};
+
+// The weight gradients: dW1 = dg^T a and dW3 = du^T a (f x d), dW2 = dy^T hs
+// (d x f), all sums over a pile's rows of a pile matrix (dg, du, hs: [R][f])
+// and a gathered one (a, dy: d wide).
+struct WeightParams {
+  const uint16_t *pile[3], *src[3];  // dW1, dW3, dW2: pile matrix and gathered matrix
+  uint16_t *out[3];
+  uint32_t src_bytes;
+  const int32_t *perm, *offsets;
+  int E, d, f;
+  int ft, dt;                        // tiles along f and d
 };
 
 __device__ __forceinline__ void lgkm_wait0() {
@@ -158,13 +171,19 @@ __device__ __forceinline__ void store_lines_f32(const f32x16 (&acc)[TM][TN], __a
     }
 }
 
-// DH: g and u come and dg, du, w h go as such lines.  dh0, h and the products
-// stay float32; dg, du and w h are rounded once to bf16, the type of the MFMA
-// that reads them next.  The row sums of dh0 h over 64 columns go to
-// part[column / 64][row].  s_w: combine weights of the tile's rows.
-template <int TM, int TN, int WM, int WN>
-__device__ __forceinline__ void store_dh(const f32x16 (&acc)[TM][TN], const GradParams &p, const float *s_w,
+// DH: g and u come and dg, du, w h go as such lines.  ALONE (one block per
+// CU): g and u of a piece of the tile are on their way while the piece before
+// it is worked on, the first one's before the barrier that frees the stages,
+// and the stores carry the non-temporal hint (Mixtral-shaped, 8 experts, 4096
+// x 14336, 16384 rows: 2240 -> 2133 us); blocks that share a CU overlap each
+// other and keep the registers.  dh0, h and the products stay float32; dg, du
+// and w h are rounded once to bf16, the type of the MFMA that reads them next.
+// The row sums of dh0 h over 64 columns go to part[column / 64][row].  s_w:
+// combine weights of the tile's rows.
+template <int TM, int TN, int WM, int WN, bool ALONE>
+__device__ __forceinline__ void store_dh(const f32x16 (&acc)[TM][TN], const RowParams &p, const float *s_w,
                                          int row0, int rows, int n0, int wm, int wn, float *piece) {
+  constexpr int NP = TM * (TN / 2);  // pieces of 32 rows x 64 columns
   const int lane = __lane_id();
   const int N = p.f;
   const size_t base = (size_t)row0 * N;
@@ -172,77 +191,166 @@ __device__ __forceinline__ void store_dh(const f32x16 (&acc)[TM][TN], const Grad
   const __amdgpu_buffer_rsrc_t rg = rsrc(p.g + base, bytes), ru = rsrc(p.u + base, bytes);
   const __amdgpu_buffer_rsrc_t rdg = rsrc(p.dg + base, bytes), rdu = rsrc(p.du + base, bytes),
                                rhs = rsrc(p.hs + base, bytes);
+  auto row_of = [&](int q, int i) { return wm * WM + q / (TN / 2) * 32 + 8 * i + (lane >> 3); };
+  auto offset = [&](int q, int i) {
+    const int r = row_of(q, i), col = n0 + wn * WN + q % (TN / 2) * 64 + (lane & 7) * 8;
+    return (r < rows && col < N) ? ((uint32_t)r * (uint32_t)N + (uint32_t)col) * 2u : kOOB;
+  };
+  constexpr int NB = ALONE ? 2 : 1, AUX = ALONE ? 2 : 0;
+  u32x4 gq[NB][4], uq[NB][4];
+  auto load = [&](int q) {
 #pragma unroll
-  for (int tm = 0; tm < TM; ++tm)
-#pragma unroll
-    for (int jj = 0; jj < TN / 2; ++jj) {
-      const int c0 = n0 + wn * WN + jj * 64, col = c0 + (lane & 7) * 8;
-      uint32_t off[4];
-      u32x4 gq[4], uq[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = wm * WM + tm * 32 + 8 * i + (lane >> 3);
-        off[i] = (r < rows && col < N) ? ((uint32_t)r * (uint32_t)N + (uint32_t)col) * 2u : kOOB;
-        gq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rg, off[i], 0, 0));
-        uq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ru, off[i], 0, 0));
-      }
-      epi_put<TM, TN>(acc, tm, jj, piece);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = wm * WM + tm * 32 + 8 * i + (lane >> 3);
-        const float wr = s_w[r];
-        float dh[8], sum = 0.f;
-        epi_get(piece, i, dh);
-        u32x4 odg, odu, ohs;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float dgv[2], duv[2], hv[2];
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const float g = __uint_as_float(b ? gq[i][q] & 0xffff0000u : gq[i][q] << 16);
-            const float u = __uint_as_float(b ? uq[i][q] & 0xffff0000u : uq[i][q] << 16);
-            const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
-            const float a = g * s;  // silu(g)
-            const float d0 = dh[2 * q + b];
-            sum = fmaf(d0, a * u, sum);
-            const float dw = d0 * wr;
-            duv[b] = dw * a;
-            dgv[b] = dw * u * fmaf(a, 1.0f - s, s);  // silu'(g) = s + g s (1 - s)
-            hv[b] = wr * (a * u);
-          }
-          odg[q] = pack_bf16x2(dgv[0], dgv[1]);
-          odu[q] = pack_bf16x2(duv[0], duv[1]);
-          ohs[q] = pack_bf16x2(hv[0], hv[1]);
-        }
-        __builtin_amdgcn_raw_buffer_store_b128(odg, rdg, off[i], 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(odu, rdu, off[i], 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(ohs, rhs, off[i], 0, 0);
-        sum = group_sum(sum, 8);
-        if (p.part && (lane & 7) == 0 && r < rows && c0 < N)
-          p.part[(size_t)(c0 / 64) * p.R + row0 + r] = sum;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t off = offset(q, i);
+      gq[q % NB][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rg, off, 0, 0));
+      uq[q % NB][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ru, off, 0, 0));
     }
+  };
+  load(0);
+  lds_barrier();  // every wave is done with the stages
+#pragma unroll
+  for (int q = 0; q < NP; ++q) {
+    if (ALONE && q + 1 < NP) load(q + 1);
+    if (!ALONE && q > 0) load(q);
+    if constexpr (ALONE) __builtin_amdgcn_sched_barrier(0);
+    epi_put<TM, TN>(acc, q / (TN / 2), q % (TN / 2), piece);
+    const int c0 = n0 + wn * WN + q % (TN / 2) * 64;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = row_of(q, i);
+      const uint32_t off = offset(q, i);
+      const float wr = s_w[r];
+      float dh[8], sum = 0.f;
+      epi_get(piece, i, dh);
+      u32x4 odg, odu, ohs;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float dgv[2], duv[2], hv[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t gb = gq[q % NB][i][x], ub = uq[q % NB][i][x];
+          const float g = __uint_as_float(b ? gb & 0xffff0000u : gb << 16);
+          const float u = __uint_as_float(b ? ub & 0xffff0000u : ub << 16);
+          const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
+          const float a = g * s;  // silu(g)
+          const float d0 = dh[2 * x + b];
+          sum = fmaf(d0, a * u, sum);
+          const float dw = d0 * wr;
+          duv[b] = dw * a;
+          dgv[b] = dw * u * fmaf(a, 1.0f - s, s);  // silu'(g) = s + g s (1 - s)
+          hv[b] = wr * (a * u);
+        }
+        odg[x] = pack_bf16x2(dgv[0], dgv[1]);
+        odu[x] = pack_bf16x2(duv[0], duv[1]);
+        ohs[x] = pack_bf16x2(hv[0], hv[1]);
+      }
+      __builtin_amdgcn_raw_buffer_store_b128(odg, rdg, off, 0, AUX);
+      __builtin_amdgcn_raw_buffer_store_b128(odu, rdu, off, 0, AUX);
+      __builtin_amdgcn_raw_buffer_store_b128(ohs, rhs, off, 0, AUX);
+      sum = group_sum(sum, 8);
+      if (p.part && (lane & 7) == 0 && r < rows && c0 < N)
+        p.part[(size_t)(c0 / 64) * p.R + row0 + r] = sum;
+    }
+  }
 }
 
-// A set of tiles: BM x BN of the products over pile rows and of the weight
-// gradients, waves per block, K step, waves per SIMD asked of the register
-// allocator, and the blocks per CU that da's split K aims at.
-template <int RBM_, int RBN_, int WBM_, int WBN_, int NW_, int BK_, int OCC_, int HOLD_>
+// A set of tiles: BM x BN of the products over pile rows, WB x WB of the
+// weight gradients, waves per block, K step, waves per SIMD asked of the
+// register allocator, and the blocks per CU that da's split K aims at.
+template <int RBM_, int RBN_, int WB_, int NW_, int BK_, int OCC_, int HOLD_>
 struct Cfg {
-  static constexpr int RBM = RBM_, RBN = RBN_, WBM = WBM_, WBN = WBN_, NW = NW_, BK = BK_, OCC = OCC_;
-  static constexpr int HOLD = HOLD_;
+  static constexpr int RBM = RBM_, RBN = RBN_, WB = WB_, NW = NW_, BK = BK_, OCC = OCC_, HOLD = HOLD_;
   static constexpr int NT = NW * 64;
   static constexpr int max(int a, int b) { return a > b ? a : b; }
-  // stages, or the epilogue's pieces (and the rows' combine weights)
-  static constexpr int EPI = NW * kEpiWave + RBM * 4;
+  // stages, or the epilogue's pieces
+  static constexpr int EPI = NW * kEpiWave;
   static constexpr int ROW_LDS = max(2 * (RBM + RBN) * BK * 2, EPI);
-  static constexpr int WEIGHT_LDS = max(2 * (WBM + WBN) * BK * 2, EPI);
+  static constexpr int WEIGHT_LDS = max(4 * WB * BK * 2, EPI);
 };
 
-// One block's tile; `block` counts from the product's first block.
+// fn(integral_constant<ACT>) for act = 0 .. TM, the number of this wave's
+// 32-row groups that hold rows.
+template <int TM, typename F>
+__device__ __forceinline__ void by_act(int act, F fn) {
+  static_assert(TM >= 2 && TM <= 5, "row groups per wave");
+  if (act == TM) {
+    fn(std::integral_constant<int, TM>{});
+  } else if (act == 0) {
+    fn(std::integral_constant<int, 0>{});
+  } else if (act == 1) {
+    fn(std::integral_constant<int, 1>{});
+  } else if constexpr (TM >= 3) {
+    if (act == 2) {
+      fn(std::integral_constant<int, 2>{});
+    } else if constexpr (TM >= 4) {
+      if (act == 3) {
+        fn(std::integral_constant<int, 3>{});
+      } else if constexpr (TM >= 5) {
+        fn(std::integral_constant<int, 4>{});
+      }
+    }
+  }
+}
+
+// The K loop over nk > 0 steps, of which step 0's copies have been issued:
+// issue(kt, stage) copies a step, read_frags reads a slice's fragments (READS
+// LDS reads with ACT row groups), mfmas multiplies them.  Rotated by one slice
+// against its barriers: the last slice's products run after the barrier that
+// publishes the next stage, over that stage's first reads.
+template <int ACT, int TM, int TN, int SLICES, int READS, typename Issue, typename Read, typename Mul>
+__device__ __forceinline__ void k_loop(const uint8_t *smem, int stage_bytes, int nk, Issue issue, Read read_frags,
+                                       Mul mfmas) {
+  constexpr std::integral_constant<int, ACT> actc{};
+  constexpr int NF = ACT > 0 ? READS : 0, NM = ACT * TN;    // LDS reads and MFMAs per slice
+  constexpr int RPM = NM > 0 ? (NF + NM - 1) / NM : 1;      // reads per MFMA
+  wait_vmcnt<0>();
+  __syncthreads();
+  bf16x8 a0[TM], b0[TN], a1[TM], b1[TN];
+  read_frags(actc, smem, 0, a0, b0);
+  issue(1, 1);
+  __builtin_amdgcn_sched_barrier(0);
+  auto slices = [&](int st) {
+    const uint8_t *sa = smem + st * stage_bytes;
+#pragma unroll
+    for (int kk = 0; kk + 1 < SLICES; ++kk) {
+      bf16x8 *ac = (kk & 1) ? a1 : a0, *bc = (kk & 1) ? b1 : b0;
+      bf16x8 *an = (kk & 1) ? a0 : a1, *bn = (kk & 1) ? b0 : b1;
+      read_frags(actc, sa, kk + 1, an, bn);
+      mfmas(actc, ac, bc);
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (i * RPM < NF) __builtin_amdgcn_sched_group_barrier(0x100, RPM, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  for (int kt = 0; kt + 1 < nk; ++kt) {
+    const int st = kt & 1;
+    slices(st);
+    // This stage's copies have landed and the last slice's fragments are in
+    // registers on every wave before anyone copies into it again.
+    wait_vmcnt<0>();
+    lgkm_wait0();
+    __syncthreads();
+    read_frags(actc, smem + (st ^ 1) * stage_bytes, 0, a0, b0);
+    mfmas(actc, a1, b1);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+    for (int i = 0; i < NM; ++i) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    issue(kt + 2, st);
+  }
+  slices((nk - 1) & 1);
+  mfmas(actc, a1, b1);
+}
+
+// One block's tile of DH or DX; `block` counts from the product's first block.
+// s_w (DH): room for the combine weights of the tile's rows.
 template <Mode MODE, bool GATHER, int BM, int BN, int NW, int BK>
-__device__ __forceinline__ void grad_tile(const GradParams &p, int block, uint8_t *smem, TileSlot &s_t) {
-  constexpr bool WEIGHT = MODE == DW13 || MODE == DW2;  // A is K-major too
+__device__ __forceinline__ void row_tile(const RowParams &p, int block, uint8_t *smem, TileSlot &s_t,
+                                         float *s_w = nullptr) {
   constexpr int WM = BM / 2, WN = BN / (NW / 2), TM = WM / 32, TN = WN / 32;
   constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE = A_BYTES + B_BYTES;
   constexpr int A_RUNS = A_BYTES / 1024 / NW, B_RUNS = B_BYTES / 1024 / NW;
@@ -250,124 +358,57 @@ __device__ __forceinline__ void grad_tile(const GradParams &p, int block, uint8_
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int N = MODE == DH || MODE == DW2 ? p.f : p.d;  // output columns
+  const int N = MODE == DH ? p.f : p.d;  // output columns
 
   // ---- block -> tile ------------------------------------------------------
-  int e, nt, m0, rows;  // output rows m0 .. m0 + rows (pile rows, or weight rows of the expert)
-  int nk;               // K steps
-  int kcount;           // K of one range
-  int kt0 = 0;          // first step of this block's K range (DX)
-  int split = 0;
-  bool second = false;  // DW13: the tile is dW3's
-  int pile0 = 0;        // weight gradients: the pile's first row
-  if constexpr (!WEIGHT) {
-    const int S = MODE == DX ? p.splits : 1;
-    if (wave == 0) map_block<BM, false, true>(p.offsets, p.E, p.n_nt, S, lane, &s_t, S, 4);
-    __syncthreads();
-    e = s_t.e;
-    if (e < 0) return;
-    nt = s_t.nt;
-    m0 = s_t.row0;
-    rows = s_t.rows;
-    kcount = MODE == DH ? p.d : p.f;
-    nk = (kcount + BK - 1) / BK * (MODE == DX ? 2 : 1);
-    if (MODE == DX && S > 1) {
-      split = s_t.split;
-      kt0 = (int)((long long)split * nk / S);
-      nk = (int)((long long)(split + 1) * nk / S) - kt0;
-    }
-  } else {
-    // Every XCD (block b runs on XCD b mod 8) takes an eighth of each
-    // expert's tiles, so that all have the same share of large and small
-    // piles; within it, groups of eight row tiles column by column.
-    const int T = p.n_mt * p.n_nt, per = (T + 7) / 8;
-    const int slot = block >> 3;
-    e = slot / per;
-    const int tile = (block & 7) * per + slot % per;
-    if (tile >= T) return;
-    constexpr int RG = 8;
-    const int grp = tile / (RG * p.n_nt), within = tile - grp * RG * p.n_nt;
-    const int gr = min(RG, p.n_mt - grp * RG);
-    nt = within / gr;
-    int mt = grp * RG + within % gr;
-    const int M = MODE == DW13 ? p.f : p.d;
-    if (MODE == DW13 && mt >= p.n_mt / 2) {
-      second = true;
-      mt -= p.n_mt / 2;
-    }
-    m0 = mt * BM;
-    rows = min(BM, M - m0);
-    pile0 = p.offsets[e];
-    kcount = p.offsets[e + 1] - pile0;
-    nk = (kcount + BK - 1) / BK;
+  const int S = MODE == DX ? p.splits : 1;
+  if (wave == 0) map_block<BM, false, true>(p.offsets, p.E, p.n_nt, S, lane, &s_t, S, 4, block);
+  __syncthreads();
+  const int e = s_t.e;
+  if (e < 0) return;
+  const int m0 = s_t.row0, rows = s_t.rows, n0 = s_t.nt * BN;
+  const int kcount = MODE == DH ? p.d : p.f;  // K of one range
+  int nk = (kcount + BK - 1) / BK * (MODE == DX ? 2 : 1);
+  int kt0 = 0, split = 0;  // first step of this block's K range
+  if (MODE == DX && S > 1) {
+    split = s_t.split;
+    kt0 = (int)((long long)split * nk / S);
+    nk = (int)((long long)(split + 1) * nk / S) - kt0;
   }
-  const int n0 = nt * BN;
 
   // ---- operands -------------------------------------------------------------
-  const int lda = WEIGHT ? (MODE == DW13 ? p.f : p.d) : kcount;  // A's row pitch
-  const int ldb = N;
-  constexpr bool A_GATHER = GATHER && (MODE == DH || MODE == DW2);
-  constexpr bool B_GATHER = GATHER && MODE == DW13;
-  // A pile's rows start at m0 (row products) or pile0; gathered matrices are
-  // addressed from their start.
-  const size_t a_first = A_GATHER ? 0 : (size_t)(WEIGHT ? pile0 : m0) * lda;
-  const uint32_t a_bytes = A_GATHER ? p.src_bytes : (uint32_t)(WEIGHT ? kcount : rows) * (uint32_t)lda * 2u;
-  const uint16_t *a_base = (MODE == DW13 && second ? p.a1 : p.a0) + a_first;
-  const __amdgpu_buffer_rsrc_t ra0 = rsrc(a_base, a_bytes);
+  constexpr bool A_GATHER = GATHER && MODE == DH;
+  const size_t a_first = A_GATHER ? 0 : (size_t)m0 * kcount;
+  const uint32_t a_bytes = A_GATHER ? p.src_bytes : (uint32_t)rows * (uint32_t)kcount * 2u;
+  const __amdgpu_buffer_rsrc_t ra0 = rsrc(p.a0 + a_first, a_bytes);
   const __amdgpu_buffer_rsrc_t ra1 = MODE == DX ? rsrc(p.a1 + a_first, a_bytes) : ra0;
-  size_t b_first;
-  uint32_t b_bytes;
-  if constexpr (!WEIGHT) {
-    b_first = (size_t)phys_slot(p.slot, p.n_slots, e) * p.d * p.f;
-    b_bytes = (uint32_t)p.d * (uint32_t)p.f * 2u;
-  } else {
-    b_first = B_GATHER ? 0 : (size_t)pile0 * ldb;
-    b_bytes = B_GATHER ? p.src_bytes : (uint32_t)kcount * (uint32_t)ldb * 2u;
-  }
+  const size_t b_first = (size_t)phys_slot(p.slot, p.n_slots, e) * p.d * p.f;
+  const uint32_t b_bytes = (uint32_t)p.d * (uint32_t)p.f * 2u;
   const __amdgpu_buffer_rsrc_t rb0 = rsrc(p.b0 + b_first, b_bytes);
   const __amdgpu_buffer_rsrc_t rb1 = MODE == DX ? rsrc(p.b1 + b_first, b_bytes) : rb0;
 
   // ---- per-lane copy offsets --------------------------------------------------
   // K-major tile of W columns: run q fills 1024 / (2 W) rows; lane i of run
-  // NW j + wave has row kr + j KROWS, stored chunk i % (W / 8).
-  constexpr int A_CPR = WEIGHT ? BM / 8 : 8, B_CPR = BN / 8;  // chunks per K-major row
-  constexpr int A_RPR = 64 / A_CPR, B_RPR = 64 / B_CPR;     // rows per run
+  // NW j + wave has row kr + j NW RPR, stored chunk i % (W / 8).
+  constexpr int B_CPR = BN / 8, B_RPR = 64 / B_CPR;  // chunks per row, rows per run
   const int b_kr = wave * B_RPR + lane / B_CPR;
   const int b_col = n0 + (((lane % B_CPR) ^ kmaj_key<BN>(b_kr)) << 3);
   const uint32_t b_pen = b_col < N ? 0u : kOOB;
-  const int a_kr = wave * A_RPR + lane / A_CPR;
-  int a_col = 0;
-  if constexpr (WEIGHT) a_col = m0 + (((lane % A_CPR) ^ kmaj_key<BM>(a_kr)) << 3);
-  const uint32_t a_pen = WEIGHT && a_col >= lda ? kOOB : 0u;
-  static_assert((NW * A_RPR) % 4 == 0 && (NW * B_RPR) % 4 == 0, "a lane's key is the same in every run");
+  static_assert((NW * B_RPR) % 4 == 0, "a lane's key is the same in every run");
   // Row-major A tile: as in the forward GEMM.
   const int c = dma_chunk<BK * 2>(wave, lane);
   constexpr int RPR = 1024 / (BK * 2), RUN_ROWS = NW * RPR;  // rows of a run, and of all waves' runs
   const int a_r = wave * RPR + lane / (BK / 8);
-  uint32_t a_off[!WEIGHT ? A_RUNS : 1];
-  if constexpr (!WEIGHT) {
-    int src[A_RUNS];
+  uint32_t a_off[A_RUNS];
+  int src[A_RUNS];
 #pragma unroll
-    for (int j = 0; j < A_RUNS; ++j) {
-      const int r = a_r + j * RUN_ROWS;
-      src[j] = A_GATHER ? p.perm[m0 + min(r, rows - 1)] : r;
-    }
-#pragma unroll
-    for (int j = 0; j < A_RUNS; ++j)
-      a_off[j] = a_r + j * RUN_ROWS < rows ? ((uint32_t)src[j] * (uint32_t)lda + (uint32_t)c * 8u) * 2u : kOOB;
+  for (int j = 0; j < A_RUNS; ++j) {
+    const int r = a_r + j * RUN_ROWS;
+    src[j] = A_GATHER ? p.perm[m0 + min(r, rows - 1)] : r;
   }
-  // Gathered K-major operand: the token of each of this lane's K rows of the
-  // next step, loaded one step ahead of the copies that use it.
-  constexpr int K_RUNS = A_GATHER ? A_RUNS : B_RUNS;
-  const int g_kr = A_GATHER ? a_kr : b_kr;
-  constexpr int G_ROWS = NW * (A_GATHER ? A_RPR : B_RPR);
-  int tok[WEIGHT && GATHER ? K_RUNS : 1];
-  auto load_tokens = [&](int kt) {
-    if constexpr (WEIGHT && GATHER)
 #pragma unroll
-      for (int j = 0; j < K_RUNS; ++j)
-        tok[j] = p.perm[pile0 + min(kt * BK + g_kr + j * G_ROWS, kcount - 1)];
-  };
+  for (int j = 0; j < A_RUNS; ++j)
+    a_off[j] = a_r + j * RUN_ROWS < rows ? ((uint32_t)src[j] * (uint32_t)kcount + (uint32_t)c * 8u) * 2u : kOOB;
 
   // Copies of K step kt into LDS stage `stage` (a step past the end is copied
   // and not used, or copies zeros).
@@ -376,28 +417,16 @@ __device__ __forceinline__ void grad_tile(const GradParams &p, int block, uint8_
     const bool sec = MODE == DX && kt0 + kt >= nk_range;
     const int k0 = (kt0 + kt - (sec ? nk_range : 0)) * BK;
     uint8_t *sa = smem + stage * STAGE, *sb = sa + A_BYTES;
-    if constexpr (!WEIGHT) {
-      const uint32_t pen = k0 + c * 8 < kcount ? 0u : kOOB;
+    const uint32_t pen = k0 + c * 8 < kcount ? 0u : kOOB;
 #pragma unroll
-      for (int j = 0; j < A_RUNS; ++j)
-        dma16(sec ? ra1 : ra0, sa + (NW * j + wave) * 1024, (a_off[j] + (uint32_t)k0 * 2u) | pen);
-    } else {
-#pragma unroll
-      for (int j = 0; j < A_RUNS; ++j) {
-        const int kr = k0 + a_kr + j * NW * A_RPR;
-        const uint32_t row = A_GATHER ? (uint32_t)tok[j] : (uint32_t)kr;
-        const uint32_t pen = kr < kcount ? a_pen : kOOB;
-        dma16(ra0, sa + (NW * j + wave) * 1024, ((row * (uint32_t)lda + (uint32_t)a_col) * 2u) | pen);
-      }
-    }
+    for (int j = 0; j < A_RUNS; ++j)
+      dma16(sec ? ra1 : ra0, sa + (NW * j + wave) * 1024, (a_off[j] + (uint32_t)k0 * 2u) | pen);
 #pragma unroll
     for (int j = 0; j < B_RUNS; ++j) {
       const int kr = k0 + b_kr + j * NW * B_RPR;
-      const uint32_t row = B_GATHER ? (uint32_t)tok[j] : (uint32_t)kr;
-      const uint32_t pen = kr < kcount ? b_pen : kOOB;
-      dma16(sec ? rb1 : rb0, sb + (NW * j + wave) * 1024, ((row * (uint32_t)ldb + (uint32_t)b_col) * 2u) | pen);
+      const uint32_t penb = kr < kcount ? b_pen : kOOB;
+      dma16(sec ? rb1 : rb0, sb + (NW * j + wave) * 1024, (((uint32_t)kr * (uint32_t)N + (uint32_t)b_col) * 2u) | penb);
     }
-    load_tokens(kt + 1);
   };
 
   const int wm = wave / (NW / 2), wn = wave % (NW / 2);
@@ -410,23 +439,16 @@ __device__ __forceinline__ void grad_tile(const GradParams &p, int block, uint8_
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
 
-  int a_lane[WEIGHT ? TM : 1], b_lane[TN];
+  int b_lane[TN];
 #pragma unroll
   for (int tn = 0; tn < TN; ++tn) b_lane[tn] = kmaj_lane<BN>(wn * WN + tn * 32, lane);
-  if constexpr (WEIGHT)
-#pragma unroll
-    for (int tm = 0; tm < TM; ++tm) a_lane[tm] = kmaj_lane<BM>(wm * WM + tm * 32, lane);
 
   auto read_frags = [&](auto actc, const uint8_t *sa, int kk, bf16x8 *af, bf16x8 *bfr) {
     constexpr int ACT = decltype(actc)::value;
     const uint8_t *sb = sa + A_BYTES;
 #pragma unroll
-    for (int tm = 0; tm < ACT; ++tm) {
-      if constexpr (WEIGHT)
-        af[tm] = kmaj_frag<BM>(sa, a_lane[tm], kk);
-      else
-        af[tm] = *(const bf16x8 *)(sa + swz<BK * 2>(wm * WM + tm * 32 + lr, kk * 2 + lg));
-    }
+    for (int tm = 0; tm < ACT; ++tm)
+      af[tm] = *(const bf16x8 *)(sa + swz<BK * 2>(wm * WM + tm * 32 + lr, kk * 2 + lg));
     if constexpr (ACT > 0) {
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn) bfr[tn] = kmaj_frag<BN>(sb, b_lane[tn], kk);
@@ -443,114 +465,190 @@ __device__ __forceinline__ void grad_tile(const GradParams &p, int block, uint8_
 
   auto kloop = [&](auto actc) {
     constexpr int ACT = decltype(actc)::value;
-    constexpr int NF = ACT > 0 ? ACT * (WEIGHT ? 2 : 1) + TN * 2 : 0;  // LDS reads per slice
-    constexpr int NM = ACT * TN;                                       // MFMAs per slice
-    constexpr int RPM = NM > 0 ? (NF + NM - 1) / NM : 1;               // reads per MFMA
-    wait_vmcnt<0>();
-    __syncthreads();
-    bf16x8 a0[TM], b0[TN], a1[TM], b1[TN];
-    read_frags(actc, smem, 0, a0, b0);
-    issue(1, 1);
-    __builtin_amdgcn_sched_barrier(0);
-    auto slices = [&](int st) {
-      const uint8_t *sa = smem + st * STAGE;
-#pragma unroll
-      for (int kk = 0; kk + 1 < SLICES; ++kk) {
-        bf16x8 *ac = (kk & 1) ? a1 : a0, *bc = (kk & 1) ? b1 : b0;
-        bf16x8 *an = (kk & 1) ? a0 : a1, *bn = (kk & 1) ? b0 : b1;
-        read_frags(actc, sa, kk + 1, an, bn);
-        mfmas(actc, ac, bc);
-#pragma unroll
-        for (int i = 0; i < NM; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          if (i * RPM < NF) __builtin_amdgcn_sched_group_barrier(0x100, RPM, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
-    for (int kt = 0; kt + 1 < nk; ++kt) {
-      const int st = kt & 1;
-      slices(st);
-      // This stage's copies have landed and the last slice's fragments are
-      // in registers on every wave before anyone copies into it again.
-      wait_vmcnt<0>();
-      lgkm_wait0();
-      __syncthreads();
-      read_frags(actc, smem + (st ^ 1) * STAGE, 0, a0, b0);
-      mfmas(actc, a1, b1);
-#pragma unroll
-      for (int i = 0; i < NF; ++i) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-#pragma unroll
-      for (int i = 0; i < NM; ++i) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_barrier(0);
-      issue(kt + 2, st);
+    k_loop<ACT, TM, TN, SLICES, ACT + TN * 2>(smem, STAGE, nk, issue, read_frags, mfmas);
+  };
+  issue(0, 0);
+  if constexpr (MODE == DH)  // the rows' combine weights, looked up under the first copies
+    for (int r = tid; r < BM; r += NW * 64)
+      s_w[r] = GATHER && r < rows ? pair_weight(p.inv, p.topk_w, p.k, p.perm[m0 + r], m0 + r) : 1.f;
+  by_act<TM>(__builtin_amdgcn_readfirstlane(min(TM, max(0, (rows - wm * WM + 31) / 32))), kloop);
+  wait_vmcnt<0>();
+
+  // ---- epilogue ---------------------------------------------------------------
+  float *piece = (float *)(smem + wave * kEpiWave);
+  if constexpr (MODE == DH) {
+    store_dh<TM, TN, WM, WN, NW == 8>(acc, p, s_w, m0, rows, n0, wm, wn, piece);
+  } else {
+    __syncthreads();  // every wave is done with the stages
+    if (S > 1) {
+      float *out = p.dx_part + ((size_t)split * p.R + m0) * N;
+      store_lines_f32<TM, TN, WM, WN>(acc, rsrc(out, (uint32_t)rows * (uint32_t)N * 4u), N, rows, n0, wm, wn,
+                                      piece);
+    } else {
+      uint16_t *out = p.c + (size_t)m0 * N;
+      store_lines<TM, TN, WM, WN, 0>(acc, rsrc(out, (uint32_t)rows * (uint32_t)N * 2u), N, rows, n0, wm, wn,
+                                     piece);
     }
-    slices((nk - 1) & 1);
-    mfmas(actc, a1, b1);
+  }
+}
+
+// ---- weight gradients ----------------------------------------------------------
+// A tile is a 256 (128) column range of the pile matrix against one of the
+// gathered matrix; dW1 and dW3 have the pile matrix's columns as their rows,
+// dW2 the gathered one's, which is a choice of LDS regions, so one loop takes
+// all three.
+struct WeightTile {
+  int e, which;       // 0 dW1, 1 dW3, 2 dW2
+  int f0, d0;
+  int pile0, kcount;  // the pile's rows
+};
+
+// The block's tile (false: none).  Every XCD (block b runs on XCD b mod 8)
+// takes an eighth of each expert's tiles of dW1 and dW3, then of dW2, so that
+// all have the same share of large and small piles; within an eighth, groups
+// of eight row tiles column by column.
+template <int B>
+__device__ __forceinline__ bool weight_place(const WeightParams &p, int block, WeightTile &t) {
+  const int T13 = 2 * p.ft * p.dt, T2 = p.ft * p.dt;
+  const int per13 = (T13 + 7) / 8, per2 = (T2 + 7) / 8;
+  int i = block >> 3;
+  const bool w2 = i >= p.E * per13;
+  if (w2) i -= p.E * per13;
+  const int per = w2 ? per2 : per13, T = w2 ? T2 : T13;
+  const int n_mt = w2 ? p.dt : 2 * p.ft, n_nt = w2 ? p.ft : p.dt;
+  t.e = i / per;
+  const int tile = (block & 7) * per + i % per;
+  if (tile >= T) return false;
+  constexpr int RG = 8;
+  const int grp = tile / (RG * n_nt), within = tile - grp * RG * n_nt;
+  const int gr = min(RG, n_mt - grp * RG);
+  const int nt = within / gr;
+  int mt = grp * RG + within % gr;
+  t.which = w2 ? 2 : (mt >= p.ft ? 1 : 0);
+  if (!w2 && mt >= p.ft) mt -= p.ft;
+  t.f0 = (w2 ? nt : mt) * B;
+  t.d0 = (w2 ? mt : nt) * B;
+  t.pile0 = p.offsets[t.e];
+  t.kcount = p.offsets[t.e + 1] - t.pile0;
+  return true;
+}
+
+// `block` counts from the first of the weight gradients' blocks.  (Blocks that
+// stay and take tiles from a queue per XCD, the next tile's first copies
+// under this one's stores, were no faster on any of the measured shapes.)
+template <bool GATHER, int B, int NW, int BK>
+__device__ __forceinline__ void weight_tile(const WeightParams &p, int block, uint8_t *smem) {
+  constexpr int WM = B / 2, WN = B / (NW / 2), TM = WM / 32, TN = WN / 32;
+  constexpr int REGION = B * BK * 2, STAGE = 2 * REGION, RUNS = REGION / 1024 / NW, SLICES = BK / 16;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  WeightTile t;
+  if (!weight_place<B>(p, block, t)) return;
+  const bool w2 = t.which == 2;
+  const int M = w2 ? p.d : p.f, N = w2 ? p.f : p.d, m0 = w2 ? t.d0 : t.f0, n0 = w2 ? t.f0 : t.d0;
+  const int rows = min(B, M - m0), nk = (t.kcount + BK - 1) / BK;
+
+  // Lane i of run NW j + wave of a region has K row kr + j KROWS, stored chunk
+  // i % CPR.
+  constexpr int CPR = B / 8, RPR = 64 / CPR, KROWS = NW * RPR;
+  const int kr = wave * RPR + lane / CPR;
+  const int chunk = ((lane % CPR) ^ kmaj_key<B>(kr)) << 3;
+  static_assert(KROWS % 4 == 0, "a lane's key is the same in every run");
+
+  // The token of each of this lane's K rows of the step to come, loaded one
+  // step ahead of the copies that use it.
+  int tok[RUNS];
+  auto load_tokens = [&](int kt) {
+    if constexpr (GATHER)
+#pragma unroll
+      for (int j = 0; j < RUNS; ++j)
+        tok[j] = p.perm[t.pile0 + min(kt * BK + kr + j * KROWS, t.kcount - 1)];
+  };
+  // The tile's two operands and this lane's columns of them.
+  const __amdgpu_buffer_rsrc_t rp =
+      rsrc(p.pile[t.which] + (size_t)t.pile0 * p.f, (uint32_t)t.kcount * (uint32_t)p.f * 2u);
+  const __amdgpu_buffer_rsrc_t rs = rsrc(p.src[t.which] + (GATHER ? (size_t)0 : (size_t)t.pile0 * p.d),
+                                         GATHER ? p.src_bytes : (uint32_t)t.kcount * (uint32_t)p.d * 2u);
+  const uint32_t foff = (uint32_t)(t.f0 + chunk) * 2u, doff = (uint32_t)(t.d0 + chunk) * 2u;
+  const uint32_t fpen = t.f0 + chunk < p.f ? 0u : kOOB, dpen = t.d0 + chunk < p.d ? 0u : kOOB;
+  // Copies of K step kt into LDS stage `stage`: the pile matrix's columns, then
+  // the gathered one's (rows past the pile copy zeros).
+  auto issue = [&](int kt, int stage) {
+    uint8_t *s0 = smem + stage * STAGE;
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+      const int k = kt * BK + kr + j * KROWS;
+      const uint32_t kpen = k < t.kcount ? 0u : kOOB;
+      dma16(rp, s0 + (NW * j + wave) * 1024, ((uint32_t)k * (uint32_t)p.f * 2u + foff) | fpen | kpen);
+      dma16(rs, s0 + REGION + (NW * j + wave) * 1024,
+            ((uint32_t)(GATHER ? tok[j] : k) * (uint32_t)p.d * 2u + doff) | dpen | kpen);
+    }
+    load_tokens(kt + 1);
+  };
+
+  const int wm = wave / (NW / 2), wn = wave % (NW / 2);
+  const int a_reg = w2 ? REGION : 0, b_reg = REGION - a_reg;
+  int a_lane[TM], b_lane[TN];
+#pragma unroll
+  for (int tm = 0; tm < TM; ++tm) a_lane[tm] = a_reg + kmaj_lane<B>(wm * WM + tm * 32, lane);
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn) b_lane[tn] = b_reg + kmaj_lane<B>(wn * WN + tn * 32, lane);
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int a = 0; a < TM; ++a)
+#pragma unroll
+    for (int b = 0; b < TN; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+  auto read_frags = [&](auto actc, const uint8_t *st, int kk, bf16x8 *af, bf16x8 *bfr) {
+    constexpr int ACT = decltype(actc)::value;
+#pragma unroll
+    for (int tm = 0; tm < ACT; ++tm) af[tm] = kmaj_frag<B>(st, a_lane[tm], kk);
+    if constexpr (ACT > 0) {
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn) bfr[tn] = kmaj_frag<B>(st, b_lane[tn], kk);
+    }
+  };
+  auto mfmas = [&](auto actc, const bf16x8 *af, const bf16x8 *bfr) {
+    constexpr int ACT = decltype(actc)::value;
+#pragma unroll
+    for (int tm = 0; tm < ACT; ++tm)
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+        acc[tm][tn] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bfr[tn], af[tm], acc[tm][tn], 0, 0, 0);
+  };
+  auto kloop = [&](auto actc) {
+    constexpr int ACT = decltype(actc)::value;
+    k_loop<ACT, TM, TN, SLICES, ACT * 2 + TN * 2>(smem, STAGE, nk, issue, read_frags, mfmas);
   };
   if (nk > 0) {  // (an empty pile's weight gradients are zeros)
     load_tokens(0);
     issue(0, 0);
-    const int act = __builtin_amdgcn_readfirstlane(min(TM, max(0, (rows - wm * WM + 31) / 32)));
-    static_assert(TM >= 2 && TM <= 5, "row groups per wave");
-    if (act == TM) {
-      kloop(std::integral_constant<int, TM>{});
-    } else if (act == 0) {
-      kloop(std::integral_constant<int, 0>{});
-    } else if (act == 1) {
-      kloop(std::integral_constant<int, 1>{});
-    } else if constexpr (TM == 4) {
-      if (act == 2)
-        kloop(std::integral_constant<int, 2>{});
-      else
-        kloop(std::integral_constant<int, 3>{});
-    } else if constexpr (TM == 5) {
-      if (act == 2)
-        kloop(std::integral_constant<int, 2>{});
-      else if (act == 3)
-        kloop(std::integral_constant<int, 3>{});
-      else
-        kloop(std::integral_constant<int, 4>{});
-    }
+    by_act<TM>(__builtin_amdgcn_readfirstlane(min(TM, max(0, (rows - wm * WM + 31) / 32))), kloop);
     wait_vmcnt<0>();
   }
-
-  // ---- epilogue ---------------------------------------------------------------
   __syncthreads();  // every wave is done with the stages
-  float *piece = (float *)(smem + wave * kEpiWave);
-  if constexpr (MODE == DH) {
-    float *s_w = (float *)(smem + NW * kEpiWave);
-    for (int r = tid; r < BM; r += NW * 64)
-      s_w[r] = GATHER && r < rows ? pair_weight(p.inv, p.topk_w, p.k, p.perm[m0 + r], m0 + r) : 1.f;
-    __syncthreads();
-    store_dh<TM, TN, WM, WN>(acc, p, s_w, m0, rows, n0, wm, wn, piece);
-  } else if (MODE == DX && p.splits > 1) {
-    float *out = p.dx_part + ((size_t)split * p.R + m0) * N;
-    store_lines_f32<TM, TN, WM, WN>(acc, rsrc(out, (uint32_t)rows * (uint32_t)N * 4u), N, rows, n0, wm, wn,
-                                    piece);
-  } else {
-    // da: the tile's pile rows; weight gradients: rows m0 .. of expert e
-    uint16_t *out = (uint16_t *)(MODE == DW13 && second ? p.c1 : p.c0) +
-                    (WEIGHT ? (size_t)e * p.d * p.f : (size_t)0) + (size_t)m0 * N;
-    store_lines<TM, TN, WM, WN, WEIGHT ? 2 : 0>(acc, rsrc(out, (uint32_t)rows * (uint32_t)N * 2u), N, rows, n0,
-                                                wm, wn, piece);
-  }
+  uint16_t *out = p.out[t.which] + ((size_t)t.e * M + m0) * N;
+  store_lines<TM, TN, WM, WN, 2>(acc, rsrc(out, (uint32_t)rows * (uint32_t)N * 2u), N, rows, n0, wm, wn,
+                                 (float *)(smem + wave * kEpiWave));
 }
 
 // dg, du, w h: everything else waits for them.
 template <bool GATHER, typename C>
-__global__ __launch_bounds__(C::NT, C::OCC) void grad_dh_kernel(GradParams p) {
+__global__ __launch_bounds__(C::NT, C::OCC) void grad_dh_kernel(RowParams p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ TileSlot s_t;
-  grad_tile<DH, GATHER, C::RBM, C::RBN, C::NW, C::BK>(p, blockIdx.x, smem, s_t);
+  __shared__ float s_w[C::RBM];
+  row_tile<DH, GATHER, C::RBM, C::RBN, C::NW, C::BK>(p, blockIdx.x, smem, s_t, s_w);
 }
 
-// The products that follow, in one grid: da's blocks (the longest) first,
-// then dW1 and dW3, then dW2, so that a product's last, half-empty round of
-// blocks is filled by the next product's.
+// The products that follow, in one grid: da's blocks (the longest) first, then
+// the weight gradients', which fill the CUs that da's last, half-empty round
+// of blocks leaves.
 struct RestParams {
-  GradParams dx, dw13, dw2;
-  int end_dx, end_dw13, end_dw2;  // block ranges, multiples of 8
+  RowParams dx;
+  WeightParams dw;
+  int end_dx;  // a multiple of 8 blocks
 };
 
 template <bool GATHER, typename C>
@@ -559,11 +657,9 @@ __global__ __launch_bounds__(C::NT, C::OCC) void grad_rest_kernel(RestParams q) 
   __shared__ TileSlot s_t;
   const int b = blockIdx.x;
   if (b < q.end_dx)
-    grad_tile<DX, false, C::RBM, C::RBN, C::NW, C::BK>(q.dx, b, smem, s_t);
-  else if (b < q.end_dw13)
-    grad_tile<DW13, GATHER, C::WBM, C::WBN, C::NW, C::BK>(q.dw13, b - q.end_dx, smem, s_t);
+    row_tile<DX, false, C::RBM, C::RBN, C::NW, C::BK>(q.dx, b, smem, s_t);
   else
-    grad_tile<DW2, GATHER, C::WBM, C::WBN, C::NW, C::BK>(q.dw2, b - q.end_dw13, smem, s_t);
+    weight_tile<GATHER, C::WB, C::NW, C::BK>(q.dw, b - q.end_dx, smem);
 }
 
 // Dynamic LDS above 64 KB must be allowed once per device and kernel.
@@ -583,10 +679,8 @@ hipError_t allow_lds(Kern kern, int lds, std::atomic<uint64_t> &done) {
 
 int tiles(int v, int b) { return (v + b - 1) / b; }
 
-// Row tiles of the piles at most (one ragged tile per pile), and blocks of a
-// weight gradient (E experts, each an eighth of its tiles per XCD).
+// Row tiles of the piles at most (one ragged tile per pile).
 int row_tiles(int R, int E, int bm) { return tiles(R, bm) + (E < R ? E : R); }
-int weight_blocks(const GradParams &p) { return p.E * 8 * tiles(p.n_mt * p.n_nt, 8); }
 
 // K ranges of da's product: its K is 2 d_ff, so with few row tiles its blocks
 // would outlast everything that runs beside them.  With fewer blocks than
@@ -601,7 +695,7 @@ int dx_splits(int R, int E, int d, int f) {
 }
 
 template <bool GATHER, typename C>
-hipError_t launch_both(GradParams dh, RestParams q, hipStream_t st) {
+hipError_t launch_both(RowParams dh, RestParams q, hipStream_t st) {
   auto k1 = grad_dh_kernel<GATHER, C>;
   auto k2 = grad_rest_kernel<GATHER, C>;
   constexpr int rest_lds = C::ROW_LDS > C::WEIGHT_LDS ? C::ROW_LDS : C::WEIGHT_LDS;
@@ -609,19 +703,15 @@ hipError_t launch_both(GradParams dh, RestParams q, hipStream_t st) {
   hipError_t err = allow_lds(k1, C::ROW_LDS, allowed1);
   if (err == hipSuccess) err = allow_lds(k2, rest_lds, allowed2);
   if (err != hipSuccess) return err;
-  const int f = dh.f, d = dh.d;
-  dh.n_nt = tiles(f, C::RBN);
-  q.dx.n_nt = tiles(d, C::RBN);
-  q.dw13.n_mt = 2 * tiles(f, C::WBM);
-  q.dw13.n_nt = tiles(d, C::WBN);
-  q.dw2.n_mt = tiles(d, C::WBM);
-  q.dw2.n_nt = tiles(f, C::WBN);
   const int rt = row_tiles(dh.R, dh.E, C::RBM);
+  dh.n_nt = tiles(dh.f, C::RBN);
   k1<<<rt * dh.n_nt, C::NT, C::ROW_LDS, st>>>(dh);
+  q.dx.n_nt = tiles(dh.d, C::RBN);
   q.end_dx = tiles(rt * q.dx.n_nt * q.dx.splits, 8) * 8;
-  q.end_dw13 = q.end_dx + weight_blocks(q.dw13);
-  q.end_dw2 = q.end_dw13 + weight_blocks(q.dw2);
-  k2<<<q.end_dw2, C::NT, rest_lds, st>>>(q);
+  q.dw.ft = tiles(dh.f, C::WB);
+  q.dw.dt = tiles(dh.d, C::WB);
+  const int per_xcd = dh.E * (tiles(2 * q.dw.ft * q.dw.dt, 8) + tiles(q.dw.ft * q.dw.dt, 8));
+  k2<<<q.end_dx + 8 * per_xcd, C::NT, rest_lds, st>>>(q);
   return hipGetLastError();
 }
 
@@ -632,8 +722,8 @@ namespace {
 // One block of 8 waves per CU; or four blocks of 4 waves, which overlap each
 // other's first loads and last stores but move 1.6 times the bytes through L2
 // per product.
-using Big = Cfg<320, 256, 256, 256, 8, 64, 1, 1>;
-using Small = Cfg<128, 128, 128, 128, 4, 32, 4, 2>;
+using Big = Cfg<320, 256, 256, 8, 64, 1, 1>;
+using Small = Cfg<128, 128, 128, 4, 32, 4, 2>;
 
 // Small tiles where blocks are short, few, or mostly padding (measured, Big
 // against Small, us):
@@ -660,18 +750,39 @@ GradPlan grad_plan_bf16(const FfnGradArgs &a) {
 }
 
 hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, hipStream_t st) {
-  GradParams b{};
-  b.offsets = a.offsets;
-  b.slot = a.slot;
-  b.n_slots = a.n_slots;
-  b.E = a.E;
-  b.R = a.R;
-  b.d = a.d;
-  b.f = a.d_ff;
-  b.src_bytes = (uint32_t)((size_t)(a.perm ? a.n : a.R) * a.d * 2);
-  b.splits = 1;
+  RowParams p{};
+  p.offsets = a.offsets;
+  p.slot = a.slot;
+  p.n_slots = a.n_slots;
+  p.E = a.E;
+  p.R = a.R;
+  p.d = a.d;
+  p.f = a.d_ff;
+  p.src_bytes = (uint32_t)((size_t)(a.perm ? a.n : a.R) * a.d * 2);
+  p.splits = 1;
 
-  GradParams p = b;
+  RestParams q{p, {}, 0};
+  q.dx.a0 = (const uint16_t *)w.dg;
+  q.dx.a1 = (const uint16_t *)w.du;
+  q.dx.b0 = (const uint16_t *)a.w1;
+  q.dx.b1 = (const uint16_t *)a.w3;
+  q.dx.c = (uint16_t *)a.da;
+  q.dx.splits = w.plan.dx_splits;
+  q.dx.dx_part = w.dx_part;
+  const void *pile[3] = {w.dg, w.du, w.hs}, *src[3] = {a.a, a.a, a.dy};
+  void *out[3] = {a.dw1, a.dw3, a.dw2};
+  for (int i = 0; i < 3; ++i) {
+    q.dw.pile[i] = (const uint16_t *)pile[i];
+    q.dw.src[i] = (const uint16_t *)src[i];
+    q.dw.out[i] = (uint16_t *)out[i];
+  }
+  q.dw.src_bytes = p.src_bytes;
+  q.dw.perm = a.perm;
+  q.dw.offsets = a.offsets;
+  q.dw.E = a.E;
+  q.dw.d = a.d;
+  q.dw.f = a.d_ff;
+
   p.a0 = (const uint16_t *)a.dy;
   p.b0 = (const uint16_t *)a.w2;
   p.perm = a.perm;
@@ -684,22 +795,6 @@ hipError_t launch_grad_bf16(const FfnGradArgs &a, const FfnGradWs &w, hipStream_
   p.du = (uint16_t *)w.du;
   p.hs = (uint16_t *)w.hs;
   p.part = a.perm ? w.part : nullptr;
-
-  RestParams q{b, b, b, 0, 0, 0};
-  q.dx.a0 = q.dw13.a0 = (const uint16_t *)w.dg;
-  q.dx.a1 = q.dw13.a1 = (const uint16_t *)w.du;
-  q.dx.b0 = (const uint16_t *)a.w1;
-  q.dx.b1 = (const uint16_t *)a.w3;
-  q.dx.c0 = a.da;
-  q.dx.splits = w.plan.dx_splits;
-  q.dx.dx_part = w.dx_part;
-  q.dw13.b0 = (const uint16_t *)a.a;
-  q.dw13.perm = q.dw2.perm = a.perm;
-  q.dw13.c0 = a.dw1;
-  q.dw13.c1 = a.dw3;
-  q.dw2.a0 = (const uint16_t *)a.dy;
-  q.dw2.b0 = (const uint16_t *)w.hs;
-  q.dw2.c0 = a.dw2;
   if (use_small(a))
     return a.perm ? launch_both<true, Small>(p, q, st) : launch_both<false, Small>(p, q, st);
   return a.perm ? launch_both<true, Big>(p, q, st) : launch_both<false, Big>(p, q, st);
