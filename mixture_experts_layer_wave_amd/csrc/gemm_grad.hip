@@ -728,12 +728,13 @@ using Small = Cfg<128, 128, 128, 4, 32, 4, 2>;
 // Small tiles where blocks are short, few, or mostly padding (measured, Big
 // against Small, us):
 //   at most 128 rows per expert: 128 experts, d = d_ff = 2880, 256 tokens top-4
-//     2838 against 2154, 4096 tokens Zipf-skewed 4237 against 3642 (uniform
-//     3843 against 4039); at 256 rows (8 experts, 1024 x 4096) 199 against 234
+//     2840 against 2160, 4096 tokens Zipf-skewed 4190 against 3610 (uniform
+//     3806 against 4000); at 256 rows (8 experts, 1024 x 4096) 206 against 233
 //   the dh product under half a round of the CUs: 1 expert, 2048 x 8192, 500
-//     tokens 168 against 155; 1024 tokens (160 blocks) 268 against 260
-//   padding: d = 264, d_ff = 520, 8000 tokens 116 against 88.  Without padding
-//     Small takes 1.2 times as long (Mixtral-shaped 11.7 against 14.1 ms).
+//     tokens 168 against 154; 1024 tokens (160 blocks) 260 against 253
+//   padding: d = 264, d_ff = 520, 8000 tokens 135 against 91.  Without padding
+//     Small takes 1.2 times as long (8 experts, 4096 x 14336, 16384 rows: 11.7
+//     against 14.1 ms).
 bool use_small(const FfnGradArgs &a) {
   auto area = [&](int b) { return (double)(tiles(a.d, b) * b) * (tiles(a.d_ff, b) * b); };
   return a.R <= 128ll * a.E || row_tiles(a.R, a.E, Big::RBM) * tiles(a.d_ff, Big::RBN) < 128 ||
