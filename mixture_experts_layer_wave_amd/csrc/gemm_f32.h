@@ -1,10 +1,12 @@
 // A float32 product tile on the matrix cores, shared by the float32 kernels
 // of the training operators (gemm_f32.hip, router_grad.hip).
 //
-// Block of 512 threads: two groups of 4 waves (2 x 2, each 32 x 32 on
-// v_mfma_f32_32x32x2_f32) compute the same 64 x 64 output tile over the even
-// and the odd K steps of 32, so that a small grid still has two waves per
-// SIMD (one group's LDS and barrier waits lie under the other's products).
+// Block: G groups of 4 waves (2 x 2, each 32 x 32 on v_mfma_f32_32x32x2_f32)
+// compute the same 64 x 64 output tile, group g over the K steps of 32 that
+// are g mod G.  G = 2 is for grids of few blocks, which have two waves per
+// SIMD all the same (one group's LDS and barrier waits lie under the other's
+// products); with many blocks G = 1 has four of them on a CU, each at its own
+// place.
 // Both operands lie in LDS K row by K row, 66 floats apart: the stores of
 // operands contiguous along K (8 pieces of four K, 8 rows) and the fragment
 // reads (32 rows of K rows k and k + 16) meet 64 different banks.  Two stages
@@ -24,12 +26,20 @@
 namespace moe {
 namespace f32gemm {
 
-constexpr int kT = 64, kK = 32, kPitch = kT + 2, kThreads = 512;
+constexpr int kT = 64, kK = 32, kPitch = kT + 2;
 constexpr int kFour = kT * kK / 4 / 256;       // pieces a thread fetches per operand and step
 constexpr int kStage = 2 * kK * kPitch;        // floats of both tiles of a stage
-constexpr int kSmem = 4 * kStage;              // two groups, two stages
 constexpr int kOutPitch = kT + 4;
-constexpr int kLines = kT * kT / 4 / kThreads;  // pieces of the result a thread holds
+template <int G>
+struct Groups {
+  static constexpr int THREADS = 256 * G;
+  static constexpr int SMEM = 2 * G * kStage;            // floats: two stages a group
+  static constexpr int LINES = kT * kT / 4 / THREADS;    // pieces of the result a thread holds
+  // Row and first column (in the tile) of the result's piece i of this
+  // thread: 16 lanes hold a row.
+  static __device__ __forceinline__ int row(int i) { return (threadIdx.x >> 4) + i * (THREADS / 16); }
+  static __device__ __forceinline__ int col() { return (threadIdx.x & 15) * 4; }
+};
 
 // Four consecutive elements at byte offset `off` of a buffer, of which the
 // first `n` (<= 0: none, >= 4: all) belong to the operand.  Dwords past the
@@ -82,18 +92,13 @@ __device__ __forceinline__ void put(float *tile, int i, f32x4 v) {
   for (int j = 0; j < 4; ++j) tile[KMAJ ? k * kPitch + r + j : (k + j) * kPitch + r] = v[j];
 }
 
-// Row and first column (in the tile) of the result's piece i of this thread:
-// 16 lanes hold a row.
-__device__ __forceinline__ int line_row(int i) { return (threadIdx.x >> 4) + i * (kThreads / 16); }
-__device__ __forceinline__ int line_col() { return (threadIdx.x & 15) * 4; }
-
-// out += sum over k < K of A(k, m) B(k, n), as pieces of four columns
-// (line_row, line_col).  piece_a(i, k, m) and piece_b(i, k, n) give the
-// thread's piece i at tile row m or column n; k may be past K (the piece is
-// cut here).  smem: kSmem floats.  Every thread of the block calls it.
-template <bool A_KMAJ, bool B_KMAJ, typename FA, typename FB>
-__device__ __forceinline__ void product(f32x4 (&out)[kLines], float *smem, int K, FA piece_a, FB piece_b) {
-  const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) & 3, kg = threadIdx.x >> 8;
+// This group's part of total += sum over k < K of A(k, m) B(k, n).
+// piece_a(i, k, m) and piece_b(i, k, n) give the thread's piece i at tile row
+// m or column n; k may be past K (the piece is cut here).  smem:
+// Groups<G>::SMEM floats.  Every thread of the block calls it.
+template <int G, bool A_KMAJ, bool B_KMAJ, typename FA, typename FB>
+__device__ __forceinline__ void product(f32x16 &total, float *smem, int K, FA piece_a, FB piece_b) {
+  const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) & 3, kg = G > 1 ? threadIdx.x >> 8 : 0;
   const int am = (wave >> 1) * 32 + (lane & 31), bn = (wave & 1) * 32 + (lane & 31), kh = lane >> 5;
   auto get = [&](auto kmaj, auto f, int i, int k0) {
     constexpr bool KMAJ = decltype(kmaj)::value;
@@ -109,15 +114,15 @@ __device__ __forceinline__ void product(f32x4 (&out)[kLines], float *smem, int K
   f32x4 ra[2][kFour], rb[2][kFour];
   // step s of this group
   auto fetch = [&](f32x4 *a, f32x4 *b, int s) {
-    const int k0 = (2 * s + kg) * kK;
+    const int k0 = (G * s + kg) * kK;
 #pragma unroll
     for (int i = 0; i < kFour; ++i) {
       a[i] = get(std::integral_constant<bool, A_KMAJ>{}, piece_a, i, k0);
       b[i] = get(std::integral_constant<bool, B_KMAJ>{}, piece_b, i, k0);
     }
   };
-  f32x16 acc = {}, total = {};
-  const int steps = (K + 2 * kK - 1) / (2 * kK);  // of either group
+  f32x16 acc = {};
+  const int steps = (K + G * kK - 1) / (G * kK);  // of every group
   fetch(ra[0], rb[0], 0);
   fetch(ra[1], rb[1], 1);
   __syncthreads();  // smem's readers before this call are done
@@ -132,18 +137,21 @@ __device__ __forceinline__ void product(f32x4 (&out)[kLines], float *smem, int K
     }
     fetch(ra[P], rb[P], s + 2);
     __syncthreads();
-    // all of the step's fragments first, so that the products wait for the
+    // half of the step's fragments first, so that the products wait for the
     // first of them only
-    float fa[kK / 2], fb[kK / 2];
+    constexpr int H = kK / 4;
 #pragma unroll
-    for (int k = 0; k < kK / 2; ++k) {
-      fa[k] = sa[(k + 16 * kh) * kPitch + am];
-      fb[k] = sb[(k + 16 * kh) * kPitch + bn];
+    for (int h = 0; h < kK / 2; h += H) {
+      float fa[H], fb[H];
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        fa[k] = sa[(h + k + 16 * kh) * kPitch + am];
+        fb[k] = sb[(h + k + 16 * kh) * kPitch + bn];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < H; ++k) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[k], fa[k], acc, 0, 0, 0);
     }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int k = 0; k < kK / 2; ++k)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[k], fa[k], acc, 0, 0, 0);
     if ((s & 7) == 7) {
       total += acc;
       acc = f32x16{};
@@ -154,10 +162,18 @@ __device__ __forceinline__ void product(f32x4 (&out)[kLines], float *smem, int K
     if (s + 1 < steps) step(s + 1, std::integral_constant<int, 1>{});
   }
   total += acc;
+}
+
+// The groups' totals, added, as pieces of four columns (Groups::row, col).
+template <int G>
+__device__ __forceinline__ void lines(const f32x16 &total, float *smem, f32x4 (&out)[Groups<G>::LINES]) {
+  using L = Groups<G>;
+  const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) & 3, kg = G > 1 ? threadIdx.x >> 8 : 0;
+  const int am = (wave >> 1) * 32 + (lane & 31), kh = lane >> 5;
   // Lane l of wave (wm, wn) holds row 32 wm + l % 32 and columns 32 wn +
-  // 8 g + 4 (l / 32) + 0 .. 3: the even steps' sums, then the odd steps'.
+  // 8 g + 4 (l / 32) + 0 .. 3: the groups' sums, in order.
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
+  for (int half = 0; half < G; ++half) {
     __syncthreads();
     if (kg == half)
 #pragma unroll
@@ -170,7 +186,7 @@ __device__ __forceinline__ void product(f32x4 (&out)[kLines], float *smem, int K
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kLines; ++i) out[i] += *(const f32x4 *)(smem + line_row(i) * kOutPitch + line_col());
+  for (int i = 0; i < L::LINES; ++i) out[i] = *(const f32x4 *)(smem + L::row(i) * kOutPitch + L::col());
 }
 
 }  // namespace f32gemm
