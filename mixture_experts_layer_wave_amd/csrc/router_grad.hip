@@ -40,59 +40,80 @@ __device__ __forceinline__ void split_bf16(float x, uint16_t &hi, uint16_t &lo) 
 __host__ __device__ constexpr int padded(int E) { return (E + 31) & ~31; }
 
 // ---- dz: one group of G = topk_group(E) lanes per token -----------------------
-// split (bf16 rows): dz's two halves too, hi [n][padded(E)], then lo, which
-// the dW_g product reads once per column tile.
+// Lane l owns experts l, l + G, ... (PER of them at most) and, as k <= 32 and
+// k <= E make k <= G, slot l: every load of a token is one of a few that do
+// not wait for each other.  split (bf16 rows): dz's two halves too, hi
+// [n][padded(E)], then lo, which the dW_g product reads once per column tile.
+template <int PER>
 __global__ __launch_bounds__(256) void router_dz_kernel(
     const float *__restrict__ logits, const int32_t *__restrict__ idx, const float *__restrict__ w,
     const float *__restrict__ dw, const float *__restrict__ f, float aux, int n, int E, int k, int renorm,
     float *__restrict__ dz, uint16_t *__restrict__ split) {
   const int G = topk_group(E);
-  const int gl = (threadIdx.x & 63) & (G - 1);
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1), g0 = lane - gl;
   const int t = (blockIdx.x * 256 + threadIdx.x) / G;
   if ((blockIdx.x * 256 + (threadIdx.x & ~63)) / G >= n) return;  // whole wave idle
   const bool live = t < n;
   const int Ep = padded(E);
   const size_t row = live ? t : 0;
-  const float *z = logits + row * E;
-  idx += row * k;
-  w += row * k;
-  dw += row * k;
-  float D = 0.f;
-  for (int j = 0; j < k; ++j)
-    if ((unsigned)idx[j] < (unsigned)E) D = fmaf(w[j], dw[j], D);
-  float m = -__builtin_inff();
-  for (int e = gl; e < E; e += G) m = fmaxf(m, z[e]);
+  float z[PER], fv[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = gl + i * G;
+    z[i] = e < E ? logits[row * E + e] : -__builtin_inff();
+    fv[i] = f && e < E ? f[e] : 0.f;
+  }
+  int c = -1;  // this lane's slot: expert, weight and the weight's gradient
+  float wj = 0.f, dj = 0.f;
+  if (gl < k) {
+    c = idx[row * k + gl];
+    wj = w[row * k + gl];
+    dj = dw[row * k + gl];
+  }
+  const float D = group_sum((unsigned)c < (unsigned)E ? wj * dj : 0.f, G);
+  float m = z[0];
+#pragma unroll
+  for (int i = 1; i < PER; ++i) m = fmaxf(m, z[i]);
   m = group_max(m, G);
-  float s = 0.f, fp = 0.f;
-  for (int e = gl; e < E; e += G) {
-    const float q = expf(z[e] - m);
-    s += q;
-    if (f) fp = fmaf(q, f[e], fp);
+  float q[PER], s = 0.f, fp = 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    q[i] = gl + i * G < E ? expf(z[i] - m) : 0.f;
+    s += q[i];
+    fp = fmaf(q[i], fv[i], fp);
   }
   s = group_sum(s, G);
   fp = group_sum(fp, G) / s;
+  // Renormalised: sum over the expert's slots of w_j (dw_j - D); else of dw_j.
+  float g[PER] = {};
+  if (renorm) dj = wj * (dj - D);
+  for (int j = 0; j < k; ++j) {
+    const int cj = __shfl(c, g0 + j);
+    const float vj = __shfl(dj, g0 + j);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) g[i] += cj == gl + i * G ? vj : 0.f;
+  }
   if (!live) return;
-  for (int e = gl; e < E; e += G) {
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = gl + i * G;
+    if (e >= E) {
+      if (split && e < Ep) split[row * Ep + e] = split[(size_t)n * Ep + row * Ep + e] = 0;
+      continue;
+    }
     float v = 0.f;
     // a token whose logits are all -inf has no expert and no gradient
     if (m != -__builtin_inff()) {
-      const float p = expf(z[e] - m) / s;
-      if (renorm) {
-        for (int j = 0; j < k; ++j)
-          if (idx[j] == e) v = fmaf(w[j], dw[j] - D, v);
-      } else {
-        float g = 0.f;
-        for (int j = 0; j < k; ++j)
-          if (idx[j] == e) g += dw[j];
-        v = p * (g - D);
-      }
-      if (f) v = fmaf(aux * p, f[e] - fp, v);
+      const float p = q[i] / s;
+      v = renorm ? g[i] : p * (g[i] - D);
+      if (f) v = fmaf(aux * p, fv[i] - fp, v);
     }
     dz[row * E + e] = v;
     if (split) split_bf16(v, split[row * Ep + e], split[(size_t)n * Ep + row * Ep + e]);
   }
+  // (the padding past PER G experts)
   if (split)
-    for (int e = E + gl; e < Ep; e += G) split[row * Ep + e] = split[(size_t)n * Ep + row * Ep + e] = 0;
+    for (int e = gl + PER * G; e < Ep; e += G) split[row * Ep + e] = split[(size_t)n * Ep + row * Ep + e] = 0;
 }
 
 // ---- dx, bf16 -------------------------------------------------------------------
@@ -471,15 +492,17 @@ __global__ __launch_bounds__(Two::THREADS, 4) void router_dw_f32_kernel(const fl
   }
 }
 
-// Token ranges of the dW_g product: one block per CU beside dx's, but planes
-// of at most the bytes of x (S E 4 <= n 2), and whole steps; a range's rows
+// Token ranges of the dW_g product: blocks for three CUs of four beside dx's
+// (128 experts, 2880 wide, 4096 tokens: 54.2 us; for every CU, whose planes
+// cost more, 60, for every second 55.4, for every fourth 60), but planes of at
+// most the bytes of x (S E 4 <= n 2), and whole steps; a range's rows
 // of x and dz stay under 2^30 bytes (32-bit buffer offsets, float32).
 struct Ranges {
   int S, range;
 };
 Ranges dw_ranges(int n, int d, int E) {
   const int cols = E <= 64 ? 256 : 128, tiles = ((d + cols - 1) / cols) * ((E + 127) / 128);
-  int S = (256 + tiles - 1) / tiles;
+  int S = (192 + tiles - 1) / tiles;
   const int most = n / (2 * E) > 1 ? n / (2 * E) : 1;
   if (S > most) S = most;
   const long long bytes = (long long)n * (d > E ? d : E) * 4;
@@ -545,7 +568,9 @@ size_t router_grad_bytes(int n, int d, int E) {
 hipError_t launch_router_grad(const RouterGradArgs &a, hipStream_t st) {
   uint16_t *split = a.bf16 ? (uint16_t *)((char *)a.ws + plane_bytes(a.n, a.d, a.E)) : nullptr;
   const int per_block = 256 / topk_group(a.E);
-  router_dz_kernel<<<(a.n + per_block - 1) / per_block, 256, 0, st>>>(
+  // (E <= 64: one expert a lane, E <= 128: two)
+  auto dz = a.E <= 64 ? router_dz_kernel<1> : a.E <= 128 ? router_dz_kernel<2> : router_dz_kernel<16>;
+  dz<<<(a.n + per_block - 1) / per_block, 256, 0, st>>>(
       a.logits, a.idx, a.topk_w, a.dtopk_w, a.f, a.alpha * (float)a.E / (float)a.n, a.n, a.E, a.k,
       a.renorm ? 1 : 0, a.dlogits, split);
   const Ranges q = dw_ranges(a.n, a.d, a.E);
