@@ -393,7 +393,7 @@ __device__ __forceinline__ void row_tile(const RowParams &p, int block, uint8_t 
   constexpr int B_CPR = BN / 8, B_RPR = 64 / B_CPR;  // chunks per row, rows per run
   const int b_kr = wave * B_RPR + lane / B_CPR;
   const int b_col = n0 + (((lane % B_CPR) ^ kmaj_key<BN>(b_kr)) << 3);
-  const uint32_t b_pen = b_col < N ? 0u : kOOB;
+  const uint32_t b_off = b_col < N ? ((uint32_t)b_kr * (uint32_t)N + (uint32_t)b_col) * 2u : kOOB;
   static_assert((NW * B_RPR) % 4 == 0, "a lane's key is the same in every run");
   // Row-major A tile: as in the forward GEMM.
   const int c = dma_chunk<BK * 2>(wave, lane);
@@ -422,11 +422,8 @@ __device__ __forceinline__ void row_tile(const RowParams &p, int block, uint8_t 
     for (int j = 0; j < A_RUNS; ++j)
       dma16(sec ? ra1 : ra0, sa + (NW * j + wave) * 1024, (a_off[j] + (uint32_t)k0 * 2u) | pen);
 #pragma unroll
-    for (int j = 0; j < B_RUNS; ++j) {
-      const int kr = k0 + b_kr + j * NW * B_RPR;
-      const uint32_t penb = kr < kcount ? b_pen : kOOB;
-      dma16(sec ? rb1 : rb0, sb + (NW * j + wave) * 1024, (((uint32_t)kr * (uint32_t)N + (uint32_t)b_col) * 2u) | penb);
-    }
+    for (int j = 0; j < B_RUNS; ++j)  // (rows past K are past the buffer's end)
+      dma16(sec ? rb1 : rb0, sb + (NW * j + wave) * 1024, b_off + (uint32_t)(k0 + j * NW * B_RPR) * ((uint32_t)N * 2u));
   };
 
   const int wm = wave / (NW / 2), wn = wave % (NW / 2);
@@ -569,19 +566,26 @@ __device__ __forceinline__ void weight_tile(const WeightParams &p, int block, ui
       rsrc(p.pile[t.which] + (size_t)t.pile0 * p.f, (uint32_t)t.kcount * (uint32_t)p.f * 2u);
   const __amdgpu_buffer_rsrc_t rs = rsrc(p.src[t.which] + (GATHER ? (size_t)0 : (size_t)t.pile0 * p.d),
                                          GATHER ? p.src_bytes : (uint32_t)t.kcount * (uint32_t)p.d * 2u);
-  const uint32_t foff = (uint32_t)(t.f0 + chunk) * 2u, doff = (uint32_t)(t.d0 + chunk) * 2u;
-  const uint32_t fpen = t.f0 + chunk < p.f ? 0u : kOOB, dpen = t.d0 + chunk < p.d ? 0u : kOOB;
+  const uint32_t foff = t.f0 + chunk < p.f ? ((uint32_t)kr * (uint32_t)p.f + (uint32_t)(t.f0 + chunk)) * 2u : kOOB;
+  const uint32_t soff = t.d0 + chunk < p.d ? (GATHER ? (uint32_t)(t.d0 + chunk) * 2u
+                                                     : ((uint32_t)kr * (uint32_t)p.d + (uint32_t)(t.d0 + chunk)) * 2u)
+                                           : kOOB;
   // Copies of K step kt into LDS stage `stage`: the pile matrix's columns, then
-  // the gathered one's (rows past the pile copy zeros).
+  // the gathered one's.  Rows past the pile copy zeros: in order they are past
+  // the buffer's end, gathered ones are sent there.  What an address owes to
+  // the step and the run is the same for all lanes and added from a scalar.
   auto issue = [&](int kt, int stage) {
     uint8_t *s0 = smem + stage * STAGE;
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
-      const int k = kt * BK + kr + j * KROWS;
-      const uint32_t kpen = k < t.kcount ? 0u : kOOB;
-      dma16(rp, s0 + (NW * j + wave) * 1024, ((uint32_t)k * (uint32_t)p.f * 2u + foff) | fpen | kpen);
-      dma16(rs, s0 + REGION + (NW * j + wave) * 1024,
-            ((uint32_t)(GATHER ? tok[j] : k) * (uint32_t)p.d * 2u + doff) | dpen | kpen);
+      const uint32_t k = (uint32_t)(kt * BK + j * KROWS);
+      dma16(rp, s0 + (NW * j + wave) * 1024, foff + k * ((uint32_t)p.f * 2u));
+      uint32_t off;
+      if constexpr (GATHER)
+        off = (int)k + kr < t.kcount ? (uint32_t)tok[j] * ((uint32_t)p.d * 2u) + soff : kOOB;
+      else
+        off = soff + k * ((uint32_t)p.d * 2u);
+      dma16(rs, s0 + REGION + (NW * j + wave) * 1024, off);
     }
     load_tokens(kt + 1);
   };
