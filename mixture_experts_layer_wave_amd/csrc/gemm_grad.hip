@@ -503,7 +503,8 @@ struct WeightTile {
 // The block's tile (false: none).  Every XCD (block b runs on XCD b mod 8)
 // takes an eighth of each expert's tiles of dW1 and dW3, then of dW2, so that
 // all have the same share of large and small piles; within an eighth, groups
-// of eight row tiles column by column.
+// of eight row tiles column by column (dW2, whose row operand is the gathered
+// one: four, 8 experts of 4096 x 14336 1% faster than with eight).
 template <int B>
 __device__ __forceinline__ bool weight_place(const WeightParams &p, int block, WeightTile &t) {
   const int T13 = 2 * p.ft * p.dt, T2 = p.ft * p.dt;
@@ -516,7 +517,7 @@ __device__ __forceinline__ bool weight_place(const WeightParams &p, int block, W
   t.e = i / per;
   const int tile = (block & 7) * per + i % per;
   if (tile >= T) return false;
-  constexpr int RG = 8;
+  const int RG = w2 ? 4 : 8;
   const int grp = tile / (RG * n_nt), within = tile - grp * RG * n_nt;
   const int gr = min(RG, n_mt - grp * RG);
   const int nt = within / gr;
