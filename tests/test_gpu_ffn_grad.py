@@ -290,6 +290,35 @@ def test_extreme_pre_activations(dtype):
     check_back(b, got, g, u, b.host["x"], b.host["dy"], True)
 
 
+@pytest.mark.parametrize("dtype,n,d,E,k,f,skew", [
+    ("bf16", 2100, 256, 2, 2, 2000, 1),  # one block per CU, da's sum over K in ranges
+    ("bf16", 8000, 1288, 1, 1, 1288, 0),  # the same, da in one range
+    ("f32", 1300, 40, 2, 2, 72, 2)])  # a pile longer than the tokens a block holds at once
+def test_long_piles(dtype, n, d, E, k, f, skew):
+    say(f"[ffn grad, long piles] {dtype} n={n} d={d} E={E} d_ff={f}")
+    b = Batch(dtype, n, d, E, k, f, skew, seed=19)
+    up = b.up()
+    check_up(b, up, b.host["x"], True)
+    check_back(b, b.back(up[1], up[2]), up[1], up[2], b.host["x"], b.host["dy"], True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_token_twice_in_one_pile(dtype):
+    """Two slots of a token with the same expert are two pile rows, each with
+    its own weight and its own gradient of it."""
+    from mixture_experts_layer_wave_amd import binding as B
+
+    say(f"[ffn grad, repeated ids] {dtype}")
+    b = Batch(dtype, 90, 72, 4, 3, 88, 0, seed=23)
+    b.idx[::2, 2] = b.idx[::2, 0]
+    B.moe_dispatch(b.shape, b.idx, b.counts, b.offsets, b.perm, b.inv)
+    for key in ("perm", "inv", "offsets"):
+        b.host[key] = getattr(b, key).cpu().numpy()
+    up = b.up()
+    check_up(b, up, b.host["x"], True)
+    check_back(b, b.back(up[1], up[2]), up[1], up[2], b.host["x"], b.host["dy"], True)
+
+
 def test_gradient_against_differences():
     """d/d step of the loss sum(y dy), with y from the library's own float32
     forward pass (up, down, combine), along a random direction of every input."""
