@@ -319,6 +319,43 @@ def test_a_token_twice_in_one_pile(dtype):
     check_back(b, b.back(up[1], up[2]), up[1], up[2], b.host["x"], b.host["dy"], True)
 
 
+def test_weights_past_32_bit_offsets():
+    """300 experts of 2704 x 2704: the last ones' weights and gradients lie
+    more than 2^32 bytes and 2^31 elements in."""
+    import torch
+    from mixture_experts_layer_wave_amd import binding as B
+
+    say("[ffn grad, offsets past 32 bits]")
+    n, d, E, f = 5, 2704, 300, 2704
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    small = Batch("bf16", n, d, 3, 1, f, 0, seed=29)
+    where = [0, 150, 299]
+    big = [torch.zeros(E, *m.shape[1:], **bf) for m in (small.w1, small.w3, small.w2)]
+    for m, t in zip(big, (small.w1, small.w3, small.w2)):
+        m[where] = t
+    out = [torch.full_like(m, 7.0) for m in big]
+    shape = (n, d, E, 1, f)
+    idx = torch.tensor(where, dtype=torch.int32, device="cuda")[small.idx.long()].to(torch.int32).contiguous()
+    counts, offsets = (torch.empty(E + i, dtype=torch.int32, device="cuda") for i in (0, 1))
+    B.moe_dispatch(shape, idx, counts, offsets, small.perm, small.inv)
+    weights = dict(dtype="bf16", w1=big[0], w3=big[1], w2=big[2])
+    h, g, u = (small.rows(f) for _ in range(3))
+    B.moe_expert_up_save(shape, small.x, "bf16", small.perm, offsets, weights, h, g, u)
+    da, dtw = small.rows(d), torch.empty(n, 1, device="cuda")
+    nb = B.moe_grouped_ffn_backward_workspace_bytes(shape, "bf16")
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    B.moe_grouped_ffn_backward(shape, small.dy, small.x, "bf16", small.perm, small.inv, small.w, offsets, weights, g,
+                               u, da, *out, dtw, ws, nb)
+    torch.cuda.synchronize()
+    check_up(small, (h, g, u), small.host["x"], True)
+    got = (da, *(m[where] for m in out), dtw)
+    check_back(small, got, g, u, small.host["x"], small.host["dy"], True)
+    rest = torch.ones(E, dtype=torch.bool, device="cuda")
+    rest[where] = False
+    for m in out:
+        assert not m[rest].any()
+
+
 def test_gradient_against_differences():
     """d/d step of the loss sum(y dy), with y from the library's own float32
     forward pass (up, down, combine), along a random direction of every input."""

@@ -156,6 +156,41 @@ def test_gradient_against_differences(dtype, d):
     assert abs((yp * dy64).sum() - want) <= (2 * HALF[dtype] + 256 * U) * (size * np.abs(dy64)).sum() * 2
 
 
+def test_rows_past_32_bit_offsets():
+    """131500 rows of 16384: the last ones lie more than 2^32 bytes and 2^31
+    elements in.  dy is zero in all but a few rows."""
+    import torch
+    from mixture_experts_layer_wave_amd import binding as B
+
+    say("[layer norm, offsets past 32 bits]")
+    n, d = 131500, 16384
+    rows = [0, 65536, n - 2, n - 1]
+    xs, dys, w, b = _inputs("bf16", len(rows), d, seed=3)
+    x, dy = (torch.zeros(n, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[rows], dy[rows] = xs, dys
+    y, dx = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
+    mean, rstd = (torch.empty(n, device="cuda") for _ in range(2))
+    dw, db = (torch.empty(d, device="cuda") for _ in range(2))
+    nb = B.moe_layer_norm_backward_workspace_bytes(n, d)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    B.moe_layer_norm(n, d, x, "bf16", w, b, 1e-5, y, mean, rstd)
+    B.moe_layer_norm_backward(n, d, dy, x, "bf16", w, mean, rstd, dx, dw, db, ws, nb)
+    torch.cuda.synchronize()
+    # the same rows by themselves, which the tests above hold to the oracle
+    ys, means, rstds = _forward(xs, "bf16", w, b)
+    dxs, dws, dbs = _backward(dys, xs, "bf16", w, means, rstds)
+    assert torch.equal(y[rows], ys) and torch.equal(mean[rows], means) and torch.equal(rstd[rows], rstds)
+    assert torch.equal(dx[rows], dxs)
+    # Sums over rows: the same four addends (and exact zeros) in two orders, each
+    # sum four roundings of at most 2^-24 of the addends' sizes.
+    xh = (xs.double() - means.double()[:, None]) * rstds.double()[:, None]
+    for p, q, size in ((dw, dws, (dys.double() * xh).abs().sum(0)), (db, dbs, dys.double().abs().sum(0))):
+        assert ((p.double() - q.double()).abs() <= 9 * 2.0 ** -24 * size).all()
+    other = torch.ones(n, dtype=torch.bool, device="cuda")
+    other[rows] = False
+    assert not dx[other].any()
+
+
 def test_no_rows_and_optional_outputs():
     import torch
     from mixture_experts_layer_wave_amd import binding as B
