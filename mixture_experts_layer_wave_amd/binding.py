@@ -130,7 +130,9 @@ def _stream(stream):
     if stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: torch.cuda.current_stream() makes a Stream object
+        # around it, which took 2.9 us a call against 0.3
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -163,6 +163,17 @@ def test_captured_step_replays(name):
         torch.cuda.synchronize()
 
 
+def test_calls_take_the_current_stream():
+    import torch
+    from mixture_experts_layer_wave_amd import binding as B
+
+    side = torch.cuda.Stream()
+    assert B._stream(None) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(side):
+        assert B._stream(None) == side.cuda_stream == B._stream(side)
+    assert B._stream(None) == torch.cuda.current_stream().cuda_stream != side.cuda_stream
+
+
 def test_two_steps_at_once_on_two_streams():
     import torch
     from mixture_experts_layer_wave_amd.device import TrainingLayer
