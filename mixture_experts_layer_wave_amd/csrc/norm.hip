@@ -18,9 +18,9 @@
 // groups, then, by a second kernel, over the blocks, always in the same
 // order.  Sums are float32; rows are rounded once on their way out.
 //
-// Measured, 8192 rows of 4096 in bf16: forward 34.1 us (134 MB, 3.9 TB/s),
-// gradient 40.8 us (201 MB, 4.9 TB/s) and 4.6 us for the sum over the blocks;
-// a 1 GiB copy reaches 5.07 TB/s.
+// Measured, 8192 rows of 4096 in bf16: forward 27.6 us (134 MB, 4.9 TB/s),
+// gradient 43 us (201 MB, 4.7 TB/s) with 4.6 us of it for the sum over the
+// blocks; a 1 GiB copy reaches 5.07 TB/s.
 #include <type_traits>
 
 #include "common.h"
@@ -85,7 +85,7 @@ struct Chunk {
 // w's (or b's) values for the chunk at col, 0 past the row's end.  In 16-B
 // loads: with one load per value, a chunk's stride apart over the lanes, the
 // norm of one row of 16384 took 16.8 us instead of 5.7, that of 8192 rows of
-// 4096 34.0 instead of 30.0.
+// 4096 34.0 instead of 29.4.
 template <bool TAIL, int V>
 __device__ __forceinline__ void load_columns(const float *__restrict__ p, int col, int d, float (&o)[V]) {
 #pragma unroll
@@ -377,8 +377,7 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restric
 
 // Threads per row and chunks per thread for rows of d: the fewest threads
 // that hold a row in one 16-B chunk each (two above 1024 threads, four for
-// float32 above 8192), so narrow rows share a block.  (Rows of 4096 bf16 in
-// two chunks by 256 threads: 46 us against 36 for 8192 of them.)
+// float32 above 8192), so narrow rows share a block.
 template <bool BF, bool TAIL, typename Launch>
 hipError_t with_layout(int d, Launch go) {
   constexpr int V = Chunk<BF, TAIL>::V;
@@ -400,10 +399,9 @@ hipError_t with_layout(int d, Launch go) {
 // fewer for few rows; each writes one partial row of 2 d floats.
 int grad_blocks(int n) { return n < 256 ? n : 256; }
 
-// Threads per CU of the forward pass: more rows at once repeat more of w and
-// b's loads, fewer leave HBM idle (8192 rows of 4096 bf16: 512 threads 37.6,
-// 1024 33.8, 2048 36.4, 4096 48.3 us).
-constexpr int kRowThreads = 1024;
+// Threads per CU of the forward pass: all that fit (8192 rows of 4096 bf16: 512
+// threads 35.7, 1024 29.4, 2048 27.6 us; 8192 rows of 2880: 33.3, 26.0, 22.9).
+constexpr int kRowThreads = 2048;
 
 template <bool BF, bool TAIL>
 hipError_t launch_fwd(const void *x, const float *w, const float *b, float eps, int n, int d, void *y,
