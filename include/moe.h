@@ -386,8 +386,8 @@ int moe_expert_up_save(const moe_shape *s, const void *a, int act, const int32_t
  * otherwise).  Products accumulate in float32 and outputs are rounded once;
  * with BF16 weights dg, du and w silu(g) u are rounded to bf16 in between
  * (the matrix cores' input type) and pointers are 16-byte aligned.  Sizes as
- * in moe_expert_up_save.  Deterministic.  The size helper returns 0 for an invalid
- * shape or weight dtype. */
+ * in moe_expert_up_save.  Deterministic.  The size helper returns 0 for an
+ * invalid shape or weight dtype. */
 size_t moe_grouped_ffn_backward_workspace_bytes(const moe_shape *s, int w_dtype);
 int moe_grouped_ffn_backward(const moe_shape *s, const void *dy, const void *a, int act,
                              const int32_t *perm, const int32_t *inv, const float *topk_w,
@@ -417,8 +417,9 @@ int moe_grouped_ffn_backward(const moe_shape *s, const void *dy, const void *a, 
  * ws       at least moe_router_backward_workspace_bytes(s), 16-byte aligned
  * Sums are float32; with MOE_BF16 dlogits enters the two products with 16 of
  * its 24 bits, and dx and dwg are rounded once.  A token whose logits are
- * all -inf has dlogits 0; one with a NaN logit has NaN.  n < 2^24, d < 2^20,
- * E*d < 2^29; MOE_BF16 needs d % 8 == 0 and 16-byte aligned x, wg, da_perm, dx and dwg.
+ * all -inf has dlogits 0; a NaN logit makes its token's p, and what takes p,
+ * NaN (renormalised without f: nothing does).  n < 2^24, d < 2^20, E*d < 2^29;
+ * MOE_BF16 needs d % 8 == 0 and 16-byte aligned x, wg, da_perm, dx and dwg.
  * Deterministic.  The size helper returns 0 for an invalid shape. */
 size_t moe_router_backward_workspace_bytes(const moe_shape *s);
 int moe_router_backward(const moe_shape *s, const float *logits, const int32_t *topk_idx,
