@@ -75,10 +75,18 @@ __global__ __launch_bounds__(256) void router_dz_kernel(
     dj = dw[row * k + gl];
   }
   const float D = group_sum((unsigned)c < (unsigned)E ? wj * dj : 0.f, G);
+  // A token whose logits are all -inf has no expert and no gradient.  The
+  // maximum cannot tell: fmaxf drops a NaN beside -inf, which lanes without an
+  // expert hold too.
   float m = z[0];
+  bool some = false;  // one of this lane's logits is not -inf (NaN counts)
 #pragma unroll
-  for (int i = 1; i < PER; ++i) m = fmaxf(m, z[i]);
+  for (int i = 0; i < PER; ++i) {
+    m = fmaxf(m, z[i]);
+    some |= !(z[i] == -__builtin_inff());
+  }
   m = group_max(m, G);
+  const bool any = (__ballot(some) >> g0 & (G == 64 ? ~0ull : (1ull << G) - 1)) != 0;
   float q[PER], s = 0.f, fp = 0.f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -106,8 +114,7 @@ __global__ __launch_bounds__(256) void router_dz_kernel(
       continue;
     }
     float v = 0.f;
-    // a token whose logits are all -inf has no expert and no gradient
-    if (m != -__builtin_inff()) {
+    if (any) {
       const float p = q[i] / s;
       v = renorm ? g[i] : p * (g[i] - D);
       if (f) v = fmaf(aux * p, fv[i] - fp, v);
