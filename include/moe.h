@@ -316,9 +316,9 @@ int moe_forward_noalloc(const moe_shape *s, const void *x, int act, const void *
  *   mean[t] = sum_c x[t][c] / d
  *   rstd[t] = 1 / sqrt(sum_c (x[t][c] - mean[t])^2 / d + eps)
  *   y[t][c] = (x[t][c] - mean[t]) rstd[t] weight[c] + bias[c]
- *   x, y       [n][d] (act = MOE_F32 or MOE_BF16); sums are float32, the
- *              variance is taken from differences from the mean, and y is
- *              rounded once
+ *   x, y       [n][d] (act = MOE_F32 or MOE_BF16); sums are float32 (the mean's
+ *              of MOE_F32 rows float64), the variance is taken from differences
+ *              from the mean, and y is rounded once
  *   weight     [d] f32; bias [d] f32 or NULL (none)
  *   mean, rstd [n] f32 outputs for the gradient; each may be NULL
  * 0 <= n < 2^30 (n = 0 does nothing), 1 <= d <= 16384, eps >= 0
