@@ -3,8 +3,9 @@
 Layer norm, the gated expert FFN with its kept pre-activations, and their
 gradients and the router's, each written from its formula in plain numpy
 float64.  It shares no code with the HIP library.  Every gradient here is
-pinned in ``tests/test_oracle_train.py`` by central differences of the
-forward functions and by torch's float64 autograd.
+pinned by central differences of the forward functions
+(``tests/test_oracle_train.py``) and by torch's float64 autograd through an
+independent layer (``tests/test_oracle_train_autograd.py``).
 
 Sources: "How Mixture of Experts Scales Model Parameters"
 (zhangchitc.github.io), sections "Routing", "Top-K", "The forward pass:
