@@ -739,9 +739,20 @@ using Small = Cfg<128, 128, 128, 4, 32, 4, 2>;
 
 // Small tiles where blocks are short, few, or mostly padding (measured, Big
 // against Small, us):
-//   at most 128 rows per expert: 128 experts, d = d_ff = 2880, 256 tokens top-4
-//     2840 against 2160, 4096 tokens Zipf-skewed 4190 against 3610 (uniform
-//     3806 against 4000); at 256 rows (8 experts, 1024 x 4096) 206 against 233
+//   at most 144 rows per expert.  The piles' own sizes decide, which the host
+//     does not know: with even piles Big is ahead from about 110 rows on, with
+//     Zipf-skewed ones Small up to 250 and more.  At 144 either mistake costs
+//     about as much:
+//       128 experts, 2880 x 2880: even, 64 rows 3160 against 2890, 112 rows 3540
+//         against 3600, 144 4050 against 4260, 208 4700 against 4960; skewed, 64
+//         rows 2910 against 2560, 144 4290 against 3880, 208 5180 against 4910
+//       64 experts, 2048 x 4096: even, 64 rows 1650 against 1580, 112 rows 1820
+//         against 1920, 144 2030 against 2240; skewed, 144 rows 2160 against
+//         1940, 256 3000 against 2790
+//       128 experts, 2048 x 768: even, 80 rows 718 against 643, 112 rows 755
+//         against 752, 144 823 against 857; skewed, 144 rows 842 against 774, 208
+//         1041 against 959
+//       8 experts, 1024 x 4096: even, 256 rows 206 against 233
 //   the dh product under half a round of the CUs: 1 expert, 2048 x 8192, 500
 //     tokens 168 against 154; 1024 tokens (160 blocks) 260 against 253
 //   padding: d = 264, d_ff = 520, 8000 tokens 135 against 91.  Without padding
@@ -749,7 +760,7 @@ using Small = Cfg<128, 128, 128, 4, 32, 4, 2>;
 //     against 14.1 ms).
 bool use_small(const FfnGradArgs &a) {
   auto area = [&](int b) { return (double)(tiles(a.d, b) * b) * (tiles(a.d_ff, b) * b); };
-  return a.R <= 128ll * a.E || row_tiles(a.R, a.E, Big::RBM) * tiles(a.d_ff, Big::RBN) < 128 ||
+  return a.R <= 144ll * a.E || row_tiles(a.R, a.E, Big::RBM) * tiles(a.d_ff, Big::RBN) < 128 ||
          1.2 * area(128) < area(256);
 }
 
