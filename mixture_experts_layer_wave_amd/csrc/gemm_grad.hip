@@ -19,12 +19,13 @@
 // the forward GEMM (gemm_big.hip).  Loads past a buffer's record count return zero:
 // that fills ragged rows, columns and the K tail.
 //
-// Measured, 8 experts of 4096 x 14336 and 16384 rows (11.5 Tflop): dh 2117 us,
-// the rest 9070 us; within it da's blocks run at 1240 TFLOP/s and the weight
-// tiles' loops at 1090 to 1200, where the power limit sets the clock (a large
-// library product: 1222).  8 experts of 1024 x 4096, 4096 rows: 75 and 229 us.
-// 128 experts of 2880 x 2880, 16384 skewed rows: 663 and 2905 us, bound by the
-// 13 GB of weights and gradients.
+// Measured (medians of profiled launches), 8 experts of 4096 x 14336 and 16384
+// rows (11.5 Tflop): dh 2116 us, the rest 9106 us; within it da's blocks run at
+// 1240 TFLOP/s and the weight tiles' loops at 1090 to 1200, where the power
+// limit sets the clock (a large library product: 1222).  8 experts of 1024 x
+// 4096, 4096 rows: 81 and 251 us (the whole pass 305 back to back).  128 experts
+// of 2880 x 2880, 16384 skewed rows: 663 and 2896 us for 13 GB of weights,
+// gradients and activations.
 #include <atomic>
 #include <type_traits>
 
@@ -184,7 +185,9 @@ __device__ __forceinline__ void store_lines_f32(const f32x16 (&acc)[TM][TN], __a
 // and the stores carry the non-temporal hint (Mixtral-shaped, 8 experts, 4096
 // x 14336, 16384 rows: 2240 -> 2133 us); blocks that share a CU overlap each
 // other and keep the registers.  dh0, h and the products stay float32; dg, du
-// and w h are rounded once to bf16, the type of the MFMA that reads them next.
+// and w h are rounded once to bf16, the type of the MFMA that reads them next:
+// the gradients are then off by 2.3e-3 of themselves (root mean square, against
+// 64 bits), where their own rounding to bf16 alone is 1.7e-3.
 // The row sums of dh0 h over 64 columns go to part[column / 64][row].  s_w:
 // combine weights of the tile's rows.
 template <int TM, int TN, int WM, int WN, bool ALONE>

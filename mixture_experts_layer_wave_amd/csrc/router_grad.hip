@@ -18,9 +18,11 @@
 // rounded only on their way out.  Both products are too narrow (E) to matter
 // beside their traffic: dx reads n k + writes n rows of d, dW_g reads n.
 //
-// Measured: 8192 tokens of 4096, 8 experts top-2 66.9 us (269 MB, 53 us at a
-// copy's rate); 4096 of 2880, 128 experts top-4 54.2 us (29 us: there W_g's
-// tiles from L2 and the two halves of dz weigh as much as the rows).
+// Measured: 8192 tokens of 4096, 8 experts top-2 67.0 us (269 MB, 53 us at a
+// copy's rate); 4096 of 2880, 128 experts top-4 53.7 us (29 us: there W_g's
+// tiles from L2 and the two halves of dz weigh as much as the rows, and the dz
+// and sum launches take 10 us).  float32, the same two: 268 and 189 us (106 and
+// 57: the gathered rows come four separate dwords at a time, after the product).
 #include <atomic>
 
 #include "common.h"
@@ -427,9 +429,9 @@ __global__ __launch_bounds__(256) void router_sum_kernel(const float *__restrict
 
 // ---- float32 ----------------------------------------------------------------------
 using namespace f32gemm;
-// (E = 8, 1024 wide, 4096 tokens: dx in One 35.3 us against 41.9 for the whole
-// pass in Two; dW_g, with E = 128, 2880 wide, 8000 tokens: 348 in Two against
-// 363)
+// (the whole pass, E = 8, 1024 wide, 4096 tokens: 35.3 us with dx in One, 41.9
+// with it in Two; E = 128, 2880 wide, 8000 tokens: 348 us with dW_g in Two, 363
+// with it in One)
 using One = Groups<1>;
 using Two = Groups<2>;
 
