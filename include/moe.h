@@ -350,8 +350,10 @@ int moe_layer_norm_backward(int32_t n, int32_t d, const void *dy, const void *x,
  * moe_expert_up; h goes to moe_expert_down.  Rows outside the piles are left
  * as they were.  F32 and BF16 weights only (MOE_ERR_DTYPE otherwise); d and
  * d_ff below 2^20, and operands under 2^31 bytes: n*k*max(d, d_ff) and
- * d*d_ff below 2^30 with BF16 and 2^29 with F32 weights (MOE_ERR_SHAPE);
- * with BF16 weights a, h, g and u 16-byte aligned.
+ * d*d_ff below 2^30 with BF16 and 2^29 with F32 weights, and grids under 2^32
+ * threads, which only a d or d_ff of a few elements beside a very long other
+ * one, or 2^28 pile rows, pass (MOE_ERR_SHAPE); with BF16 weights a, h, g and u
+ * 16-byte aligned.
  * A dense gated feed-forward block is the case E = 1, k = 1, perm = NULL,
  * offsets = {0, n}. */
 int moe_expert_up_save(const moe_shape *s, const void *a, int act, const int32_t *perm,

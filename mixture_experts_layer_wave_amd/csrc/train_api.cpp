@@ -22,6 +22,23 @@ int check_norm(int32_t n, int32_t d, int act) {
   return MOE_OK;
 }
 
+// The training FFN's largest grids, in threads: those of the products over pile
+// rows (512 a block at most), of da and the three weight gradients together
+// (256 a block; larger tiles have fewer blocks), and of the last kernel (1024 a
+// block).  A launch takes less than 2^32.  Only a d or d_ff of a few elements
+// beside a very long other side, or piles of hundreds of millions of rows, come
+// near it.
+bool grids_fit(const moe_shape *s, int wdt) {
+  const long long T = wdt == MOE_F32 ? 64 : 128;  // the smallest tiles
+  auto tiles = [](long long v, long long t) { return (v + t - 1) / t; };
+  const long long R = (long long)s->n * s->k, ft = tiles(s->d_ff, T), dt = tiles(s->d, T);
+  const long long rt = tiles(R, T) + std::min<long long>(s->E, R);
+  // (two of da's K ranges; there are more only where its blocks are a few hundred)
+  const long long rest = 2 * rt * dt + 2048 + 3 * s->E * ft * dt + 16ll * s->E;
+  const long long last = tiles(R, 64) + tiles(R * s->d, 1024);
+  return std::max({rt * ft * 512, rest * 256, last * 1024}) < (1ll << 32);
+}
+
 // Shapes and weights of the training FFN: weights that are trained (F32 or
 // BF16), sizes that every product's grid and buffer offsets take.
 int check_ffn_shape(const moe_shape *s, int act, int wdt) {
@@ -35,7 +52,7 @@ int check_ffn_shape(const moe_shape *s, int act, int wdt) {
   const long long R = (long long)s->n * s->k, bytes = wdt == MOE_F32 ? 4 : 2;
   if (R * std::max(s->d, s->d_ff) * bytes >= (1ll << 31) || (long long)s->d * s->d_ff * bytes >= (1ll << 31))
     return MOE_ERR_SHAPE;
-  return MOE_OK;
+  return grids_fit(s, wdt) ? MOE_OK : MOE_ERR_SHAPE;
 }
 
 int check_ffn(const moe_shape *s, int act, const moe_expert_weights *w) {
