@@ -2,7 +2,9 @@
  * moe.h -- C ABI of libmoe_mi355x.so, the sparse Mixture-of-Experts layer
  * for AMD Instinct MI355X (gfx950): its forward pass, and, in the second
  * part of this file, what training it needs (layer norm, the expert FFN that
- * keeps its pre-activations, and the gradients).
+ * keeps its pre-activations, and the gradients); in the third, what serving
+ * an MXFP4 layer token by token needs (the MXFP4 encoder and product, the
+ * layer for a few tokens) and the norms around a block, with their gradient.
  *
  * What is computed follows "How Mixture of Experts Scales Model Parameters"
  * (zhangchitc.github.io/posts/mixture-of-experts/):
@@ -60,7 +62,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 5
+#define MOE_ABI_VERSION 6
 
 typedef enum {
   MOE_OK = 0,
@@ -429,6 +431,122 @@ int moe_router_backward(const moe_shape *s, const float *logits, const int32_t *
                         const void *x, int act, const void *wg, const void *da_perm,
                         const int32_t *inv, float *dlogits, void *dx, void *dwg, float *dbias,
                         void *ws, size_t ws_bytes, void *stream);
+
+/* ---- MXFP4, a few tokens, norms around a block ----------------------------- */
+
+/* MXFP4 encoding of x [rows][cols] (act = MOE_F32 or MOE_BF16): codes q
+ * [rows][cols/2] and scales s [rows][cols/32], the layout of the experts'
+ * weights.  Per block of 32: X = max(floor(log2 amax) - 2, -127), scale code
+ * X + 127 (0 for a block of zeros); each element is v / 2^X to the nearest
+ * E2M1 value, ties to the even code, at most 6.  A block holding an infinity
+ * or a NaN gets scale code 255 (NaN) and codes 0: all of it reads as NaN.
+ * 0 <= rows < 2^31 (0 does nothing), cols % 32 == 0; pointers 16-byte
+ * aligned.  E matrices of the same width are one call of E * rows rows. */
+int moe_quantize_mxfp4(int64_t rows, int32_t cols, const void *x, int act, uint8_t *q, uint8_t *s,
+                       void *stream);
+
+/* The values of an MXFP4 matrix: y [rows][cols], out = MOE_F32 or MOE_BF16.
+ * Both hold every value below 2^128 exactly (scale code 0 with an element of
+ * 0.5, 2^-128, included); values past that (scale codes 253 and 254 only)
+ * become infinities, and scale code 255 gives NaN.  Limits as in
+ * moe_quantize_mxfp4. */
+int moe_dequantize_mxfp4(int64_t rows, int32_t cols, const uint8_t *q, const uint8_t *s, void *y,
+                         int out, void *stream);
+
+/* Product with an MXFP4 matrix:  y[t] = x[t] W^T + bias.
+ *   w, w_s  [m][d/2] codes and [m][d/32] scales
+ *   x       act = MOE_BF16: [n][d] bf16, x_s NULL or ignored.  act =
+ *           MOE_MXFP4: [n][d/2] codes with scales x_s [n][d/32] (as
+ *           moe_quantize_mxfp4 writes them); both operands then enter the
+ *           matrix cores in their stored form
+ *   bias    [m] f32 or NULL
+ *   y       [n][m], out = MOE_F32 or MOE_BF16 (the float32 sum, bias
+ *           included, rounded once)
+ *   ws      at least moe_mxfp4_linear_workspace_bytes(n, d, m, act), 16-byte
+ *           aligned; NULL where that is 0
+ * n = 0 does nothing.  d % 32 == 0, any m >= 1; n * max(d, m) and m * d below
+ * 2^30 (MOE_ERR_SHAPE otherwise; a larger call is split by the caller);
+ * pointers 16-byte aligned (bias: 4).  Deterministic. */
+size_t moe_mxfp4_linear_workspace_bytes(int32_t n, int32_t d, int32_t m, int act);
+int moe_mxfp4_linear(int32_t n, int32_t d, int32_t m, const void *x, const uint8_t *x_s, int act,
+                     const uint8_t *w, const uint8_t *w_s, const float *bias, void *y, int out, void *ws,
+                     size_t ws_bytes, void *stream);
+
+/* The whole layer, as moe_forward, for at most MOE_FEW_MAX_TOKENS tokens, in
+ * two launches: for decoding, where the layer's time is that of reading the
+ * chosen experts and of the launches between its steps.
+ *   Arguments, results and refusals: as moe_forward, but for the workspace
+ *   (moe_forward_few_workspace_bytes) and for what is refused beside:
+ *   n > MOE_FEW_MAX_TOKENS and n * k * d_ff >= 2^30 (MOE_ERR_SHAPE), and
+ *   act_quant (MOE_ERR_DTYPE).
+ * Each hidden value is multiplied by its combine weight in float32 and rounded
+ * once to the activations' type; outputs are summed in float32 over the
+ * experts and rounded once.  Deterministic; a token's output may differ in its
+ * last bits from moe_forward's and with the other tokens of the call.
+ * Within the second kernel, workgroups that form outputs wait for those that
+ * form the hidden.  The wait ends whatever else runs on the device: only
+ * workgroups that are running already are waited for. */
+#define MOE_FEW_MAX_TOKENS 16
+size_t moe_forward_few_workspace_bytes(const moe_shape *s, int w_dtype);
+int moe_forward_few(const moe_shape *s, const void *x, int act, const void *wg, const float *bias,
+                    const moe_expert_weights *w, void *y, int out, int32_t *topk_idx, float *topk_w,
+                    void *ws, size_t ws_bytes, void *stream);
+
+/* A norm over rows of d (a HOST struct, read during the call only):
+ *   MOE_NORM_LAYER: (v - mean) rstd weight + bias, as moe_layer_norm
+ *   MOE_NORM_RMS:   v rstd weight + bias, rstd = 1 / sqrt(avg(v^2) + eps)
+ * weight [d] f32 (device), bias [d] f32 or NULL (none), eps >= 0. */
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
+typedef struct {
+  int32_t kind;
+  float eps;
+  const float *weight, *bias;
+} moe_norm;
+
+/* What stands between one block and the next: the norm behind the block, its
+ * gate, the residual's scale, and the next block's norm.
+ *   h[t] = scale x[t] + gate * post(z[t]),   u[t] = pre(h[t])
+ *   x, z   [n][d] residual stream and block output (act = MOE_F32 or MOE_BF16)
+ *   gate   [d] f32, or NULL (ones)
+ *   post   norm of z, or NULL (z itself)
+ *   pre    norm of h, or NULL (u is then not written and may be NULL)
+ *   h, u   [n][d] outputs (act), rounded once each; u is taken from h before
+ *          its rounding.  h may be x or z, and u may be x or z (not both the
+ *          same one): a row is read before it is written
+ *   stats  [4][n] f32 for the gradient, or NULL: post's mean and rstd, pre's
+ *          mean and rstd (mean 0 for an RMS norm; rows of absent norms are
+ *          left as they were)
+ * Sums are float32 (the mean's of MOE_F32 rows float64), variances are taken
+ * from differences.  Sizes and alignment as in moe_layer_norm. */
+int moe_block_norm(int32_t n, int32_t d, const void *x, const void *z, int act, float scale,
+                   const float *gate, const moe_norm *post, const moe_norm *pre, void *h, void *u,
+                   float *stats, void *stream);
+
+/* Gradient of moe_block_norm.  With D = dh + (pre's gradient of du at h):
+ *   dx = scale D,   dz = post's gradient of (gate * D) at z,
+ *   dgate = sum_t D[t] post(z[t]), and the norms' weights and biases as in
+ *   moe_layer_norm_backward, from du and from gate * D
+ *   dh     [n][d], the gradient that reaches h from elsewhere, or NULL (with
+ *          pre only: zeros)
+ *   du     [n][d], required with pre
+ *   z, h   as given to and written by the forward pass (z: with post or gate;
+ *          h: with pre); stats as it wrote them
+ *   dx, dz [n][d] outputs (act), rounded once; each may be dh or du (not both
+ *          the same one)
+ *   dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias [d] f32 outputs,
+ *          overwritten; each may be NULL, and has to be where the call has no
+ *          such gate or norm (MOE_ERR_NULL).  A bias's gradient is given for
+ *          a norm without one too
+ *   ws     at least moe_block_norm_backward_workspace_bytes(n, d), 16-byte
+ *          aligned
+ * Same limits; n = 0 writes zeros to the parameters' gradients.  Sums over
+ * rows run in a fixed order (deterministic). */
+size_t moe_block_norm_backward_workspace_bytes(int32_t n, int32_t d);
+int moe_block_norm_backward(int32_t n, int32_t d, const void *dh, const void *du, const void *z,
+                            const void *h, int act, float scale, const float *gate, const moe_norm *post,
+                            const moe_norm *pre, const float *stats, void *dx, void *dz, float *dgate,
+                            float *dpost_weight, float *dpost_bias, float *dpre_weight, float *dpre_bias,
+                            void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -17,6 +17,9 @@ import os
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi355x.so")
 
 MOE_F32, MOE_BF16, MOE_MXFP4, MOE_MXFP8 = 0, 1, 2, 3
+MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
+MOE_FEW_MAX_TOKENS = 16
+NORMS = {"layer": MOE_NORM_LAYER, "rms": MOE_NORM_RMS}
 DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp4": MOE_MXFP4, "mxfp8": MOE_MXFP8}
 
 if not os.path.exists(LIB_PATH):
@@ -43,6 +46,13 @@ class ExpertWeights(ctypes.Structure):
                 ("act_quant", ctypes.c_int32)]
 
 
+class Norm(ctypes.Structure):
+    # kind: MOE_NORM_LAYER or MOE_NORM_RMS; weight and bias: device float32 [d]
+    # (bias may be NULL)
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -54,6 +64,9 @@ _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _SP = ctypes.POINTER(Shape)
 _WP = ctypes.POINTER(ExpertWeights)
+_NP = ctypes.POINTER(Norm)
+_L = ctypes.c_int64
+_F = ctypes.c_float
 
 lib.moe_abi_version.restype = _I
 lib.moe_abi_version.argtypes = []
@@ -107,6 +120,25 @@ lib.moe_router_backward_workspace_bytes.argtypes = [_SP]
 lib.moe_router_backward.restype = _I
 lib.moe_router_backward.argtypes = [_SP, _P, _P, _P, _P, _P, ctypes.c_float, _P, _I, _P, _P, _P, _P, _P, _P,
                                     _P, _P, _SZ, _P]
+lib.moe_quantize_mxfp4.restype = _I
+lib.moe_quantize_mxfp4.argtypes = [_L, _I, _P, _I, _P, _P, _P]
+lib.moe_dequantize_mxfp4.restype = _I
+lib.moe_dequantize_mxfp4.argtypes = [_L, _I, _P, _P, _P, _I, _P]
+lib.moe_mxfp4_linear_workspace_bytes.restype = _SZ
+lib.moe_mxfp4_linear_workspace_bytes.argtypes = [_I, _I, _I, _I]
+lib.moe_mxfp4_linear.restype = _I
+lib.moe_mxfp4_linear.argtypes = [_I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _I, _P, _SZ, _P]
+lib.moe_forward_few_workspace_bytes.restype = _SZ
+lib.moe_forward_few_workspace_bytes.argtypes = [_SP, _I]
+lib.moe_forward_few.restype = _I
+lib.moe_forward_few.argtypes = [_SP, _P, _I, _P, _P, _WP, _P, _I, _P, _P, _P, _SZ, _P]
+lib.moe_block_norm.restype = _I
+lib.moe_block_norm.argtypes = [_I, _I, _P, _P, _I, _F, _P, _NP, _NP, _P, _P, _P, _P]
+lib.moe_block_norm_backward_workspace_bytes.restype = _SZ
+lib.moe_block_norm_backward_workspace_bytes.argtypes = [_I, _I]
+lib.moe_block_norm_backward.restype = _I
+lib.moe_block_norm_backward.argtypes = [_I, _I, _P, _P, _P, _P, _I, _F, _P, _NP, _NP, _P, _P, _P, _P, _P, _P,
+                                        _P, _P, _P, _SZ, _P]
 
 EXPORTS = ("moe_abi_version", "moe_status_string", "moe_workspace_bytes", "moe_mxfp8_bytes",
            "moe_quantize_mxfp8", "moe_router_topk",
@@ -115,7 +147,10 @@ EXPORTS = ("moe_abi_version", "moe_status_string", "moe_workspace_bytes", "moe_m
            "moe_forward", "moe_forward_noalloc", "moe_layer_norm",
            "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward",
            "moe_expert_up_save", "moe_grouped_ffn_backward_workspace_bytes", "moe_grouped_ffn_backward",
-           "moe_router_backward_workspace_bytes", "moe_router_backward")
+           "moe_router_backward_workspace_bytes", "moe_router_backward", "moe_quantize_mxfp4",
+           "moe_dequantize_mxfp4", "moe_mxfp4_linear_workspace_bytes", "moe_mxfp4_linear",
+           "moe_forward_few_workspace_bytes", "moe_forward_few", "moe_block_norm",
+           "moe_block_norm_backward_workspace_bytes", "moe_block_norm_backward")
 
 
 def _ptr(t):
@@ -160,6 +195,17 @@ def _weights(w) -> ExpertWeights:
     return ExpertWeights(_dt(w["dtype"]), _ptr(w["w1"]), _ptr(w["w3"]), _ptr(w["w2"]),
                          _ptr(w.get("s1")), _ptr(w.get("s3")), _ptr(w.get("s2")),
                          _ptr(w.get("slot")), int(w.get("n_slots", 0)), _dt(aq) if aq else 0)
+
+
+def _norm(v):
+    """A Norm by reference, from a Norm, a dict (kind "layer" or "rms", weight, bias, eps) or None."""
+    if v is None:
+        return None
+    if not isinstance(v, Norm):
+        kind = v["kind"]
+        v = Norm(NORMS[kind] if isinstance(kind, str) else int(kind), float(v.get("eps", 1e-5)),
+                 _ptr(v["weight"]), _ptr(v.get("bias")))
+    return ctypes.byref(v)
 
 
 def moe_abi_version() -> int:
@@ -304,3 +350,52 @@ def moe_router_backward(shape, logits, topk_idx, topk_w, dtopk_w, f, alpha, x, a
         ctypes.byref(_shape(shape)), _ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(dtopk_w), _ptr(f),
         float(alpha), _ptr(x), _dt(act), _ptr(wg), _ptr(da_perm), _ptr(inv), _ptr(dlogits), _ptr(dx),
         _ptr(dwg), _ptr(dbias), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moe_quantize_mxfp4(rows, cols, x, act, q, s, stream=None):
+    _check("moe_quantize_mxfp4", lib.moe_quantize_mxfp4(
+        int(rows), int(cols), _ptr(x), _dt(act), _ptr(q), _ptr(s), _stream(stream)))
+
+
+def moe_dequantize_mxfp4(rows, cols, q, s, y, out, stream=None):
+    _check("moe_dequantize_mxfp4", lib.moe_dequantize_mxfp4(
+        int(rows), int(cols), _ptr(q), _ptr(s), _ptr(y), _dt(out), _stream(stream)))
+
+
+def moe_mxfp4_linear_workspace_bytes(n, d, m, act) -> int:
+    return int(lib.moe_mxfp4_linear_workspace_bytes(int(n), int(d), int(m), _dt(act)))
+
+
+def moe_mxfp4_linear(n, d, m, x, x_s, act, w, w_s, bias, y, out, ws=None, ws_bytes=0, stream=None):
+    _check("moe_mxfp4_linear", lib.moe_mxfp4_linear(
+        int(n), int(d), int(m), _ptr(x), _ptr(x_s), _dt(act), _ptr(w), _ptr(w_s), _ptr(bias), _ptr(y),
+        _dt(out), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moe_forward_few_workspace_bytes(shape, w_dtype) -> int:
+    return int(lib.moe_forward_few_workspace_bytes(ctypes.byref(_shape(shape)), _dt(w_dtype)))
+
+
+def moe_forward_few(shape, x, act, wg, bias, weights, y, out, topk_idx, topk_w, ws, ws_bytes, stream=None):
+    w = _weights(weights)
+    _check("moe_forward_few", lib.moe_forward_few(
+        ctypes.byref(_shape(shape)), _ptr(x), _dt(act), _ptr(wg), _ptr(bias), ctypes.byref(w), _ptr(y),
+        _dt(out), _ptr(topk_idx), _ptr(topk_w), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moe_block_norm(n, d, x, z, act, scale, gate, post, pre, h, u=None, stats=None, stream=None):
+    _check("moe_block_norm", lib.moe_block_norm(
+        int(n), int(d), _ptr(x), _ptr(z), _dt(act), float(scale), _ptr(gate), _norm(post), _norm(pre), _ptr(h),
+        _ptr(u), _ptr(stats), _stream(stream)))
+
+
+def moe_block_norm_backward_workspace_bytes(n, d) -> int:
+    return int(lib.moe_block_norm_backward_workspace_bytes(int(n), int(d)))
+
+
+def moe_block_norm_backward(n, d, dh, du, z, h, act, scale, gate, post, pre, stats, dx, dz, dgate,
+                            dpost_weight, dpost_bias, dpre_weight, dpre_bias, ws, ws_bytes, stream=None):
+    _check("moe_block_norm_backward", lib.moe_block_norm_backward(
+        int(n), int(d), _ptr(dh), _ptr(du), _ptr(z), _ptr(h), _dt(act), float(scale), _ptr(gate), _norm(post),
+        _norm(pre), _ptr(stats), _ptr(dx), _ptr(dz), _ptr(dgate), _ptr(dpost_weight), _ptr(dpost_bias),
+        _ptr(dpre_weight), _ptr(dpre_bias), _ptr(ws), int(ws_bytes), _stream(stream)))

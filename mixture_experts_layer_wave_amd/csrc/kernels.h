@@ -201,4 +201,68 @@ hipError_t launch_layer_norm_grad(const void *dy, const void *x, bool bf16, cons
                                   const float *mean, const float *rstd, int n, int d, void *dx,
                                   float *dw, float *db, float *part, hipStream_t st);
 
+// ---- MXFP4 codec and product ----------------------------------------------
+// blocks = rows * cols / 32 consecutive blocks (float32 or bf16 values at x, y).
+hipError_t launch_quantize_mx4(const void *x, bool is_bf16, size_t blocks, uint8_t *q, uint8_t *s,
+                               hipStream_t st);
+hipError_t launch_dequantize_mx4(const uint8_t *q, const uint8_t *s, size_t blocks, void *y,
+                                 bool out_bf16, hipStream_t st);
+// y [n][m] = x [n][d] W^T + bias; x bf16, or MXFP4 codes with scales x_s.
+struct LinearArgs {
+  int n, d, m;
+  const void *x;
+  const uint8_t *x_s;
+  bool x_mx4;
+  const uint8_t *w, *w_s;
+  const float *bias;
+  void *y;
+  bool out_bf16;
+  void *ws;  // mxfp4_linear_bytes
+};
+size_t mxfp4_linear_bytes(int n, int d, int m, bool x_mx4);
+hipError_t launch_mxfp4_linear(const LinearArgs &a, hipStream_t st);
+
+// ---- the layer for a few tokens ---------------------------------------------
+constexpr int kFewMaxTokens = 16;
+struct FewArgs {
+  const void *x, *wg;
+  const float *bias;
+  int n, d, E, k, d_ff, renorm;
+  int w_dtype;  // 0 f32, 1 bf16, 2 mxfp4
+  const void *w1, *w3, *w2;
+  const uint8_t *s1, *s3, *s2;
+  const int32_t *slot;
+  int n_slots;
+  void *y;
+  bool out_bf16;
+  int32_t *idx;  // [n][k] or NULL
+  float *w;      // [n][k] or NULL
+  void *ws;      // forward_few_bytes
+};
+size_t forward_few_bytes(int n, int E, int k, int d_ff, bool f32);
+hipError_t launch_forward_few(const FewArgs &a, hipStream_t st);
+
+// ---- norms around a block ----------------------------------------------------
+struct BlockNorm {
+  int kind;  // 0 none, 1 layer, 2 rms
+  float eps;
+  const float *weight, *bias;
+};
+struct BlockNormArgs {
+  int n, d;
+  bool bf16;
+  float scale;
+  const float *gate;
+  BlockNorm post, pre;
+  const void *x, *z;
+  void *h, *u;    // forward: outputs; gradient: h as it was kept
+  float *stats;   // [4][n]: post mean, rstd, pre mean, rstd
+  const void *dh, *du;
+  void *dx, *dz;
+  float *dgate, *dpost_w, *dpost_b, *dpre_w, *dpre_b, *part;  // part: block_norm_grad_bytes
+};
+hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t st);
+size_t block_norm_grad_bytes(int n, int d);
+hipError_t launch_block_norm_grad(const BlockNormArgs &a, hipStream_t st);
+
 }  // namespace moe

@@ -4,8 +4,10 @@
 :func:`mixture_experts_layer_wave_amd.workloads.make_layer`) to device
 memory, sizes the workspace with ``moe_workspace_bytes`` and calls the
 library's entry points.  :class:`TrainingLayer` adds the norm in front of the
-layer, the buffers that a training step keeps, and the gradients.  torch
-provides device memory and streams only.
+layer, the buffers that a training step keeps, and the gradients.
+:class:`DecodeBlock` serves a layer a few tokens at a time: experts encoded as
+MXFP4, the norms around the layer, and an output projection.  torch provides
+device memory and streams only.
 """
 
 from __future__ import annotations
@@ -137,3 +139,64 @@ class TrainingLayer(DeviceLayer):
         B.moe_layer_norm_backward(self.n, self.d, self.dxn, self.x, self.act, self.norm_weight, self.mean,
                                   self.rstd, gr["x"], gr["norm_weight"], gr["norm_bias"], ws, nb, stream)
         return gr
+
+
+def encode_mxfp4(w, stream=None):
+    """(codes, scales) of a device tensor [..., cols] of bf16 or float32 in
+    MXFP4, by moe_quantize_mxfp4."""
+    act = "f32" if w.dtype == torch.float32 else "bf16"
+    cols = w.shape[-1]
+    q = torch.empty((*w.shape[:-1], cols // 2), dtype=torch.uint8, device=w.device)
+    s = torch.empty((*w.shape[:-1], cols // 32), dtype=torch.uint8, device=w.device)
+    B.moe_quantize_mxfp4(w.numel() // cols, cols, w, act, q, s, stream)
+    return q, s
+
+
+class DecodeBlock:
+    """A layer with the norms around it, for at most 16 tokens a step:
+
+        z = layer(u),  h <- scale h + gate * post(z),  u <- pre(h),  logits = u head^T
+
+    with the experts and the head in MXFP4.  ``w1``, ``w3`` [E][d_ff][d], ``w2``
+    [E][d][d_ff] and ``head`` [m][d] (or None) are bf16 or float32 device
+    tensors, encoded once; ``wg`` [E][d] is bf16, ``bias`` float32 or None.
+    ``post`` and ``pre`` are dicts (kind "layer" or "rms", weight, bias, eps)
+    or None.  :meth:`step` works on the block's own h and u [n][d] in place and
+    neither allocates nor synchronises, so it can be captured in a HIP graph.
+    """
+
+    def __init__(self, n, wg, w1, w3, w2, k, bias=None, scale=1.0, gate=None, post=None, pre=None, head=None,
+                 renorm=-1):
+        E, d_ff, d = w1.shape
+        dev = w1.device
+        self.n, self.d, self.wg, self.bias = n, d, wg, bias
+        self.shape = B.Shape(n, d, E, k, d_ff, renorm)
+        self.scale, self.gate, self.post, self.pre = scale, gate, post, pre
+        self.experts = dict(dtype="mxfp4")
+        for key, w in (("1", w1), ("3", w3), ("2", w2)):
+            self.experts["w" + key], self.experts["s" + key] = encode_mxfp4(w)
+        self.weights = B._weights(self.experts)
+
+        def empty(*shape, dtype=torch.bfloat16):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        self.h, self.u, self.z = empty(n, d), empty(n, d), empty(n, d)
+        self.idx, self.topw = empty(n, k, dtype=torch.int32), empty(n, k, dtype=torch.float32)
+        need = B.moe_forward_few_workspace_bytes(self.shape, "mxfp4")
+        self.head = None
+        if head is not None:
+            self.head, self.m = encode_mxfp4(head), head.shape[0]
+            self.logits = empty(n, self.m, dtype=torch.float32)
+            need = max(need, B.moe_mxfp4_linear_workspace_bytes(n, d, self.m, "bf16"))
+        self.ws = empty(max(need, 16), dtype=torch.uint8)
+
+    def step(self, stream=None):
+        nb = self.ws.numel()
+        B.moe_forward_few(self.shape, self.u, "bf16", self.wg, self.bias, self.weights, self.z, "bf16", self.idx,
+                          self.topw, self.ws, nb, stream)
+        B.moe_block_norm(self.n, self.d, self.h, self.z, "bf16", self.scale, self.gate, self.post, self.pre,
+                         self.h, self.u if self.pre else None, None, stream)
+        if self.head:
+            B.moe_mxfp4_linear(self.n, self.d, self.m, self.u if self.pre else self.h, None, "bf16", *self.head,
+                               None, self.logits, "f32", self.ws, nb, stream)
+        return self.logits if self.head else self.u
