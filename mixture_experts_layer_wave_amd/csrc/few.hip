@@ -43,16 +43,29 @@ namespace moe {
 namespace {
 
 constexpr int kT = kFewMaxTokens;  // 16: the M of the MFMA
-constexpr int kThreads = 512, kWaves = kThreads / 64;
+#ifndef PW
+#define PW 8
+#define PI 4
+#endif
+constexpr int kWaves = PW, kThreads = kWaves * 64;
+constexpr int kInFlight = PI;  // chunks of weights
 constexpr int kFewLds = 160 * 1024;
-constexpr int kMaxXBytes = 112 * 1024;  // the tokens' rows in LDS, else read through the ring
 // Tries of a waiting output part (each at least a microsecond): seconds, where a
 // call takes microseconds.  Past it the part writes NaN.
 constexpr int kMaxTries = 1 << 23;
+// Parts done are counted in kDone counters (part i in counter i mod kDone), each on a
+// line of its own: 256 additions to one address, with the waiting workgroups reading
+// it, took 4 us.
+constexpr int kAhead = 6;  // pieces of the tokens' rows a thread fetches before the top-k
+constexpr int kQueue = 8;  // segments a wave has loaded ahead of those it finished, at most kInFlight + 1
+static_assert(kInFlight < kQueue, "segments ahead");
+constexpr int kDone = 8, kCountInts = 64;
 
 struct FewLds {
-  int x, pitch;     // tokens' rows (pitch bytes each); the output part's staging lies over it
-  int red, idx, w, mask, aidx, act, pile, misc, total;
+  int x;      // the tokens' row chunks, later a round's hidden
+  int cap;    // row chunks that fit there
+  int ex;     // the waves' exchange buffers
+  int idx, w, mask, aidx, act, slot, pre, pile, queue, misc, total;
 };
 
 struct FewParams {
@@ -67,59 +80,90 @@ struct FewParams {
   void *y;
   int32_t *idx;    // [n][k] or NULL
   float *w;
-  int *count;      // ticket counter, parts done
+  int *count;      // kCounts counters a line apart: tickets, then parts done in kDone pieces
   int G;
   FewLds lds;
 };
 
-template <int WT, int PER, int ARU, int ARD, int PFU, int PFD>
+// XL: the tokens' rows fit LDS.
+template <int WT, int PER, bool XL, bool NARROW, int PC>
 __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
   using F = Form<WT>;
-  constexpr int NF = F::kActBytes / 16;
+  constexpr int NF = F::kActBytes / 16, RC = kRowChunk<WT>;
+  constexpr int SL = (RC - 16) / 16;  // lanes of a row chunk
+  constexpr int kStage = WT == kMx ? 4 : 8;  // chunks whose hidden a wave fetches at a time
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const FewLds &L = p.lds;
   int *s_idx = (int *)(smem + L.idx), *s_mask = (int *)(smem + L.mask), *s_act = (int *)(smem + L.act);
-  float *s_w = (float *)(smem + L.w), *s_red = (float *)(smem + L.red);
+  int *s_slot = (int *)(smem + L.slot), *s_pre = (int *)(smem + L.pre);
+  float *s_w = (float *)(smem + L.w);
   uint16_t *s_aidx = (uint16_t *)(smem + L.aidx), *s_pile = (uint16_t *)(smem + L.pile);
-  int *s_misc = (int *)(smem + L.misc);  // active experts, ticket, whether the wait ended
+  int *s_misc = (int *)(smem + L.misc);  // active experts, ticket, whether the wait ended, tiles taken
+  int *s_queue = (int *)(smem + L.queue);
+  uint8_t *s_x = smem + L.x, *xbuf = smem + L.ex + (threadIdx.x >> 6) * kExchange;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = p.n, k = p.k, E = p.E, d = p.d, f = p.f, R = n * k, G = p.G;
   const size_t xrow = (size_t)d * (F::f32 ? 4 : 2), hrow = (size_t)f * (F::f32 ? 4 : 2);
+  const int Cd = (F::blocks(d) + kChunkBlocks - 1) / kChunkBlocks, Cf = (F::blocks(f) + kChunkBlocks - 1) / kChunkBlocks;
 
   auto take = [&]() {
     return __hip_atomic_fetch_add(p.count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
   int first = 0;
   if (tid == 0) first = take();
-  if constexpr (ARU == 0)  // the tokens' rows
-    for (int i = tid; i < n * (d / 8); i += kThreads) {
-      const int t = i / (d / 8), c = i % (d / 8);
-      *(u32x4 *)(smem + L.x + t * L.pitch + c * 16) = *(const u32x4 *)((const uint8_t *)p.x + t * xrow + c * 16);
-    }
+  // the tokens' rows: the first pieces are on their way during the top-k
+  u32x4 xq[kAhead];
+  auto x_piece = [&](int v) {
+    const int i = (v * kThreads + tid) / SL, c = i / n, t = i - c * n;
+    return row_chunk_piece<WT>((const uint8_t *)p.x + t * xrow, c, d, tid % SL);
+  };
+  const int pieces = XL ? (n * Cd * SL + kThreads - 1) / kThreads : 0;
+  auto x_live = [&](int v) { return (v * kThreads + tid) / SL < n * Cd; };
+  if constexpr (XL)
+#pragma unroll
+    for (int v = 0; v < kAhead; ++v)
+      if (v < pieces && x_live(v)) xq[v] = x_piece(v);
   for (int e = tid; e < E; e += kThreads) s_mask[e] = 0;
   const int TG = topk_group(E);
   for (int t0 = 0; t0 < n; t0 += kThreads / TG)
     topk_token_t<PER>(p.logits, 1, 0, t0 + tid / TG, n, E, k, p.renorm, s_idx, s_w, nullptr, nullptr);
+  if constexpr (XL) {
+    auto put = [&](int v, u32x4 q) {
+      *(u32x4 *)(s_x + (v * kThreads + tid) / SL * RC + tid % SL * 16) = q;
+    };
+#pragma unroll
+    for (int v = 0; v < kAhead; ++v)
+      if (v < pieces && x_live(v)) put(v, xq[v]);
+    for (int v = kAhead; v < pieces; ++v)
+      if (x_live(v)) put(v, x_piece(v));
+  }
+  if (tid == 0) s_misc[3] = 0;
   if (tid == 0) s_misc[1] = first;
   __syncthreads();
   // ---- who takes which expert ------------------------------------------------
   for (int q = tid; q < R; q += kThreads) atomicOr(&s_mask[s_idx[q]], 1 << (q / k));
   __syncthreads();
   if (wave == 0) {
-    int a = 0;
+    int a = 0, m0 = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
-      const int e = e0 + lane;
-      const bool on = e < E && s_mask[e] != 0;
-      const uint64_t bits = __ballot(on);
-      if (on) {
+      const int e = e0 + lane, m = e < E ? __popc(s_mask[e]) : 0;
+      const uint64_t bits = __ballot(m != 0);
+      const int incl = wave_incl_scan(m);
+      if (m) {
         const int at = a + __popcll(bits & ((1ull << lane) - 1));
         s_aidx[e] = (uint16_t)at;
         s_act[at] = e;
+        s_slot[at] = phys_slot(p.slot, p.n_slots, e);
+        s_pre[at] = m0 + incl - m;
       }
       a += __popcll(bits);
+      m0 += __builtin_amdgcn_readlane(incl, 63);
     }
-    if (lane == 0) s_misc[0] = a;
+    if (lane == 0) {
+      s_misc[0] = a;
+      s_pre[a] = m0;
+    }
   }
   __syncthreads();
   for (int q = tid; q < R; q += kThreads) {
@@ -127,8 +171,8 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
     s_pile[s_aidx[e] * kT + __popc(s_mask[e] & ((1 << t) - 1))] = (uint16_t)q;
   }
   __syncthreads();
-  const int A = s_misc[0];
-  int ticket = s_misc[1];
+  const int A = uniform(s_misc[0]);
+  int ticket = uniform(s_misc[1]);
 
   if (ticket == 0 && p.idx)
     for (int q = tid; q < R; q += kThreads) p.idx[q] = s_idx[q];
@@ -140,50 +184,54 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
   while (ticket < 2 * G) {
     if (ticket < G) {
       // ---- up: hidden columns [u0, u1) of the chosen experts' A f -----------
-      const long long U = (long long)A * f, NW = (long long)G * kWaves, wv = (long long)ticket * kWaves + wave;
-      const int u0 = (int)(U * wv / NW), u1 = (int)(U * (wv + 1) / NW);
-      // Tiles: runs of at most 8 columns of one expert.
-      auto tile_at = [&](int u, int &a, int &c, int &cnt) {
-        a = u / f;
-        c = u - a * f;
-        cnt = min(8, min(u1 - u, f - c));
-      };
-      int tiles = 0;
-      for (int u = u0; u < u1;) {
-        int a, c, cnt;
-        tile_at(u, a, c, cnt);
-        u += cnt;
-        ++tiles;
-      }
-      const int S = (F::blocks(d) + 3) / 4;
-      int lu = u0, eu = u0;  // first column of the tile to load, to finish
+      const long long U = (long long)A * f;
+      const int u0 = (int)(U * ticket / G), cols = (int)(U * (ticket + 1) / G) - u0;
+      // Tiles of at most 8 columns, a tile for every wave at least; the waves take them
+      // in turn (the older waves of a SIMD run ahead of the younger).  A tile has a
+      // segment for each expert it meets.
+      const int tiles = max((cols + 7) / 8, min(cols, kWaves));
+      int lu = 0, lu_to = 0;  // what is left of the tile to load
+      int *queue = s_queue + wave * (2 * kQueue);  // the segments' first columns and widths
       const size_t rb = F::row_bytes(d);
-      stream<WT, PFU, ARU>(
-          tiles * S, S, 0, d, smem + L.x + wave * 1024 * (ARU ? ARU : 1),
-          [&](int, const uint8_t *&row, const uint8_t *&srow, const uint8_t *(&arow)[ARU ? ARU : 1],
-              const uint8_t *&) {
-            int a, c, cnt;
-            tile_at(lu, a, c, cnt);
+      const int tok = min(r, n - 1);  // (rows past the last token: any)
+      stream<WT, PC, NARROW>(
+          0x7fffffff, Cd, 0, d, xbuf,
+          [&](int i, RowGroups &w) {
+            if (lu == lu_to) {
+              int t = 0;
+              if (lane == 0) t = atomicAdd(&s_misc[3], 1);
+              t = uniform(t);
+              if (t >= tiles) return false;
+              lu = u0 + (int)((long long)cols * t / tiles);
+              lu_to = u0 + (int)((long long)cols * (t + 1) / tiles);
+            }
+            const int a = lu / f, c = lu - a * f, cnt = min(lu_to - lu, f - c);
+            if (lane == 0) {
+              queue[2 * (i % kQueue)] = lu;
+              queue[2 * (i % kQueue) + 1] = cnt;
+            }
             lu += cnt;
-            const int e = s_act[a];
-            const size_t wr = (size_t)phys_slot(p.slot, p.n_slots, e) * f + c + min(r & 7, cnt - 1);
-            row = (r < 8 ? p.w1 : p.w3) + wr * rb;
-            if constexpr (WT == kMx) srow = (r < 8 ? p.s1 : p.s3) + wr * (d / 32);
-            if constexpr (ARU > 0)
-#pragma unroll
-              for (int i = 0; i < ARU; ++i)
-                arow[i] = (const uint8_t *)p.x + min(WT == kMx ? g + 4 * i : r, n - 1) * xrow;
+            const size_t wr = (size_t)uniform(s_slot[a]) * f + c;
+            w.row[0] = p.w1 + wr * rb;
+            w.row[1] = p.w3 + wr * rb;
+            w.scale[0] = F::mx ? p.s1 + wr * (d / 32) : nullptr;
+            w.scale[1] = F::mx ? p.s3 + wr * (d / 32) : nullptr;
+            w.cnt[0] = w.cnt[1] = cnt;
+            return true;
           },
-          [&](int, int b, u32x4 (&a)[NF]) {
-            const uint8_t *px = smem + L.x + min(r, n - 1) * L.pitch + b * F::kActBytes;
+          [] {},
+          [&](int, int c, int b, u32x4 (&a)[NF], uint32_t &) {
+            if constexpr (XL) {
+              const uint8_t *px = s_x + (c * n + tok) * RC + b * F::kActBytes;
 #pragma unroll
-            for (int q = 0; q < NF; ++q) a[q] = *(const u32x4 *)(px + q * 16);
+              for (int q = 0; q < NF; ++q) a[q] = *(const u32x4 *)(px + q * 16);
+            } else {
+              load_block<WT>((const uint8_t *)p.x + tok * xrow, c * kChunkBlocks + b, d, a);
+            }
           },
-          [&](int) { return min(r, n - 1); },
-          [&](int, f32x4 v) {
-            int a, c, cnt;
-            tile_at(eu, a, c, cnt);
-            eu += cnt;
+          [&](int i, f32x4 v) {
+            const int at = uniform(queue[2 * (i % kQueue)]), cnt = uniform(queue[2 * (i % kQueue) + 1]);
+            const int a = at / f, c = at - a * f;
             const int mask = s_mask[s_act[a]];
             // lane (r, g): token 4 g + i, column c + r (r < 8: gate, r + 8: value)
 #pragma unroll
@@ -202,79 +250,151 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
               }
             }
           });
-      __syncthreads();  // the block's hidden is on its way out
+      // (all workgroups that run have their first ticket by now: the next one is taken
+      // here, under the other waves' work)
+      int next = 0;
+      if (tid == 0) next = take();
+      // The hidden's stores write through to the memory that all XCDs share (atomic
+      // stores of agent scope); waited for, they are there before the count is.  An
+      // agent-scope release fence would write back the whole L2 besides: with one per
+      // workgroup the last of 256 came 15 us after the first.
+      __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+      lds_barrier();
       if (tid == 0) {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-        __hip_atomic_fetch_add(p.count + 1, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_misc[1] = take();
+        __hip_atomic_fetch_add(p.count + (1 + ticket % kDone) * kCountInts, 1, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+        s_misc[1] = next;
+        s_misc[3] = 0;
       }
-      __syncthreads();
-      ticket = s_misc[1];
+      lds_barrier();
+      ticket = uniform(s_misc[1]);
       continue;
     }
     // ---- output columns [c_lo, c_hi) ------------------------------------------
-    __syncthreads();  // everyone has read s_misc
-    if (tid == 0) {
-      int tries = 0;
-      while (__hip_atomic_load(p.count + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < G && ++tries < kMaxTries)
-        __builtin_amdgcn_s_sleep(1);
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-      s_misc[2] = tries < kMaxTries;
-      s_misc[1] = take();
-    }
-    __syncthreads();
-    const bool whole = s_misc[2];
+    // The chosen experts' (expert, chunk of K) pairs in order, in rounds whose hidden
+    // fits LDS: pair (a, c) has popc(mask) row chunks, pre[a] Cf + m c lie before it.
     const int part = ticket - G;
-    ticket = s_misc[1];
     const int c_lo = (int)((long long)d * part / G), c_hi = (int)((long long)d * (part + 1) / G);
-    const int S = (F::blocks(f) + 3) / 4;
-    const long long steps = (long long)A * S;
-    const int i0 = (int)(steps * wave / kWaves), i1 = (int)(steps * (wave + 1) / kWaves);
-    const size_t rb = F::row_bytes(f);
-    for (int c0 = c_lo; c0 < c_hi; c0 += 16) {
-      const int cnt = min(16, c_hi - c0), a0 = i0 / S;
-      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-      stream<WT, PFD, ARD>(
-          i1 - i0, S, i0 - a0 * S, f, smem + L.x + wave * 1024 * ARD,
-          [&](int i, const uint8_t *&row, const uint8_t *&srow, const uint8_t *(&arow)[ARD], const uint8_t *&) {
-            const int a = a0 + i, e = s_act[a], mask = s_mask[e], m = __popc(mask);
-            const size_t wr = (size_t)phys_slot(p.slot, p.n_slots, e) * d + c0 + min(r, cnt - 1);
-            row = p.w2 + wr * rb;
-            if constexpr (WT == kMx) srow = p.s2 + wr * (f / 32);
-            const int own = min(__popc(mask & ((1 << r) - 1)), m - 1);
+    bool waited = false;
+    if (c_lo < c_hi)
+      for (int c0 = c_lo; c0 < c_hi; c0 += 16) {
+        const int cnt = min(16, c_hi - c0);
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int a_at = 0, c_at = 0; a_at < A;) {  // a round starts at (a_at, c_at)
+          const int w0 = uniform(s_pre[a_at] * Cf + (s_pre[a_at + 1] - s_pre[a_at]) * c_at);
+          // it ends at (a_to, c_to): the experts that fit whole, then chunks of the next
+          int a_to = a_at;
+          for (int a0 = a_at; a0 < A; a0 += 64) {
+            const bool fits = a0 + lane < A && s_pre[a0 + lane + 1] * Cf - w0 <= L.cap;
+            const int more = __popcll(__ballot(fits));
+            a_to += more;
+            if (more < 64) break;
+          }
+          int c_to = 0;
+          if (a_to < A) {
+            const int m = s_pre[a_to + 1] - s_pre[a_to];
+            c_to = uniform((L.cap + w0 - s_pre[a_to] * Cf) / m);
+          }
+          const int i_at = a_at * Cf + c_at, i_to = a_to * Cf + c_to;
+          const int lo = i_at + (int)((long long)(i_to - i_at) * wave / kWaves);
+          const int hi = i_at + (int)((long long)(i_to - i_at) * (wave + 1) / kWaves);
+          const int a_lo = lo / Cf;
+          int seen = -1, at = 0;  // the lane's row in its segment's row chunks
+          stream<WT, PC, NARROW>(
+              hi - lo, Cf, lo - a_lo * Cf, f, xbuf,
+              [&](int i, RowGroups &w) {
+                const size_t wr = (size_t)uniform(s_slot[a_lo + i]) * d + c0;
+                w = row_groups<WT>(p.w2, p.s2, wr, cnt, f);
+                return true;
+              },
+              [&] {  // the first weights are on their way: wait for the hidden, fetch it
+                if (!waited) {
+                  waited = true;
+                  if (wave == 0) {
+                    // lane i: the parts i, i + kDone, .. of G
+                    const int all = lane < kDone ? (G - lane + kDone - 1) / kDone : 0;
+                    int tries = 0, done = 0;
+                    do {
+                      if (lane < kDone)
+                        done = __hip_atomic_load(p.count + (1 + lane) * kCountInts, __ATOMIC_RELAXED,
+                                                 __HIP_MEMORY_SCOPE_AGENT);
+                    } while (__any(done < all) && ++tries < kMaxTries);
+                    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+                    if (lane == 0) s_misc[2] = tries < kMaxTries;
+                  }
+                }
+                lds_barrier();  // also: the round before is done with its hidden
+                for (int i = i_at + wave; i < i_to; i += kStage * kWaves) {
+                  // kStage chunks at a time, a row of each in flight together
+                  int at[kStage], a[kStage], c[kStage], m[kStage], most = 0;
 #pragma unroll
-            for (int j = 0; j < ARD; ++j)
-              arow[j] = (const uint8_t *)p.h + s_pile[a * kT + (WT == kMx ? min(g + 4 * j, m - 1) : own)] * hrow;
-          },
-          [&](int, int, u32x4 (&)[NF]) {},
-          [&](int i) {
-            const int mask = s_mask[s_act[a0 + i]];
-            return min(__popc(mask & ((1 << r) - 1)), __popc(mask) - 1);
-          },
-          [&](int i, f32x4 v) {  // only the expert's own tokens: 0 times a NaN weight is NaN
-            const int mask = s_mask[s_act[a0 + i]];
+                  for (int v = 0; v < kStage; ++v) {
+                    const int iv = min(i + v * kWaves, i_to - 1);
+                    a[v] = iv / Cf;
+                    c[v] = iv - a[v] * Cf;
+                    const int pre = s_pre[a[v]];
+                    m[v] = i + v * kWaves < i_to ? s_pre[a[v] + 1] - pre : 0;
+                    at[v] = pre * Cf + m[v] * c[v] - w0;
+                    most = max(most, m[v]);
+                  }
+                  for (int j0 = 0; j0 < most; j0 += 64 / SL) {
+                    const int j = j0 + lane / SL;
+                    u32x4 q[kStage];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if ((mask >> (4 * g + q)) & 1) sum[q] += v[q];
-          });
-      *(f32x4 *)(s_red + (wave * 64 + lane) * 4) = sum;
-      __syncthreads();
-      if (wave < 4) {  // wave i: token 4 g + i
-        float v = 0.f;
+                    for (int v = 0; v < kStage; ++v)
+                      if (j < m[v])
+                        q[v] = row_chunk_piece<WT>((const uint8_t *)p.h + s_pile[a[v] * kT + j] * hrow, c[v], f, lane % SL);
 #pragma unroll
-        for (int j = 0; j < kWaves; ++j) v += s_red[(j * 64 + lane) * 4 + wave];
-        if (!whole) v = __builtin_nanf("");
-        const int t = 4 * g + wave;
-        if (t < n && r < cnt) {
-          const size_t at = (size_t)t * d + c0 + r;
-          if (p.out_bf16)
-            ((uint16_t *)p.y)[at] = (uint16_t)f32_to_bf16_bits(v);
-          else
-            ((float *)p.y)[at] = v;
+                    for (int v = 0; v < kStage; ++v)
+                      if (j < m[v]) *(u32x4 *)(s_x + (at[v] + j) * RC + lane % SL * 16) = q[v];
+                  }
+                }
+                lds_barrier();
+              },
+              [&](int i, int c, int b, u32x4 (&a)[NF], uint32_t &) {
+                const int m = s_pre[a_lo + i + 1] - s_pre[a_lo + i];
+                if (seen != i) {
+                  seen = i;
+                  const int mask = s_mask[s_act[a_lo + i]];
+                  at = s_pre[a_lo + i] * Cf - w0 + min(__popc(mask & ((1 << r) - 1)), m - 1);
+                }
+                const uint8_t *ph = s_x + (at + m * c) * RC + b * F::kActBytes;
+#pragma unroll
+                for (int q = 0; q < NF; ++q) a[q] = *(const u32x4 *)(ph + q * 16);
+              },
+              [&](int i, f32x4 v) {  // only the expert's own tokens: 0 times a NaN weight is NaN
+                const int mask = s_mask[s_act[a_lo + i]];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  if ((mask >> (4 * g + q)) & 1) sum[q] += v[q];
+              });
+          a_at = a_to;
+          c_at = c_to;
         }
+        if (tid == 0 && c0 + 16 >= c_hi) s_misc[1] = take();
+        *(f32x4 *)(xbuf + lane * 16) = sum;
+        lds_barrier();
+        if (wave < 4) {  // wave i: token 4 g + i
+          float v = 0.f;
+#pragma unroll
+          for (int j = 0; j < kWaves; ++j) v += *(const float *)(smem + L.ex + j * kExchange + lane * 16 + wave * 4);
+          if (!s_misc[2]) v = __builtin_nanf("");
+          const int t = 4 * g + wave;
+          if (t < n && r < cnt) {
+            const size_t at = (size_t)t * d + c0 + r;
+            if (p.out_bf16)
+              ((uint16_t *)p.y)[at] = (uint16_t)f32_to_bf16_bits(v);
+            else
+              ((float *)p.y)[at] = v;
+          }
+        }
+        lds_barrier();
       }
-      __syncthreads();
-    }
+    else if (tid == 0)
+      s_misc[1] = take();
+    lds_barrier();
+    ticket = uniform(s_misc[1]);
+    lds_barrier();  // (read before the next ticket is written)
   }
 }
 
@@ -286,7 +406,7 @@ __global__ __launch_bounds__(256) void few_router_kernel(const void *__restrict_
                                                          float *__restrict__ logits, int *__restrict__ count) {
   __shared__ float s_sum[4][kT];
   const int e = blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  if (e == 0 && tid < 2) count[tid] = 0;
+  if (e == 0 && tid <= kDone) count[tid * kCountInts] = 0;
   float acc[kT] = {};
   if constexpr (BF) {
     const u32x4 *wr = (const u32x4 *)((const uint16_t *)wg + (size_t)e * d);
@@ -336,15 +456,20 @@ FewPlan plan_of(int n, int E, int k, int d_ff, bool f32) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   P.logits = 0;
   P.count = up((size_t)n * E * 4);
-  P.h = P.count + 256;
+  P.h = P.count + up((1 + kDone) * kCountInts * sizeof(int));
   P.total = P.h + up((size_t)n * k * d_ff * (f32 ? 4 : 2));
   return P;
 }
 
-template <int WT, int PER, int ARU, int ARD, int PFU, int PFD>
-hipError_t launch(FewParams &p, hipStream_t st) {
-  auto kern = few_layer_kernel<WT, PER, ARU, ARD, PFU, PFD>;
-  FewLds &L = p.lds;
+template <int WT>
+int chunks_of(int K) {
+  return (Form<WT>::blocks(K) + kChunkBlocks - 1) / kChunkBlocks;
+}
+
+// LDS of a launch: the tables, and in what is left the activations.
+template <int WT>
+FewLds lds_of(const FewParams &p) {
+  FewLds L{};
   const int R = p.n * p.k, A = std::min(R, p.E);
   int o = 0;
   auto put = [&](int bytes) {
@@ -352,19 +477,29 @@ hipError_t launch(FewParams &p, hipStream_t st) {
     o += up16(bytes);
     return at;
   };
-  // an odd number of 16-byte pieces a row: the 16 rows' reads meet different banks
-  L.pitch = WT >= kF4 ? 0 : ((p.d / 8) | 1) * 16;
-  const int stage = WT == kMx ? kWaves * 1024 * std::max(ARU, ARD) : 0;
-  L.x = put(std::max(ARU == 0 ? p.n * L.pitch : 0, stage));
-  L.red = put(kWaves * 64 * 16);
+  L.ex = put(kWaves * kExchange);
   L.idx = put(R * 4);
   L.w = put(R * 4);
   L.mask = put(p.E * 4);
   L.aidx = put(p.E * 2);
   L.act = put(A * 4);
+  L.slot = put(A * 4);
+  L.pre = put((A + 1) * 4);
   L.pile = put(A * kT * 2);
+  L.queue = put(kWaves * 2 * kQueue * 4);
   L.misc = put(16);
-  L.total = o;
+  // the rest: the tokens' rows, later a round's hidden (16 row chunks at least)
+  L.x = o;
+  L.cap = (kFewLds - o) / kRowChunk<WT>;
+  L.total = o + (int)std::min<long long>(L.cap, (long long)p.n * std::max<long long>(chunks_of<WT>(p.d), (long long)p.k * chunks_of<WT>(p.f))) * kRowChunk<WT>;
+  return L;
+}
+
+template <int WT, int PER, bool XL, bool NARROW, int PC>
+hipError_t launch(FewParams &p, hipStream_t st) {
+  auto kern = few_layer_kernel<WT, PER, XL, NARROW, PC>;
+  p.lds = lds_of<WT>(p);
+  const FewLds &L = p.lds;
   if (L.total > kFewLds) return hipErrorInvalidValue;
   if (L.total > 64 * 1024) {
     // The LDS limit is raised once per device (a per-device kernel attribute).
@@ -422,19 +557,27 @@ hipError_t launch_forward_few(const FewArgs &a, hipStream_t st) {
     few_router_kernel<true><<<a.E, 256, 0, st>>>(a.x, a.wg, a.bias, a.n, a.d, a.E, logits, p.count);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const bool few_experts = topk_per(a.E) == 2, in_lds = a.n * (size_t)(a.d / 8 + 1) * 16 <= kMaxXBytes;
+  const bool few = topk_per(a.E) == 2;
+  auto rows_fit = [&](auto form) {
+    constexpr int WT = decltype(form)::value;
+    return (long long)p.n * chunks_of<WT>(p.d) <= lds_of<WT>(p).cap;
+  };
   if (a.w_dtype == 2) {
-    if (!in_lds) return launch<kMx, 16, 4, 4, 6, 6>(p, st);
-    if (a.n <= 4) return few_experts ? launch<kMx, 2, 0, 1, 12, 12>(p, st) : launch<kMx, 16, 0, 1, 12, 12>(p, st);
-    if (a.n <= 8) return few_experts ? launch<kMx, 2, 0, 2, 12, 8>(p, st) : launch<kMx, 16, 0, 2, 12, 8>(p, st);
-    return few_experts ? launch<kMx, 2, 0, 4, 12, 6>(p, st) : launch<kMx, 16, 0, 4, 12, 6>(p, st);
+    const bool fit = rows_fit(std::integral_constant<int, kMx>{});
+    if (std::min(a.d, a.d_ff) < 128)
+      return fit ? launch<kMx, 16, true, true, kInFlight>(p, st) : launch<kMx, 16, false, true, kInFlight>(p, st);
+    if (!fit) return launch<kMx, 16, false, false, kInFlight>(p, st);
+    return few ? launch<kMx, 2, true, false, kInFlight>(p, st) : launch<kMx, 16, true, false, kInFlight>(p, st);
   }
   if (a.w_dtype == 1) {
-    if (!in_lds) return launch<kBf, 16, 1, 1, 12, 12>(p, st);
-    return few_experts ? launch<kBf, 2, 0, 1, 16, 12>(p, st) : launch<kBf, 16, 0, 1, 16, 12>(p, st);
+    if (!rows_fit(std::integral_constant<int, kBf>{})) return launch<kBf, 16, false, false, kInFlight>(p, st);
+    return few ? launch<kBf, 2, true, false, kInFlight>(p, st) : launch<kBf, 16, true, false, kInFlight>(p, st);
   }
-  if (a.d % 4 || a.d_ff % 4) return launch<kF4Tail, 16, 1, 1, 4, 4>(p, st);
-  return launch<kF4, 16, 1, 1, 12, 12>(p, st);
+  if (a.d % 4 || a.d_ff % 4)
+    return rows_fit(std::integral_constant<int, kF4Tail>{}) ? launch<kF4Tail, 16, true, false, 1>(p, st)
+                                                            : launch<kF4Tail, 16, false, false, 1>(p, st);
+  return rows_fit(std::integral_constant<int, kF4>{}) ? launch<kF4, 16, true, false, kInFlight>(p, st)
+                                                      : launch<kF4, 16, false, false, kInFlight>(p, st);
 }
 
 }  // namespace moe

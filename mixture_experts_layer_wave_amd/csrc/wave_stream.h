@@ -23,33 +23,9 @@ struct Form {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
-
-// 16 bytes of block b of a weight row of K elements.
-template <int WT>
-__device__ __forceinline__ u32x4 load_weights(const uint8_t *row, int b, int K) {
-  if constexpr (WT == kF4Tail) {
-    const float *p = (const float *)row;
-    f32x4 v;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = p[min(b * 4 + j, K - 1)];
-    return __builtin_bit_cast(u32x4, v);
-  } else if constexpr (WT == kF4) {
-    return __builtin_bit_cast(u32x4, __builtin_nontemporal_load((const f32x4_any *)(row + (size_t)b * 16)));
-  } else {
-    return __builtin_nontemporal_load((const u32x4 *)(row + (size_t)b * 16));
-  }
-}
-
-template <int WT>
-__device__ __forceinline__ u32x4 load_act(const uint8_t *row, int b, int K) {
-  if constexpr (WT == kF4Tail) {
-    return load_weights<WT>(row, b, K);
-  } else if constexpr (WT == kF4) {
-    return __builtin_bit_cast(u32x4, *(const f32x4_any *)(row + (size_t)b * 16));
-  } else {
-    return *(const u32x4 *)(row + (size_t)b * 16);
-  }
-}
+struct __attribute__((packed, aligned(1))) u32_any {
+  uint32_t v;
+};
 
 // acc += (the tokens' block) x (the weights' block); a: NF 16-byte pieces.
 template <int WT>
@@ -82,115 +58,246 @@ __device__ __forceinline__ void multiply(const u32x4 *a, uint32_t ascale, u32x4 
   }
 }
 
-// One wave's pass over `total` steps: segments (rows of weights with the tokens'
-// rows that meet them) of S steps each, the first one entered at step s0.  Lane
-// (r, g) = (lane % 16, lane / 16) holds weight row r and block 4 s + g.
-//   seg(i, row, srow, arow[], asrow)  the lane's weight row, its scales and, where
-//                 the activations come through the ring, its rows to fetch (and
-//                 with kMx4 their scales)
-//   acts(i, s, a) the lane's pieces of token r, block 4 s + g, from LDS
-//                 (ARING = 0), or nothing
-//   rank(i)       with ARING and kMx: which fetched row is token r's
-//   end(i, acc)   a segment's last step is done
-// With ARING the rows come through the ring, at its depth (in-order loads: a
-// shallower one for them would hold up the weights).  kMx4, bf16 and float32: lane
-// (r, g) fetches its own piece.  kMx: a step is 16 pieces of each row; lane l
-// fetches piece l % 16 of rows l / 16 + 4 i, i < ARING, and the pieces change
-// lanes through abuf, the wave's own LDS.
-template <int WT, int PF, int ARING, class Seg, class Acts, class Rank, class End>
-__device__ __forceinline__ void stream(int total, int S, int s0, int K, uint8_t *abuf, Seg seg, Acts acts,
-                                       Rank rank, End end) {
+// One wave's pass over at most `total` chunks: segments (two groups of 1 to 8 consecutive
+// rows of weights, with the tokens' rows that meet them) of C chunks each, the first one
+// entered at chunk c0.  A chunk is kSteps steps, a step four blocks of each row; in the
+// products lane (r, g) = (lane % 16, lane / 16) holds row r % 8 of group r / 8 and the
+// step's block g.
+//   seg(i, rows)  segment i's groups: first row, its scales, number of rows; false
+//                 where there is none (asked for in order, ahead of the products)
+//   ready()       called once by every wave behind its first loads, also by a wave
+//                 without chunks
+//   acts(i, c, b, a, as)  the lane's NF pieces (and with kMx4 the scale) of its token
+//                 r, block b of chunk c of segment i; zeros past K
+//   end(i, acc)   the wave's last chunk of segment i is done
+// A load takes 256 consecutive bytes of four rows (16 lanes a row) and the pieces
+// change lanes through xbuf, the wave's own kExchange bytes of LDS: loads of 64 bytes
+// of 16 rows, straight into the lanes that multiply, streamed 128 MXFP4 experts' up
+// projections at 3.9 TB/s.  PC chunks of weights are in flight, in registers.  Every
+// load of the loop is unconditional (the last chunk again when none is left): a load
+// behind a branch makes the compiler wait for all of them at the join.
+constexpr int kSteps = 4, kChunkBlocks = 4 * kSteps;
+constexpr int kExchange = 16 * 256 + 256;  // a chunk's codes and scales
+
+struct RowGroups {
+  const uint8_t *row[2], *scale[2];
+  int cnt[2];
+};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// 1 to 16 rows of one matrix as two groups (the second one's first row again where
+// there are no more than 8).
+template <int WT>
+__device__ __forceinline__ RowGroups row_groups(const uint8_t *w, const uint8_t *s, size_t row, int cnt, int K) {
+  using F = Form<WT>;
+  const size_t rb = F::row_bytes(K), next = cnt > 8 ? 8 : 0;
+  RowGroups g;
+  g.row[0] = w + row * rb;
+  g.row[1] = w + (row + next) * rb;
+  g.scale[0] = F::mx ? s + row * (K / 32) : nullptr;
+  g.scale[1] = F::mx ? s + (row + next) * (K / 32) : nullptr;
+  g.cnt[0] = min(cnt, 8);
+  g.cnt[1] = max(cnt - 8, 1);
+  return g;
+}
+
+template <int WT, int PC, bool NARROW, class Seg, class Ready, class Acts, class End>
+__device__ __forceinline__ void stream(int total, int C, int c0, int K, uint8_t *xbuf, Seg seg, Ready ready,
+                                       Acts acts, End end) {
   using F = Form<WT>;
   constexpr int NF = F::kActBytes / 16;
-  constexpr int NA = ARING ? ARING : 1;
-  if (total <= 0) return;
+  constexpr bool kTail = WT == kF4Tail;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int KB = F::blocks(K);
-  u32x4 w[PF], ar[ARING ? PF : 1][NA];
-  uint32_t sc[PF], asc[PF];
-  const uint8_t *row, *srow, *arow[NA], *asrow = nullptr;
-  int ld_seg = 0, ld_s = s0, left = total;
-  seg(0, row, srow, arow, asrow);
-  auto load = [&](int j) {  // the next step (the last one again when none is left)
-    const int b = min(4 * ld_s + g, KB - 1);
-    w[j] = load_weights<WT>(row, b, K);
-    if constexpr (F::mx) sc[j] = srow[b];
-    if constexpr (WT == kMx4) asc[j] = asrow[b];
-    if constexpr (ARING > 0) {
-      if constexpr (WT == kMx) {
-        const int ab = min(4 * ld_s + (r >> 2), KB - 1);
+  const int KB = F::blocks(K), last = KB - 1 - kChunkBlocks * (C - 1);  // the last chunk's last block
+  const int rb = (int)F::row_bytes(K);
+  // Scales: lane l fetches four of row l / 4.  Where a row ends inside them they are
+  // the row's last four, moved down; NARROW (some row has under four): one by one.
+  const int sback = max(0, 4 * (lane & 3) + 3 - last);  // in the last chunk
+  u32x4 w[PC][kSteps];
+  uint32_t sc[PC];
+  RowGroups rows;
+  if (total <= 0 || !seg(0, rows)) {
+    ready();
+    return;
+  }
+  uint32_t off[kSteps];  // of the lane's pieces, from its group's first row
+  const uint8_t *sp = nullptr;
+  int ld_seg = 0, ld_c = c0, issued = 1;  // the chunk to load next, and its number
+  auto open = [&](int c) {
 #pragma unroll
-        for (int i = 0; i < NA; ++i) ar[j][i] = load_act<WT>(arow[i], ab * 4 + (r & 3), K);
+    for (int u = 0; u < kSteps; ++u)
+      off[u] = (uint32_t)(min(4 * (u & 1) + g, rows.cnt[u >> 1] - 1) * rb);
+    if constexpr (F::mx) {
+      const int h = lane >> 5;
+      sp = (h ? rows.scale[1] : rows.scale[0]) +
+           (min((lane >> 2) & 7, (h ? rows.cnt[1] : rows.cnt[0]) - 1) * KB + c * kChunkBlocks);
+    }
+    if constexpr (!kTail)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) rows.row[i] += (size_t)c * kChunkBlocks * 16;
+  };
+  auto load = [&](int j) {
+    const bool end_of_row = ld_c == C - 1;
+    const uint32_t piece = min(r, end_of_row ? last : kChunkBlocks - 1) * 16;
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const uint8_t *p = rows.row[u >> 1];
+      if constexpr (kTail) {
+        const uint32_t *v = (const uint32_t *)(p + off[u]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[j][u][i] = v[min((ld_c * kChunkBlocks + r) * 4 + i, K - 1)];
+      } else if constexpr (WT == kF4) {
+        w[j][u] = __builtin_bit_cast(u32x4, __builtin_nontemporal_load((const f32x4_any *)(p + (off[u] + piece))));
       } else {
-        ar[j][0] = load_act<WT>(arow[0], b, K);
+        w[j][u] = __builtin_nontemporal_load((const u32x4 *)(p + (off[u] + piece)));
       }
     }
-    if (left > 1) {
-      --left;
-      if (++ld_s == S) {
-        ld_s = 0;
-        seg(++ld_seg, row, srow, arow, asrow);
+    if constexpr (F::mx) {
+      const int at = 4 * (lane & 3);
+      if constexpr (NARROW) {
+        const int most = end_of_row ? last : kChunkBlocks - 1;
+        sc[j] = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[j] |= (uint32_t)sp[min(at + i, most)] << (8 * i);
+      } else {
+        sc[j] = ((const u32_any *)(sp + (at - (end_of_row ? sback : 0))))->v;
+      }
+    }
+    if (issued < total) {
+      if (ld_c + 1 < C) {
+        ++ld_c;
+        ++issued;
+        if constexpr (!kTail)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) rows.row[i] += kChunkBlocks * 16;
+        if constexpr (F::mx) sp += kChunkBlocks;
+      } else {
+        RowGroups next;
+        if (seg(ld_seg + 1, next)) {
+          rows = next;
+          ++ld_seg;
+          ++issued;
+          ld_c = 0;
+          open(0);
+        } else {
+          total = issued;
+        }
       }
     }
   };
   f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-  int cur = 0, s = s0;
-  auto use = [&](int j, bool last) {
-    u32x4 a[NF], wj = w[j];
-    uint32_t scale = F::mx ? sc[j] : 0u, ascale = WT == kMx4 ? asc[j] : 0u;
-    if constexpr (ARING == 0) {
-      acts(cur, min(4 * s + g, KB - 1), a);
-    } else if constexpr (WT == kMx) {
-      __builtin_amdgcn_wave_barrier();
+  int cur = 0, c = c0;
+  auto use = [&](int j, bool finish) {
+    // piece q of row i lies in slot q ^ i of the row's 16
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int i = 0; i < NA; ++i) {
-        const int ai = g + 4 * i;
-        *(u32x4 *)(abuf + (ai * 16 + (r ^ ai)) * 16) = ar[j][i];
-      }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-      const int at = rank(cur);
-#pragma unroll
-      for (int q = 0; q < NF; ++q) a[q] = *(const u32x4 *)(abuf + (at * 16 + ((g * 4 + q) ^ at)) * 16);
-    } else {
-      a[0] = ar[j][0];
+    for (int u = 0; u < kSteps; ++u) {
+      const int row = 4 * u + g;
+      *(u32x4 *)(xbuf + (row * 16 + (r ^ row)) * 16) = w[j][u];
     }
-    if (s == S - 1 && (KB % 4 || WT == kF4Tail)) {  // blocks past the row's end
-      const u32x4 z = {0u, 0u, 0u, 0u};
-      const int b = 4 * s + g;
-      if constexpr (WT == kF4Tail) {
+    if constexpr (F::mx) *(uint32_t *)(xbuf + 4096 + lane * 4) = (!NARROW && c == C - 1) ? sc[j] >> (8 * min(sback, 3)) : sc[j];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    u32x4 wj[kSteps], sj = {0u, 0u, 0u, 0u};
+    if constexpr (F::mx) sj = *(const u32x4 *)(xbuf + 4096 + r * 16);
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) wj[u] = *(const u32x4 *)(xbuf + (r * 16 + ((4 * u + g) ^ r)) * 16);
+    uint32_t scale[kSteps];
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) scale[u] = (sj[u] >> (8 * g)) & 255u;
+    if (c == C - 1) {  // what lies past the row's end
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        if (4 * u + g > last) scale[u] = 127u;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (b * 4 + i >= K) wj[i] = 0u, a[0][i] = 0u;
-      } else if (b >= KB) {
-        wj = z;
-        scale = ascale = 127u;
-#pragma unroll
-        for (int q = 0; q < NF; ++q) a[q] = z;
+          if (kTail ? (c * kChunkBlocks + 4 * u + g) * 4 + i >= K : 4 * u + g > last) wj[u][i] = 0u;
       }
     }
-    multiply<WT>(a, ascale, wj, scale, acc);
-    if (++s == S || last) {
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      u32x4 a[NF];
+      uint32_t as = 127u;
+      acts(cur, c, 4 * u + g, a, as);
+      multiply<WT>(a, as, wj[u], scale[u], acc);
+    }
+    if (++c == C || finish) {
       end(cur, acc[0] + acc[1]);
       acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      s = 0;
+      c = 0;
       ++cur;
     }
   };
-  const int groups = (total + PF - 1) / PF;
+  open(c0);
 #pragma unroll
-  for (int j = 0; j < PF; ++j) load(j);
-  for (int gi = 0; gi + 1 < groups; ++gi)
+  for (int j = 0; j < PC; ++j) load(j);
+  ready();
+  int used = 0;
+  while (used + PC < issued) {  // at least one more load after these
 #pragma unroll
-    for (int j = 0; j < PF; ++j) {
+    for (int j = 0; j < PC; ++j) {
       use(j, false);
       load(j);
     }
-  const int rest = total - (groups - 1) * PF;
+    used += PC;
+  }
+  const int rest = issued - used;
 #pragma unroll
-  for (int j = 0; j < PF; ++j)
+  for (int j = 0; j < PC; ++j)
     if (j < rest) use(j, j == rest - 1);
+}
+
+// Rows of activations in LDS, cut into row chunks: the kChunkBlocks blocks that one
+// chunk meets, and 16 bytes more, which puts 16 rows' reads into different banks.
+template <int WT>
+constexpr int kRowChunk = kChunkBlocks * Form<WT>::kActBytes + 16;
+
+// Lane l's 16 bytes of row chunk c of a row of K elements, 0 past K (16 or 64 lanes a
+// row chunk).
+template <int WT>
+__device__ __forceinline__ u32x4 row_chunk_piece(const uint8_t *row, int c, int K, int l) {
+  using F = Form<WT>;
+  constexpr int P = F::kActBytes / 16;  // pieces of a block
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if constexpr (WT == kF4Tail) {
+    const int at = c * kChunkBlocks * 4 + l * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (at + i < K) v[i] = ((const uint32_t *)row)[at + i];
+  } else {
+    const int b = c * kChunkBlocks + l / P;
+    if (b < F::blocks(K)) {
+      const uint8_t *p = row + (size_t)b * F::kActBytes + (l % P) * 16;
+      v = F::f32 ? __builtin_bit_cast(u32x4, *(const f32x4_any *)p) : *(const u32x4 *)p;
+    }
+  }
+  return v;
+}
+
+template <int WT>
+__device__ __forceinline__ void stage_row_chunk(uint8_t *dst, const uint8_t *row, int c, int K, int l) {
+  *(u32x4 *)(dst + l * 16) = row_chunk_piece<WT>(row, c, K, l);
+}
+
+// The lane's pieces of block b of a row of K elements, from global memory, 0 past K.
+template <int WT>
+__device__ __forceinline__ void load_block(const uint8_t *row, int b, int K, u32x4 (&a)[Form<WT>::kActBytes / 16]) {
+  using F = Form<WT>;
+  if constexpr (WT == kF4Tail) {
+    const uint32_t *v = (const uint32_t *)row;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[0][i] = b * 4 + i < K ? v[b * 4 + i] : 0u;
+  } else {
+    const bool in = b < F::blocks(K);
+    const uint8_t *p = row + (in ? (size_t)b * F::kActBytes : 0);
+#pragma unroll
+    for (int q = 0; q < F::kActBytes / 16; ++q) {
+      const u32x4 v = F::f32 ? __builtin_bit_cast(u32x4, *(const f32x4_any *)(p + q * 16)) : *(const u32x4 *)(p + q * 16);
+      a[q] = in ? v : u32x4{0u, 0u, 0u, 0u};
+    }
+  }
 }
 
 }  // namespace moe
