@@ -43,12 +43,8 @@ namespace moe {
 namespace {
 
 constexpr int kT = kFewMaxTokens;  // 16: the M of the MFMA
-#ifndef PW
-#define PW 8
-#define PI 4
-#endif
-constexpr int kWaves = PW, kThreads = kWaves * 64;
-constexpr int kInFlight = PI;  // chunks of weights
+constexpr int kWaves = 8, kThreads = kWaves * 64;
+constexpr int kInFlight = 4;  // chunks of weights in flight a wave
 constexpr int kFewLds = 160 * 1024;
 // Tries of a waiting output part (each at least a microsecond): seconds, where a
 // call takes microseconds.  Past it the part writes NaN.
@@ -56,7 +52,6 @@ constexpr int kMaxTries = 1 << 23;
 // Parts done are counted in kDone counters (part i in counter i mod kDone), each on a
 // line of its own: 256 additions to one address, with the waiting workgroups reading
 // it, took 4 us.
-constexpr int kAhead = 6;  // pieces of the tokens' rows a thread fetches before the top-k
 constexpr int kQueue = 8;  // segments a wave has loaded ahead of those it finished, at most kInFlight + 1
 static_assert(kInFlight < kQueue, "segments ahead");
 constexpr int kDone = 8, kCountInts = 64;
@@ -65,7 +60,7 @@ struct FewLds {
   int x;      // the tokens' row chunks, later a round's hidden
   int cap;    // row chunks that fit there
   int ex;     // the waves' exchange buffers
-  int idx, w, mask, aidx, act, slot, pre, pile, queue, misc, total;
+  int idx, w, mask, aidx, act, slot, pre, pile, row, queue, misc, total;
 };
 
 struct FewParams {
@@ -91,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
   using F = Form<WT>;
   constexpr int NF = F::kActBytes / 16, RC = kRowChunk<WT>;
   constexpr int SL = (RC - 16) / 16;  // lanes of a row chunk
-  constexpr int kStage = WT == kMx ? 4 : 8;  // chunks whose hidden a wave fetches at a time
+  constexpr int kStage = 4;  // loads of the hidden a wave has in flight
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const FewLds &L = p.lds;
   int *s_idx = (int *)(smem + L.idx), *s_mask = (int *)(smem + L.mask), *s_act = (int *)(smem + L.act);
@@ -99,7 +94,7 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
   float *s_w = (float *)(smem + L.w);
   uint16_t *s_aidx = (uint16_t *)(smem + L.aidx), *s_pile = (uint16_t *)(smem + L.pile);
   int *s_misc = (int *)(smem + L.misc);  // active experts, ticket, whether the wait ended, tiles taken
-  int *s_queue = (int *)(smem + L.queue);
+  int *s_queue = (int *)(smem + L.queue), *s_row = (int *)(smem + L.row);
   uint8_t *s_x = smem + L.x, *xbuf = smem + L.ex + (threadIdx.x >> 6) * kExchange;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -112,34 +107,30 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
   };
   int first = 0;
   if (tid == 0) first = take();
-  // the tokens' rows: the first pieces are on their way during the top-k
-  u32x4 xq[kAhead];
-  auto x_piece = [&](int v) {
-    const int i = (v * kThreads + tid) / SL, c = i / n, t = i - c * n;
-    return row_chunk_piece<WT>((const uint8_t *)p.x + t * xrow, c, d, tid % SL);
-  };
-  const int pieces = XL ? (n * Cd * SL + kThreads - 1) / kThreads : 0;
-  auto x_live = [&](int v) { return (v * kThreads + tid) / SL < n * Cd; };
-  if constexpr (XL)
-#pragma unroll
-    for (int v = 0; v < kAhead; ++v)
-      if (v < pieces && x_live(v)) xq[v] = x_piece(v);
   for (int e = tid; e < E; e += kThreads) s_mask[e] = 0;
-  const int TG = topk_group(E);
-  for (int t0 = 0; t0 < n; t0 += kThreads / TG)
-    topk_token_t<PER>(p.logits, 1, 0, t0 + tid / TG, n, E, k, p.renorm, s_idx, s_w, nullptr, nullptr);
-  if constexpr (XL) {
-    auto put = [&](int v, u32x4 q) {
-      *(u32x4 *)(s_x + (v * kThreads + tid) / SL * RC + tid % SL * 16) = q;
-    };
+  // The top-k, and the tokens' rows into LDS: by the waves without a token where there
+  // are enough of them, else by all behind their tokens.
+  const int TG = topk_group(E), busy = (n * TG + 63) / 64, from = XL && busy <= kWaves / 2 ? busy : 0;
+  if (from == 0 || wave < from)
+    for (int t0 = 0; t0 < n; t0 += kThreads / TG)
+      topk_token_t<PER>(p.logits, 1, 0, t0 + tid / TG, n, E, k, p.renorm, s_idx, s_w, nullptr, nullptr);
+  if (XL && (from == 0 || wave >= from)) {
+    const int pieces = Cd * SL;  // of a row
+    for (int i = tid - from * 64; i < pieces; i += kThreads - from * 64)
+      for (int t0 = 0; t0 < n; t0 += 4) {
+        u32x4 q[4];
 #pragma unroll
-    for (int v = 0; v < kAhead; ++v)
-      if (v < pieces && x_live(v)) put(v, xq[v]);
-    for (int v = kAhead; v < pieces; ++v)
-      if (x_live(v)) put(v, x_piece(v));
+        for (int v = 0; v < 4; ++v)
+          q[v] = row_chunk_piece<WT>((const uint8_t *)p.x + min(t0 + v, n - 1) * xrow, i / SL, d, i % SL);
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (t0 + v < n) *(u32x4 *)(s_x + (i / SL * n + t0 + v) * RC + i % SL * 16) = q[v];
+      }
   }
-  if (tid == 0) s_misc[3] = 0;
-  if (tid == 0) s_misc[1] = first;
+  if (tid == 0) {
+    s_misc[1] = first;
+    s_misc[3] = 0;
+  }
   __syncthreads();
   // ---- who takes which expert ------------------------------------------------
   for (int q = tid; q < R; q += kThreads) atomicOr(&s_mask[s_idx[q]], 1 << (q / k));
@@ -167,8 +158,9 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
   }
   __syncthreads();
   for (int q = tid; q < R; q += kThreads) {
-    const int e = s_idx[q], t = q / k;
-    s_pile[s_aidx[e] * kT + __popc(s_mask[e] & ((1 << t) - 1))] = (uint16_t)q;
+    const int e = s_idx[q], t = q / k, a = s_aidx[e], j = __popc(s_mask[e] & ((1 << t) - 1));
+    s_pile[a * kT + j] = (uint16_t)q;
+    s_row[s_pre[a] + j] = a << 16 | q;  // pile rows in order: expert and pair
   }
   __syncthreads();
   const int A = uniform(s_misc[0]);
@@ -179,9 +171,10 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
   if (ticket == 0 && p.w)
     for (int q = tid; q < R; q += kThreads) p.w[q] = s_w[q];
 
+  int *queue = s_queue + wave * (4 * kQueue);  // the segments loaded ahead
   // (a block's tickets ascend, so no up part follows an output part, whose
   // staging overwrites the tokens' rows)
-  while (ticket < 2 * G) {
+  for (int turn = 0; ticket < 2 * G && turn < 2 * G; ++turn) {
     if (ticket < G) {
       // ---- up: hidden columns [u0, u1) of the chosen experts' A f -----------
       const long long U = (long long)A * f;
@@ -191,12 +184,11 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
       // segment for each expert it meets.
       const int tiles = max((cols + 7) / 8, min(cols, kWaves));
       int lu = 0, lu_to = 0;  // what is left of the tile to load
-      int *queue = s_queue + wave * (2 * kQueue);  // the segments' first columns and widths
       const size_t rb = F::row_bytes(d);
       const int tok = min(r, n - 1);  // (rows past the last token: any)
       stream<WT, PC, NARROW>(
-          0x7fffffff, Cd, 0, d, xbuf,
-          [&](int i, RowGroups &w) {
+          Cd, d, xbuf,
+          [&](int i, Segment &w) {
             if (lu == lu_to) {
               int t = 0;
               if (lane == 0) t = atomicAdd(&s_misc[3], 1);
@@ -206,10 +198,9 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
               lu_to = u0 + (int)((long long)cols * (t + 1) / tiles);
             }
             const int a = lu / f, c = lu - a * f, cnt = min(lu_to - lu, f - c);
-            if (lane == 0) {
-              queue[2 * (i % kQueue)] = lu;
-              queue[2 * (i % kQueue) + 1] = cnt;
-            }
+            if (lane == 0) *(i32x4 *)(queue + 4 * (i % kQueue)) = i32x4{a, c, cnt, 0};
+            w.first = 0;
+            w.count = Cd;
             lu += cnt;
             const size_t wr = (size_t)uniform(s_slot[a]) * f + c;
             w.row[0] = p.w1 + wr * rb;
@@ -220,6 +211,10 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
             return true;
           },
           [] {},
+          [&](int, int &c, int &left) {
+            c = 0;
+            left = Cd;
+          },
           [&](int, int c, int b, u32x4 (&a)[NF], uint32_t &) {
             if constexpr (XL) {
               const uint8_t *px = s_x + (c * n + tok) * RC + b * F::kActBytes;
@@ -230,8 +225,8 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
             }
           },
           [&](int i, f32x4 v) {
-            const int at = uniform(queue[2 * (i % kQueue)]), cnt = uniform(queue[2 * (i % kQueue) + 1]);
-            const int a = at / f, c = at - a * f;
+            const i32x4 at = *(const i32x4 *)(queue + 4 * (i % kQueue));
+            const int a = at[0], c = at[1], cnt = at[2];
             const int mask = s_mask[s_act[a]];
             // lane (r, g): token 4 g + i, column c + r (r < 8: gate, r + 8: value)
 #pragma unroll
@@ -272,105 +267,129 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
     }
     // ---- output columns [c_lo, c_hi) ------------------------------------------
     // The chosen experts' (expert, chunk of K) pairs in order, in rounds whose hidden
-    // fits LDS: pair (a, c) has popc(mask) row chunks, pre[a] Cf + m c lie before it.
+    // fits LDS; every wave takes an equal run of a round.  Pair (a, c) has m = popc(mask)
+    // row chunks, pre[a] Cf + m c of them before it.
     const int part = ticket - G;
     const int c_lo = (int)((long long)d * part / G), c_hi = (int)((long long)d * (part + 1) / G);
     bool waited = false;
+    struct Round {
+      int a, c, w0;     // its first expert and chunk, row chunks before them
+      int a_to, c_to;   // behind its last
+      int lo, hi;       // this wave's run, in chunks from the first expert's chunk 0 on
+    };
+    auto next_round = [&](Round &q) {  // false behind the last
+      q.a = q.a_to;
+      q.c = q.c_to;
+      if (q.a == A) return false;
+      const int pre = s_pre[q.a];
+      q.w0 = uniform(pre * Cf + (s_pre[q.a + 1] - pre) * q.c);
+      // the experts that fit whole, then chunks of the next
+      for (;;) {
+        const bool fits = q.a_to + lane < A && s_pre[min(q.a_to + lane, A - 1) + 1] * Cf - q.w0 <= L.cap;
+        const int add = __popcll(__ballot(fits));
+        q.a_to += add;
+        if (add < 64) break;
+      }
+      q.c_to = 0;
+      if (q.a_to < A) {
+        const int at = s_pre[q.a_to], m = s_pre[q.a_to + 1] - at;
+        q.c_to = uniform((L.cap + q.w0 - at * Cf) / m);
+      }
+      const int total = (q.a_to - q.a) * Cf + q.c_to - q.c;
+      q.lo = q.c + (int)((long long)total * wave / kWaves);
+      q.hi = q.c + (int)((long long)total * (wave + 1) / kWaves);
+      return true;
+    };
     if (c_lo < c_hi)
       for (int c0 = c_lo; c0 < c_hi; c0 += 16) {
         const int cnt = min(16, c_hi - c0);
         f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int a_at = 0, c_at = 0; a_at < A;) {  // a round starts at (a_at, c_at)
-          const int w0 = uniform(s_pre[a_at] * Cf + (s_pre[a_at + 1] - s_pre[a_at]) * c_at);
-          // it ends at (a_to, c_to): the experts that fit whole, then chunks of the next
-          int a_to = a_at;
-          for (int a0 = a_at; a0 < A; a0 += 64) {
-            const bool fits = a0 + lane < A && s_pre[a0 + lane + 1] * Cf - w0 <= L.cap;
-            const int more = __popcll(__ballot(fits));
-            a_to += more;
-            if (more < 64) break;
+        Round lr{0, 0, 0, 0, 0, 0, 0}, ur = lr;  // the round that is loaded, the one in LDS
+        int l_at = 0, l_a = 0, l_round = -1, u_round = -1;
+        // The next round's hidden into LDS (all waves together).
+        auto enter = [&] {
+          next_round(ur);
+          ++u_round;
+          if (!waited) {
+            waited = true;
+            if (wave == 0) {
+              // lane i: the parts i, i + kDone, .. of G
+              const int all = lane < kDone ? (G - lane + kDone - 1) / kDone : 0;
+              int tries = 0, done = 0;
+              do {
+                if (lane < kDone)
+                  done = __hip_atomic_load(p.count + (1 + lane) * kCountInts, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+              } while (__any(done < all) && ++tries < kMaxTries);
+              __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+              if (lane == 0) s_misc[2] = tries < kMaxTries;
+            }
           }
-          int c_to = 0;
-          if (a_to < A) {
-            const int m = s_pre[a_to + 1] - s_pre[a_to];
-            c_to = uniform((L.cap + w0 - s_pre[a_to] * Cf) / m);
+          lds_barrier();  // also: the round before is done with its hidden
+          // Half a pile row to a wave at a time, kStage loads in flight; 64 / SL chunks a load.
+          const int r_lo = s_pre[ur.a], r_hi = ur.c_to ? s_pre[ur.a_to + 1] : s_pre[ur.a_to];
+          for (int v = wave; v < 2 * (r_hi - r_lo); v += kWaves) {
+            const int row = uniform(r_lo + (v >> 1)), pair = uniform(s_row[row]), a = pair >> 16, q = pair & 0xffff;
+            const int pre = uniform(s_pre[a]), m = uniform(s_pre[a + 1]) - pre;
+            int ca = a == ur.a ? ur.c : 0, cb = a == ur.a_to ? ur.c_to : Cf;
+            const int mid = (ca + cb) >> 1;
+            (v & 1 ? ca : cb) = mid;
+            const uint8_t *src = (const uint8_t *)p.h + q * hrow;
+            uint8_t *dst = s_x + (pre * Cf + (row - pre) - ur.w0) * RC + lane % SL * 16;
+            for (int c = ca + lane / SL; c < cb; c += kStage * (64 / SL)) {
+              u32x4 w[kStage];
+#pragma unroll
+              for (int i = 0; i < kStage; ++i)
+                if (c + i * (64 / SL) < cb) w[i] = row_chunk_piece<WT>(src, c + i * (64 / SL), f, lane % SL);
+#pragma unroll
+              for (int i = 0; i < kStage; ++i)
+                if (c + i * (64 / SL) < cb) *(u32x4 *)(dst + m * (c + i * (64 / SL)) * RC) = w[i];
+            }
           }
-          const int i_at = a_at * Cf + c_at, i_to = a_to * Cf + c_to;
-          const int lo = i_at + (int)((long long)(i_to - i_at) * wave / kWaves);
-          const int hi = i_at + (int)((long long)(i_to - i_at) * (wave + 1) / kWaves);
-          const int a_lo = lo / Cf;
-          int seen = -1, at = 0;  // the lane's row in its segment's row chunks
-          stream<WT, PC, NARROW>(
-              hi - lo, Cf, lo - a_lo * Cf, f, xbuf,
-              [&](int i, RowGroups &w) {
-                const size_t wr = (size_t)uniform(s_slot[a_lo + i]) * d + c0;
-                w = row_groups<WT>(p.w2, p.s2, wr, cnt, f);
-                return true;
-              },
-              [&] {  // the first weights are on their way: wait for the hidden, fetch it
-                if (!waited) {
-                  waited = true;
-                  if (wave == 0) {
-                    // lane i: the parts i, i + kDone, .. of G
-                    const int all = lane < kDone ? (G - lane + kDone - 1) / kDone : 0;
-                    int tries = 0, done = 0;
-                    do {
-                      if (lane < kDone)
-                        done = __hip_atomic_load(p.count + (1 + lane) * kCountInts, __ATOMIC_RELAXED,
-                                                 __HIP_MEMORY_SCOPE_AGENT);
-                    } while (__any(done < all) && ++tries < kMaxTries);
-                    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-                    if (lane == 0) s_misc[2] = tries < kMaxTries;
-                  }
-                }
-                lds_barrier();  // also: the round before is done with its hidden
-                for (int i = i_at + wave; i < i_to; i += kStage * kWaves) {
-                  // kStage chunks at a time, a row of each in flight together
-                  int at[kStage], a[kStage], c[kStage], m[kStage], most = 0;
+          lds_barrier();
+        };
+        int at = 0, m = 0, e_mask = 0;  // the segment's: the lane's first row chunk, rows, tokens
+        stream<WT, PC, NARROW>(
+            Cf, f, xbuf,
+            [&](int i, Segment &w) {
+              while (l_at == lr.hi) {
+                if (!next_round(lr)) return false;
+                ++l_round;
+                l_a = lr.a + lr.lo / Cf;
+                l_at = lr.lo;
+              }
+              const int c = l_at - (l_a - lr.a) * Cf;
+              w.first = c;
+              w.count = min(lr.hi - l_at, Cf - c);
+              if (lane == 0) *(i32x4 *)(queue + 4 * (i % kQueue)) = i32x4{l_a, c, w.count, l_round};
+              rows_of_one<WT>(w, p.w2, p.s2, (size_t)uniform(s_slot[l_a]) * d + c0, cnt, f);
+              l_at += w.count;
+              if (c + w.count == Cf) ++l_a;
+              return true;
+            },
+            enter,
+            [&](int i, int &c, int &left) {
+              const i32x4 s = *(const i32x4 *)(queue + 4 * (i % kQueue));
+              const int a = uniform(s[0]), round = uniform(s[3]);
+              c = uniform(s[1]);
+              left = uniform(s[2]);
+              while (u_round < round) enter();
+              const int pre = s_pre[a];
+              m = uniform(s_pre[a + 1] - pre);
+              e_mask = s_mask[s_act[a]];
+              at = pre * Cf - ur.w0 + min(__popc(e_mask & ((1 << r) - 1)), m - 1);
+            },
+            [&](int, int c, int b, u32x4 (&a)[NF], uint32_t &) {
+              const uint8_t *ph = s_x + (at + m * c) * RC + b * F::kActBytes;
 #pragma unroll
-                  for (int v = 0; v < kStage; ++v) {
-                    const int iv = min(i + v * kWaves, i_to - 1);
-                    a[v] = iv / Cf;
-                    c[v] = iv - a[v] * Cf;
-                    const int pre = s_pre[a[v]];
-                    m[v] = i + v * kWaves < i_to ? s_pre[a[v] + 1] - pre : 0;
-                    at[v] = pre * Cf + m[v] * c[v] - w0;
-                    most = max(most, m[v]);
-                  }
-                  for (int j0 = 0; j0 < most; j0 += 64 / SL) {
-                    const int j = j0 + lane / SL;
-                    u32x4 q[kStage];
+              for (int q = 0; q < NF; ++q) a[q] = *(const u32x4 *)(ph + q * 16);
+            },
+            [&](int, f32x4 v) {  // only the expert's own tokens: 0 times a NaN weight is NaN
 #pragma unroll
-                    for (int v = 0; v < kStage; ++v)
-                      if (j < m[v])
-                        q[v] = row_chunk_piece<WT>((const uint8_t *)p.h + s_pile[a[v] * kT + j] * hrow, c[v], f, lane % SL);
-#pragma unroll
-                    for (int v = 0; v < kStage; ++v)
-                      if (j < m[v]) *(u32x4 *)(s_x + (at[v] + j) * RC + lane % SL * 16) = q[v];
-                  }
-                }
-                lds_barrier();
-              },
-              [&](int i, int c, int b, u32x4 (&a)[NF], uint32_t &) {
-                const int m = s_pre[a_lo + i + 1] - s_pre[a_lo + i];
-                if (seen != i) {
-                  seen = i;
-                  const int mask = s_mask[s_act[a_lo + i]];
-                  at = s_pre[a_lo + i] * Cf - w0 + min(__popc(mask & ((1 << r) - 1)), m - 1);
-                }
-                const uint8_t *ph = s_x + (at + m * c) * RC + b * F::kActBytes;
-#pragma unroll
-                for (int q = 0; q < NF; ++q) a[q] = *(const u32x4 *)(ph + q * 16);
-              },
-              [&](int i, f32x4 v) {  // only the expert's own tokens: 0 times a NaN weight is NaN
-                const int mask = s_mask[s_act[a_lo + i]];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  if ((mask >> (4 * g + q)) & 1) sum[q] += v[q];
-              });
-          a_at = a_to;
-          c_at = c_to;
-        }
+              for (int q = 0; q < 4; ++q)
+                if ((e_mask >> (4 * g + q)) & 1) sum[q] += v[q];
+            });
+        while (ur.a_to < A) enter();  // (rounds in which this wave has nothing)
         if (tid == 0 && c0 + 16 >= c_hi) s_misc[1] = take();
         *(f32x4 *)(xbuf + lane * 16) = sum;
         lds_barrier();
@@ -398,19 +417,21 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
   }
 }
 
+constexpr int kRouterThreads = 512;
+
 // logits[t][e] = x_t . wg_e + bias_e, one workgroup per expert; the first also
 // clears the next kernel's counters.  Rows of bf16 in 16-byte pieces.
 template <bool BF>
-__global__ __launch_bounds__(256) void few_router_kernel(const void *__restrict__ x, const void *__restrict__ wg,
+__global__ __launch_bounds__(kRouterThreads) void few_router_kernel(const void *__restrict__ x, const void *__restrict__ wg,
                                                          const float *__restrict__ bias, int n, int d, int E,
                                                          float *__restrict__ logits, int *__restrict__ count) {
-  __shared__ float s_sum[4][kT];
+  __shared__ float s_sum[kRouterThreads / 64][kT];
   const int e = blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   if (e == 0 && tid <= kDone) count[tid * kCountInts] = 0;
   float acc[kT] = {};
   if constexpr (BF) {
     const u32x4 *wr = (const u32x4 *)((const uint16_t *)wg + (size_t)e * d);
-    for (int c = tid; c < d / 8; c += 256) {
+    for (int c = tid; c < d / 8; c += kRouterThreads) {
       const u32x4 w = wr[c];
 #pragma unroll
       for (int t = 0; t < kT; ++t)
@@ -425,7 +446,7 @@ __global__ __launch_bounds__(256) void few_router_kernel(const void *__restrict_
     }
   } else {
     const float *wr = (const float *)wg + (size_t)e * d;
-    for (int c = tid; c < d; c += 256) {
+    for (int c = tid; c < d; c += kRouterThreads) {
       const float w = wr[c];
 #pragma unroll
       for (int t = 0; t < kT; ++t)
@@ -440,7 +461,9 @@ __global__ __launch_bounds__(256) void few_router_kernel(const void *__restrict_
     }
   __syncthreads();
   if (tid < n) {
-    const float v = (s_sum[0][tid] + s_sum[1][tid]) + (s_sum[2][tid] + s_sum[3][tid]);
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < kRouterThreads / 64; ++j) v += s_sum[j][tid];
     logits[(size_t)tid * E + e] = bias ? v + bias[e] : v;
   }
 }
@@ -486,7 +509,8 @@ FewLds lds_of(const FewParams &p) {
   L.slot = put(A * 4);
   L.pre = put((A + 1) * 4);
   L.pile = put(A * kT * 2);
-  L.queue = put(kWaves * 2 * kQueue * 4);
+  L.row = put(R * 4);
+  L.queue = put(kWaves * 4 * kQueue * 4);
   L.misc = put(16);
   // the rest: the tokens' rows, later a round's hidden (16 row chunks at least)
   L.x = o;
@@ -552,9 +576,9 @@ hipError_t launch_forward_few(const FewArgs &a, hipStream_t st) {
   p.G = cu_count();
   float *logits = (float *)(base + P.logits);
   if (f32)
-    few_router_kernel<false><<<a.E, 256, 0, st>>>(a.x, a.wg, a.bias, a.n, a.d, a.E, logits, p.count);
+    few_router_kernel<false><<<a.E, kRouterThreads, 0, st>>>(a.x, a.wg, a.bias, a.n, a.d, a.E, logits, p.count);
   else
-    few_router_kernel<true><<<a.E, 256, 0, st>>>(a.x, a.wg, a.bias, a.n, a.d, a.E, logits, p.count);
+    few_router_kernel<true><<<a.E, kRouterThreads, 0, st>>>(a.x, a.wg, a.bias, a.n, a.d, a.E, logits, p.count);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const bool few = topk_per(a.E) == 2;

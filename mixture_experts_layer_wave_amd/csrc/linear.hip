@@ -59,12 +59,15 @@ __global__ __launch_bounds__(kThreads) void linear_rows_kernel(LinearParams p) {
   auto col = [&](int tile) { return c_lo + (int)((long long)cols * tile / max(tiles, 1)); };
   const int tok = min(r, rows - 1);
   f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  // (KS > 1: a wave has one tile at most, so its chunks are k_lo .. k_hi - 1 of one segment)
+  // (KS > 1: a wave has one tile at most, and its part k_lo .. k_hi - 1 of the chunks)
   stream<WT, PC, NARROW>(
-      segs * (k_hi - k_lo), C, k_lo, d, s_ex[wave],
-      [&](int i, RowGroups &w) {
+      C, d, s_ex[wave],
+      [&](int i, Segment &w) {
+        if (i >= segs || k_lo == k_hi) return false;
         const int tile = mine + i * step, c = col(tile);
-        w = row_groups<WT>(p.w, p.ws, c, col(tile + 1) - c, d);
+        rows_of_one<WT>(w, p.w, p.ws, c, col(tile + 1) - c, d);
+        w.first = k_lo;
+        w.count = k_hi - k_lo;
         return true;
       },
       [&] {  // the first weights are on their way
@@ -75,6 +78,10 @@ __global__ __launch_bounds__(kThreads) void linear_rows_kernel(LinearParams p) {
           }
           lds_barrier();
         }
+      },
+      [&](int, int &c, int &left) {
+        c = k_lo;
+        left = k_hi - k_lo;
       },
       [&](int, int c, int b, u32x4 (&a)[NF], uint32_t &as) {
         if constexpr (XL) {

@@ -58,18 +58,18 @@ __device__ __forceinline__ void multiply(const u32x4 *a, uint32_t ascale, u32x4 
   }
 }
 
-// One wave's pass over at most `total` chunks: segments (two groups of 1 to 8 consecutive
-// rows of weights, with the tokens' rows that meet them) of C chunks each, the first one
-// entered at chunk c0.  A chunk is kSteps steps, a step four blocks of each row; in the
-// products lane (r, g) = (lane % 16, lane / 16) holds row r % 8 of group r / 8 and the
-// step's block g.
-//   seg(i, rows)  segment i's groups: first row, its scales, number of rows; false
-//                 where there is none (asked for in order, ahead of the products)
+// One wave's pass over segments: two groups of 1 to 8 consecutive rows of weights, with
+// the tokens' rows that meet them, over `count` chunks of K from chunk `first` on.  A
+// chunk is kSteps steps, a step four blocks of each row; in the products lane (r, g) =
+// (lane % 16, lane / 16) holds row r % 8 of group r / 8 and the step's block g.
+//   seg(i, s)     segment i; false where there is none (asked for in order, up to
+//                 PC segments ahead of the products)
 //   ready()       called once by every wave behind its first loads, also by a wave
-//                 without chunks
+//                 without segments
+//   begin(i, first, count)  the products of segment i begin: its chunks
 //   acts(i, c, b, a, as)  the lane's NF pieces (and with kMx4 the scale) of its token
 //                 r, block b of chunk c of segment i; zeros past K
-//   end(i, acc)   the wave's last chunk of segment i is done
+//   end(i, acc)   they are done
 // A load takes 256 consecutive bytes of four rows (16 lanes a row) and the pieces
 // change lanes through xbuf, the wave's own kExchange bytes of LDS: loads of 64 bytes
 // of 16 rows, straight into the lanes that multiply, streamed 128 MXFP4 experts' up
@@ -79,32 +79,32 @@ __device__ __forceinline__ void multiply(const u32x4 *a, uint32_t ascale, u32x4 
 constexpr int kSteps = 4, kChunkBlocks = 4 * kSteps;
 constexpr int kExchange = 16 * 256 + 256;  // a chunk's codes and scales
 
-struct RowGroups {
+struct Segment {
   const uint8_t *row[2], *scale[2];
   int cnt[2];
+  int first, count;
 };
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// 1 to 16 rows of one matrix as two groups (the second one's first row again where
-// there are no more than 8).
+// The rows of a segment: 1 to 16 rows of one matrix as two groups (the first row again
+// as the second group where there are no more than 8).
 template <int WT>
-__device__ __forceinline__ RowGroups row_groups(const uint8_t *w, const uint8_t *s, size_t row, int cnt, int K) {
+__device__ __forceinline__ void rows_of_one(Segment &g, const uint8_t *w, const uint8_t *s, size_t row, int cnt,
+                                            int K) {
   using F = Form<WT>;
   const size_t rb = F::row_bytes(K), next = cnt > 8 ? 8 : 0;
-  RowGroups g;
   g.row[0] = w + row * rb;
   g.row[1] = w + (row + next) * rb;
   g.scale[0] = F::mx ? s + row * (K / 32) : nullptr;
   g.scale[1] = F::mx ? s + (row + next) * (K / 32) : nullptr;
   g.cnt[0] = min(cnt, 8);
   g.cnt[1] = max(cnt - 8, 1);
-  return g;
 }
 
-template <int WT, int PC, bool NARROW, class Seg, class Ready, class Acts, class End>
-__device__ __forceinline__ void stream(int total, int C, int c0, int K, uint8_t *xbuf, Seg seg, Ready ready,
-                                       Acts acts, End end) {
+template <int WT, int PC, bool NARROW, class Seg, class Ready, class Begin, class Acts, class End>
+__device__ __forceinline__ void stream(int C, int K, uint8_t *xbuf, Seg seg, Ready ready, Begin begin, Acts acts,
+                                       End end) {
   using F = Form<WT>;
   constexpr int NF = F::kActBytes / 16;
   constexpr bool kTail = WT == kF4Tail;
@@ -116,15 +116,18 @@ __device__ __forceinline__ void stream(int total, int C, int c0, int K, uint8_t 
   const int sback = max(0, 4 * (lane & 3) + 3 - last);  // in the last chunk
   u32x4 w[PC][kSteps];
   uint32_t sc[PC];
-  RowGroups rows;
-  if (total <= 0 || !seg(0, rows)) {
+  Segment rows;
+  if (!seg(0, rows)) {
     ready();
     return;
   }
   uint32_t off[kSteps];  // of the lane's pieces, from its group's first row
   const uint8_t *sp = nullptr;
-  int ld_seg = 0, ld_c = c0, issued = 1;  // the chunk to load next, and its number
-  auto open = [&](int c) {
+  int ld_seg = 0, ld_c = 0, ld_left = 0, issued = 1;  // the chunk to load next, and its number
+  bool more = true;
+  auto open = [&] {
+    const int c = ld_c = rows.first;
+    ld_left = rows.count;
 #pragma unroll
     for (int u = 0; u < kSteps; ++u)
       off[u] = (uint32_t)(min(4 * (u & 1) + g, rows.cnt[u >> 1] - 1) * rb);
@@ -164,31 +167,29 @@ __device__ __forceinline__ void stream(int total, int C, int c0, int K, uint8_t 
         sc[j] = ((const u32_any *)(sp + (at - (end_of_row ? sback : 0))))->v;
       }
     }
-    if (issued < total) {
-      if (ld_c + 1 < C) {
-        ++ld_c;
-        ++issued;
-        if constexpr (!kTail)
+    if (--ld_left > 0) {
+      ++ld_c;
+      ++issued;
+      if constexpr (!kTail)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) rows.row[i] += kChunkBlocks * 16;
-        if constexpr (F::mx) sp += kChunkBlocks;
+        for (int i = 0; i < 2; ++i) rows.row[i] += kChunkBlocks * 16;
+      if constexpr (F::mx) sp += kChunkBlocks;
+    } else if (more) {
+      Segment next;
+      if (seg(ld_seg + 1, next)) {
+        rows = next;
+        ++ld_seg;
+        ++issued;
+        open();
       } else {
-        RowGroups next;
-        if (seg(ld_seg + 1, next)) {
-          rows = next;
-          ++ld_seg;
-          ++issued;
-          ld_c = 0;
-          open(0);
-        } else {
-          total = issued;
-        }
+        more = false;
       }
     }
   };
   f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-  int cur = 0, c = c0;
-  auto use = [&](int j, bool finish) {
+  int cur = -1, c = 0, c_left = 0;
+  auto use = [&](int j) {
+    if (c_left == 0) begin(++cur, c, c_left);
     // piece q of row i lies in slot q ^ i of the row's 16
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -223,14 +224,13 @@ __device__ __forceinline__ void stream(int total, int C, int c0, int K, uint8_t 
       acts(cur, c, 4 * u + g, a, as);
       multiply<WT>(a, as, wj[u], scale[u], acc);
     }
-    if (++c == C || finish) {
+    ++c;
+    if (--c_left == 0) {
       end(cur, acc[0] + acc[1]);
       acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      c = 0;
-      ++cur;
     }
   };
-  open(c0);
+  open();
 #pragma unroll
   for (int j = 0; j < PC; ++j) load(j);
   ready();
@@ -238,7 +238,7 @@ __device__ __forceinline__ void stream(int total, int C, int c0, int K, uint8_t 
   while (used + PC < issued) {  // at least one more load after these
 #pragma unroll
     for (int j = 0; j < PC; ++j) {
-      use(j, false);
+      use(j);
       load(j);
     }
     used += PC;
@@ -246,7 +246,7 @@ __device__ __forceinline__ void stream(int total, int C, int c0, int K, uint8_t 
   const int rest = issued - used;
 #pragma unroll
   for (int j = 0; j < PC; ++j)
-    if (j < rest) use(j, j == rest - 1);
+    if (j < rest) use(j);
 }
 
 // Rows of activations in LDS, cut into row chunks: the kChunkBlocks blocks that one
@@ -268,10 +268,10 @@ __device__ __forceinline__ u32x4 row_chunk_piece(const uint8_t *row, int c, int 
       if (at + i < K) v[i] = ((const uint32_t *)row)[at + i];
   } else {
     const int b = c * kChunkBlocks + l / P;
-    if (b < F::blocks(K)) {
-      const uint8_t *p = row + (size_t)b * F::kActBytes + (l % P) * 16;
-      v = F::f32 ? __builtin_bit_cast(u32x4, *(const f32x4_any *)p) : *(const u32x4 *)p;
-    }
+    const bool in = b < F::blocks(K);
+    const uint8_t *p = row + (in ? (size_t)b * F::kActBytes + (l % P) * 16 : 0);
+    const u32x4 q = F::f32 ? __builtin_bit_cast(u32x4, *(const f32x4_any *)p) : *(const u32x4 *)p;
+    if (in) v = q;
   }
   return v;
 }
