@@ -9,6 +9,7 @@
 #include <atomic>
 
 #include "common.h"
+#include "gemm_common.h"
 #include "kernels.h"
 #include "wave_stream.h"
 
@@ -18,6 +19,9 @@ namespace {
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kRows = 16;  // the M of the MFMA
 constexpr int kRowsLds = 76 * 1024;  // x in LDS where it fits
+constexpr int kRowsBf = 64, kRowsMx = 32;  // rows up to which weights are streamed
+constexpr int kLargeTiles = 256;  // 256 x 256 tiles from which they are taken
+constexpr int kSplitBlocks = 512;
 
 struct LinearParams {
   const uint8_t *x, *xs, *w, *ws;
@@ -143,11 +147,360 @@ bool rows_fit(int n, int d) {
          kRowsLds;
 }
 
+// ---- many rows --------------------------------------------------------------------
+// A block takes BM rows of x by BN rows of W, K in steps of 128 bytes a row: 64 bf16
+// elements (W decoded into the workspace once, as the product's other operand) or
+// 256 MXFP4 ones (both operands in their stored form on the scaled MFMA).  A step is
+// four slices of two 16-byte chunks a row either way, so both share one loop: two LDS
+// stages filled by direct copies, chunks swizzled by row, the MFMA taking W's rows as
+// its first operand.  MXFP4: a step's scales are eight bytes a row, laid out step by
+// step by a kernel in front (scales as stored start at any byte); lane half h of slice
+// s takes byte 2 s + h.
+struct GemmParams {
+  const uint8_t *a, *b;      // [n], [m] rows of rb bytes
+  const uint8_t *as, *bs;    // [steps][np], [steps][mp] x 8 scales
+  const float *bias;
+  void *y;                   // [n][m], or with splits > 1 the planes [splits][n][mp4]
+  int n, m, rb, steps, np, mp, out_bf16;
+  int rt, ct;                // row and column tiles
+  int splits, per;           // K splits, steps of each
+};
+
+constexpr int kRowGroup = 4;  // row tiles that blocks running together share
+
+template <bool MX, int BM, int BN, int NW>
+struct GemmTile {
+  static constexpr int WN_ = NW / 2, WM = BM / 2, WN = BN / WN_, TM = WM / 32, TN = WN / 32;
+  static constexpr int A = BM * 128, B = BN * 128, S = MX ? (BM + BN) * 8 : 0;
+  static constexpr int STAGE = A + B + S;
+  static constexpr int PITCH = WN + 4;  // floats a row of a wave's epilogue piece
+  static constexpr int LDS = 2 * STAGE > NW * 32 * PITCH * 4 ? 2 * STAGE : NW * 32 * PITCH * 4;
+  static_assert(A / 1024 % NW == 0 && B / 1024 % NW == 0, "whole copies a wave");
+};
+
+template <bool MX, int BM, int BN, int NW>
+__global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
+  using T = GemmTile<MX, BM, BN, NW>;
+  using namespace gemm;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lg = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Block -> tile: an eighth of the list to each XCD; groups of kRowGroup row tiles,
+  // column tile by column tile within a group.
+  const int total = p.rt * p.ct * p.splits, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  int base = 0;
+  for (int x = 0; x < xcd; ++x) base += (total - x + 7) >> 3;
+  if (slot >= (total - xcd + 7) >> 3) return;
+  const int item = base + slot, split = item % p.splits, L = item / p.splits;
+  const int grp = L / (kRowGroup * p.ct), within = L - grp * kRowGroup * p.ct;
+  const int gr = min(kRowGroup, p.rt - grp * kRowGroup);
+  const int row0 = (grp * kRowGroup + within % gr) * BM, col0 = within / gr * BN;
+  const int rows = min(BM, p.n - row0), cols = min(BN, p.m - col0);
+  const int k_lo = split * p.per, k_hi = min(p.steps, k_lo + p.per);
+
+  // Copies: run q of wave w is the 1 KB of rows 8 (NW q + w) .. + 7, lane l's chunk l % 8.
+  const __amdgpu_buffer_rsrc_t ra = rsrc(p.a + (size_t)row0 * p.rb, (uint32_t)rows * (uint32_t)p.rb);
+  const __amdgpu_buffer_rsrc_t rbw = rsrc(p.b + (size_t)col0 * p.rb, (uint32_t)cols * (uint32_t)p.rb);
+  const int crow = wave * 8 + (lane >> 3), chunk = (lane & 7) ^ swz_key<128>(crow);
+  static_assert(NW * 8 % 16 == 0, "the swizzle key repeats every 16 rows");
+  const uint32_t off0 = (uint32_t)crow * (uint32_t)p.rb + chunk * 16, rstep = (uint32_t)(NW * 8) * (uint32_t)p.rb;
+  auto issue = [&](int kt, int st) {
+    uint8_t *sa = smem + st * T::STAGE;
+    const uint32_t k = (uint32_t)kt * 128u;
+    const uint32_t out = (kt < k_hi && (int)k + chunk * 16 < p.rb) ? 0u : kOOB;
+#pragma unroll
+    for (int q = 0; q < T::A / 1024 / NW; ++q) {
+      const bool in = crow + q * NW * 8 < rows;
+      dma16(ra, sa + (NW * q + wave) * 1024, in ? (off0 + q * rstep + k) | out : kOOB);
+    }
+#pragma unroll
+    for (int q = 0; q < T::B / 1024 / NW; ++q) {
+      const bool in = crow + q * NW * 8 < cols;
+      dma16(rbw, sa + T::A + (NW * q + wave) * 1024, in ? (off0 + q * rstep + k) | out : kOOB);
+    }
+    if constexpr (MX) {
+      constexpr int RA = BM * 8 / 1024, RB = BN * 8 / 1024;  // copies of scales
+      const int kc = min(kt, p.steps - 1);
+      if (wave < RA) {
+        const __amdgpu_buffer_rsrc_t rs = rsrc(p.as + ((size_t)kc * p.np + row0) * 8, BM * 8);
+        dma16(rs, sa + T::A + T::B + wave * 1024, wave * 1024 + lane * 16);
+      } else if (wave < RA + RB) {
+        const __amdgpu_buffer_rsrc_t rs = rsrc(p.bs + ((size_t)kc * p.mp + col0) * 8, BN * 8);
+        dma16(rs, sa + T::A + T::B + wave * 1024, (wave - RA) * 1024 + lane * 16);
+      }
+    }
+  };
+
+  const int wm = wave / T::WN_, wn = wave % T::WN_;
+  f32x16 acc[T::TM][T::TN];
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  issue(k_lo, 0);
+  for (int kt = k_lo; kt < k_hi; ++kt) {
+    const int st = (kt - k_lo) & 1;
+    wait_vmcnt<0>();
+    __syncthreads();
+    if (kt + 1 < k_hi) issue(kt + 1, st ^ 1);
+    const uint8_t *sa = smem + st * T::STAGE, *sb = sa + T::A;
+    u32x2 as[T::TM], bs[T::TN];
+    if constexpr (MX) {
+      const uint8_t *ss = sb + T::B;
+#pragma unroll
+      for (int i = 0; i < T::TM; ++i) as[i] = *(const u32x2 *)(ss + (wm * T::WM + i * 32 + lr) * 8);
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) bs[j] = *(const u32x2 *)(ss + (BM + wn * T::WN + j * 32 + lr) * 8);
+#pragma unroll
+      for (int i = 0; i < T::TM; ++i) as[i] = u32x2{as[i].x >> (8 * lg), as[i].y >> (8 * lg)};
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) bs[j] = u32x2{bs[j].x >> (8 * lg), bs[j].y >> (8 * lg)};
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      u32x4 af[T::TM], bf[T::TN];
+      const int ch = 2 * s + lg;
+#pragma unroll
+      for (int i = 0; i < T::TM; ++i) af[i] = *(const u32x4 *)(sa + swz<128>(wm * T::WM + i * 32 + lr, ch));
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) bf[j] = *(const u32x4 *)(sb + swz<128>(wn * T::WN + j * 32 + lr, ch));
+#pragma unroll
+      for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j) {
+          if constexpr (MX) {
+            const v8i bv = {(int)bf[j].x, (int)bf[j].y, (int)bf[j].z, (int)bf[j].w, 0, 0, 0, 0};
+            const v8i av = {(int)af[i].x, (int)af[i].y, (int)af[i].z, (int)af[i].w, 0, 0, 0, 0};
+            if (s & 1)
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bv, av, acc[i][j], 4, 4, 2, (int)bs[j][s >> 1],
+                                                                          2, (int)as[i][s >> 1]);
+            else
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bv, av, acc[i][j], 4, 4, 0, (int)bs[j][s >> 1],
+                                                                          0, (int)as[i][s >> 1]);
+          } else {
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bf[j]),
+                                                                __builtin_bit_cast(bf16x8, af[i]), acc[i][j], 0, 0, 0);
+          }
+        }
+    }
+  }
+  __syncthreads();
+  // Epilogue: 32 rows at a time through the wave's own piece of LDS, so that stores
+  // take whole rows of it; 16 bytes a lane where rows of y start at multiples of
+  // eight columns, else column by column.
+  float *piece = (float *)smem + wave * 32 * T::PITCH;
+  const int c0 = col0 + wn * T::WN;
+  const bool plane = p.splits > 1, wide = plane || p.m % 8 == 0;
+  const int pitch = plane ? (p.m + 7) / 8 * 8 : p.m;
+  char *out = (char *)p.y + (plane ? (size_t)split * p.n * pitch * 4 : 0);
+  const bool half = p.out_bf16 && !plane;
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(f32x4 *)(piece + lr * T::PITCH + j * 32 + q * 8 + lg * 4) =
+            f32x4{acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+    const int r0 = wm * T::WM + i * 32;
+    if (wide) {
+      constexpr int LPR = T::WN / 8, RPI = 64 / LPR;  // lanes a row, rows an instruction
+      const int cl = lane % LPR * 8, c = c0 + cl;
+      float bv[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) bv[e] = p.bias && !plane && c + e < p.m ? p.bias[c + e] : 0.f;
+#pragma unroll
+      for (int v = 0; v < 32 / RPI; ++v) {
+        const int r = v * RPI + lane / LPR;
+        const f32x4 x0 = *(const f32x4 *)(piece + r * T::PITCH + cl), x1 = *(const f32x4 *)(piece + r * T::PITCH + cl + 4);
+        if (r0 + r < rows && c < p.m) {
+          const size_t at = (size_t)(row0 + r0 + r) * pitch + c;
+          if (half) {
+            *(u32x4 *)((uint16_t *)out + at) =
+                u32x4{pack_bf16x2(x0[0] + bv[0], x0[1] + bv[1]), pack_bf16x2(x0[2] + bv[2], x0[3] + bv[3]),
+                      pack_bf16x2(x1[0] + bv[4], x1[1] + bv[5]), pack_bf16x2(x1[2] + bv[6], x1[3] + bv[7])};
+          } else {
+            *(f32x4 *)((float *)out + at) = f32x4{x0[0] + bv[0], x0[1] + bv[1], x0[2] + bv[2], x0[3] + bv[3]};
+            *(f32x4 *)((float *)out + at + 4) = f32x4{x1[0] + bv[4], x1[1] + bv[5], x1[2] + bv[6], x1[3] + bv[7]};
+          }
+        }
+      }
+    } else {
+      const int cl = lane % T::WN, c = c0 + cl;
+      const float b = p.bias && c < p.m ? p.bias[c] : 0.f;
+      for (int r = lane / T::WN; r < 32; r += 64 / T::WN)
+        if (r0 + r < rows && c < p.m) {
+          const float v = piece[r * T::PITCH + cl] + b;
+          const size_t at = (size_t)(row0 + r0 + r) * p.m + c;
+          if (half)
+            ((uint16_t *)out)[at] = (uint16_t)f32_to_bf16_bits(v);
+          else
+            ((float *)out)[at] = v;
+        }
+    }
+    __builtin_amdgcn_wave_barrier();  // the piece is read before the next rows go there
+  }
+}
+
+// y = bias + the planes' sum, in plane order.
+__global__ __launch_bounds__(256) void linear_sum_kernel(const float *__restrict__ part, int splits, int n, int m, int mp,
+                                                         const float *__restrict__ bias, void *__restrict__ y,
+                                                         int out_bf16) {
+  const size_t lanes = (size_t)n * (mp / 4), plane = (size_t)n * mp, stride = (size_t)gridDim.x * 256;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < lanes; i += stride) {
+    const size_t r = i / (mp / 4);
+    const int c = (int)(i - r * (mp / 4)) * 4;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s) v += *(const f32x4 *)(part + s * plane + r * mp + c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < m) {
+        const float o = bias ? v[e] + bias[c + e] : v[e];
+        if (out_bf16)
+          ((uint16_t *)y)[r * m + c + e] = (uint16_t)f32_to_bf16_bits(o);
+        else
+          ((float *)y)[r * m + c + e] = o;
+      }
+  }
+}
+
+// Scales [rows][KB] of two matrices as [steps][padded rows][8], 127 (one) where there
+// are none.
+__global__ __launch_bounds__(256) void linear_scales_kernel(const uint8_t *__restrict__ xs, uint2 *__restrict__ xo, int n,
+                                                            int np, const uint8_t *__restrict__ ws,
+                                                            uint2 *__restrict__ wo, int m, int mp, int KB, int steps) {
+  const int per = (np + mp), total = per * steps;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+    // (steps of a row next to each other: the reads are consecutive)
+    const int kt = i % steps, rr = i / steps;
+    const bool first = rr < np;
+    const int row = first ? rr : rr - np;
+    const bool in = row < (first ? n : m);
+    const uint8_t *s = (first ? xs : ws) + (size_t)row * KB + kt * 8;
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lo |= (in && kt * 8 + j < KB ? s[j] : 127u) << (8 * j);
+      hi |= (in && kt * 8 + 4 + j < KB ? s[4 + j] : 127u) << (8 * j);
+    }
+    (first ? xo : wo)[(size_t)kt * (first ? np : mp) + row] = uint2{lo, hi};
+  }
+}
+
+// How a product is run: by rows (streamed weights) or by a GEMM of BM = BN tiles with K
+// split into planes.
+struct LinearPlan {
+  bool rows;
+  int tile, splits, per, steps, rb, np, mp;
+  size_t wb, xs, ws, part, total;  // workspace: decoded W; scales step by step; planes
+};
+
+LinearPlan plan_linear(int n, int d, int m, bool mx) {
+  LinearPlan P{};
+  P.rows = n <= (mx ? kRowsMx : kRowsBf);
+  if (P.rows) return P;
+  auto tiles = [&](int t) { return (long long)((n + t - 1) / t) * ((m + t - 1) / t); };
+  P.tile = tiles(256) >= kLargeTiles ? 256 : 128;
+  P.rb = mx ? d / 2 : d * 2;
+  P.steps = (P.rb + 127) / 128;
+  P.splits = 1;
+  if (P.tile == 128) {
+    const long long t = tiles(128);
+    while (P.splits < 8 && t * P.splits * 2 <= kSplitBlocks && P.steps / (P.splits * 2) >= 4) P.splits *= 2;
+  }
+  P.per = (P.steps + P.splits - 1) / P.splits;
+  P.splits = (P.steps + P.per - 1) / P.per;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  P.np = (n + 255) / 256 * 256;
+  P.mp = (m + 255) / 256 * 256;
+  if (mx) {
+    P.xs = take((size_t)P.steps * P.np * 8);
+    P.ws = take((size_t)P.steps * P.mp * 8);
+  } else {
+    P.wb = take((size_t)m * d * 2);
+  }
+  P.part = take(P.splits > 1 ? (size_t)P.splits * n * ((m + 7) / 8 * 8) * 4 : 0);
+  P.total = o;
+  return P;
+}
+
+template <bool MX, int BM, int NW>
+hipError_t launch_gemm(const GemmParams &p, hipStream_t st) {
+  using T = GemmTile<MX, BM, BM, NW>;
+  auto kern = linear_gemm_kernel<MX, BM, BM, NW>;
+  if (T::LDS > 64 * 1024) {
+    static std::atomic<uint64_t> attr_done{0};
+    int dev = 0;
+    hipError_t err = hipGetDevice(&dev);
+    if (err != hipSuccess) return err;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+      err = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
+      if (err != hipSuccess) return err;
+      attr_done.fetch_or(bit, std::memory_order_release);
+    }
+  }
+  const int total = p.rt * p.ct * p.splits;
+  kern<<<(total + 7) / 8 * 8, NW * 64, T::LDS, st>>>(p);
+  return hipGetLastError();
+}
+
+template <bool MX>
+hipError_t launch_many(const LinearArgs &a, hipStream_t st) {
+  const LinearPlan P = plan_linear(a.n, a.d, a.m, MX);
+  char *ws = (char *)a.ws;
+  GemmParams p{};
+  p.a = (const uint8_t *)a.x;
+  p.bias = a.bias;
+  p.n = a.n;
+  p.m = a.m;
+  p.rb = P.rb;
+  p.steps = P.steps;
+  p.np = P.np;
+  p.mp = P.mp;
+  p.out_bf16 = a.out_bf16;
+  p.rt = (a.n + P.tile - 1) / P.tile;
+  p.ct = (a.m + P.tile - 1) / P.tile;
+  p.splits = P.splits;
+  p.per = P.per;
+  p.y = P.splits > 1 ? (void *)(ws + P.part) : a.y;
+  hipError_t e;
+  if (MX) {
+    p.b = a.w;
+    p.as = (uint8_t *)ws + P.xs;
+    p.bs = (uint8_t *)ws + P.ws;
+    const long long total = (long long)(P.np + P.mp) * P.steps;
+    linear_scales_kernel<<<(int)std::min<long long>((total + 255) / 256, 2048), 256, 0, st>>>(
+        a.x_s, (uint2 *)(ws + P.xs), a.n, P.np, a.w_s, (uint2 *)(ws + P.ws), a.m, P.mp, a.d / 32, P.steps);
+    e = hipGetLastError();
+  } else {
+    p.b = (uint8_t *)ws + P.wb;
+    e = launch_dequantize_mx4(a.w, a.w_s, (size_t)a.m * (a.d / 32), ws + P.wb, true, st);
+  }
+  if (e != hipSuccess) return e;
+  e = P.tile == 256 ? launch_gemm<MX, 256, 8>(p, st) : launch_gemm<MX, 128, 4>(p, st);
+  if (e != hipSuccess || P.splits == 1) return e;
+  const int mp = (a.m + 7) / 8 * 8;
+  const long long lanes = (long long)a.n * (mp / 4);
+  linear_sum_kernel<<<(int)std::min<long long>((lanes + 255) / 256, 2048), 256, 0, st>>>(
+      (const float *)(ws + P.part), P.splits, a.n, a.m, mp, a.bias, a.y, a.out_bf16);
+  return hipGetLastError();
+}
+
 }  // namespace
 
-size_t mxfp4_linear_bytes(int n, int d, int m, bool x_mx4) { return 0; }
+size_t mxfp4_linear_bytes(int n, int d, int m, bool x_mx4) { return plan_linear(n, d, m, x_mx4).total; }
 
 hipError_t launch_mxfp4_linear(const LinearArgs &a, hipStream_t st) {
+  if (!plan_linear(a.n, a.d, a.m, a.x_mx4).rows) return a.x_mx4 ? launch_many<true>(a, st) : launch_many<false>(a, st);
   LinearParams p{};
   p.x = (const uint8_t *)a.x;
   p.xs = a.x_s;
