@@ -168,18 +168,17 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
   }
 }
 
-// Threads of a gradient block: a row's, at least 512.
-constexpr int grad_threads(int tpr) { return tpr > 512 ? tpr : 512; }
+constexpr int kGradThreads = 1024;  // of a gradient block
 
 template <bool BF, bool TAIL, int C, int TPR>
-__global__ __launch_bounds__(grad_threads(TPR)) void block_norm_grad_kernel(BlockNormParams p) {
+__global__ __launch_bounds__(kGradThreads) void block_norm_grad_kernel(BlockNormParams p) {
   using K = Chunk<BF, TAIL>;
-  constexpr int V = K::V, NT = grad_threads(TPR), G = NT / TPR;
+  constexpr int V = K::V, NT = kGradThreads, G = NT / TPR;
   __shared__ float s_buf[2][2][NT / 64];
   // Row groups' column sums: within a wave by lane permutations, then over WG
   // groups of TW threads in halves through LDS.
   constexpr int TW = TPR < 64 ? 64 : TPR, WG = NT / TW, COLS = TPR * C * V;
-  __shared__ __attribute__((aligned(16))) float s_col[4][WG > 1 ? WG / 2 * COLS : 4];
+  __shared__ __attribute__((aligned(16))) float s_col[2][WG > 1 ? WG / 2 * COLS : 4];
   RowSum<float, TPR, NT, 2> row_sum(s_buf);
   const int n = p.n, d = p.d, grp = threadIdx.x / TPR, gl = threadIdx.x % TPR, stride = gridDim.x * G;
   const int post = p.post.kind, pre = p.pre.kind;
@@ -236,7 +235,6 @@ __global__ __launch_bounds__(grad_threads(TPR)) void block_norm_grad_kernel(Bloc
           s[1] = fmaf(t[c][j], xh[c][j], s[1]);
         }
       }
-      load_row(row + stride);
       row_sum(s);
       const float q1 = pre == kLayer ? s[0] * inv_d : 0.f, q2 = s[1] * inv_d;
 #pragma unroll
@@ -244,9 +242,10 @@ __global__ __launch_bounds__(grad_threads(TPR)) void block_norm_grad_kernel(Bloc
 #pragma unroll
         for (int j = 0; j < V; ++j)  // (past the row's end these stay out of every sum and store)
           D[c][j] = fmaf(rb, t[c][j] - q1 - xh[c][j] * q2, D[c][j]);
-    } else {
-      load_row(row + stride);
     }
+    // the next row, under the rest of this one (asked for earlier, its registers do not
+    // fit beside the first norm's)
+    load_row(row + stride);
 #pragma unroll
     for (int c = 0; c < C; ++c)
       if (live) {
@@ -306,27 +305,31 @@ __global__ __launch_bounds__(grad_threads(TPR)) void block_norm_grad_kernel(Bloc
   const bool mine = (int)threadIdx.x % TW < TPR;  // (below 64 threads a row: the wave's first group)
 #pragma unroll
   for (int half = WG / 2; half > 0; half /= 2) {
-    auto each = [&](int at, auto fn) {
-      if (mine)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int two = 0; two < 4; two += 2) {  // two sums at a time
+      auto each = [&](int at, auto fn) {
+        if (mine)
 #pragma unroll
-          for (int c = 0; c < C; ++c)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < V; j += 4) fn(i, c, j, at * COLS + (c * TPR + gl) * V + j);
-    };
-    if (wg >= half && wg < 2 * half)
-      each(wg - half, [&](int i, int c, int j, int at) {
-        *(f32x4 *)&s_col[i][at] = f32x4{S[i][c][j], S[i][c][j + 1], S[i][c][j + 2], S[i][c][j + 3]};
-      });
-    __syncthreads();
-    if (wg < half)
-      each(wg, [&](int i, int c, int j, int at) {
-        const f32x4 q = *(const f32x4 *)&s_col[i][at];
+            for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) S[i][c][j + y] += q[y];
-      });
-    __syncthreads();
+              for (int j = 0; j < V; j += 4) fn(i, c, j, at * COLS + (c * TPR + gl) * V + j);
+      };
+      if (wg >= half && wg < 2 * half)
+        each(wg - half, [&](int i, int c, int j, int at) {
+          const float *v = &S[two + i][c][j];
+          *(f32x4 *)&s_col[i][at] = f32x4{v[0], v[1], v[2], v[3]};
+        });
+      __syncthreads();
+      if (wg < half)
+        each(wg, [&](int i, int c, int j, int at) {
+          const f32x4 q = *(const f32x4 *)&s_col[i][at];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) S[two + i][c][j + y] += q[y];
+        });
+      __syncthreads();
+    }
   }
   if (wg == 0 && mine)
 #pragma unroll
@@ -403,9 +406,9 @@ template <bool BF, bool TAIL>
 hipError_t launch_grad(const BlockNormParams &p, int &P, hipStream_t st) {
   return with_layout<BF, TAIL>(p.d, [&](auto cc, auto tt) {
     constexpr int C = decltype(cc)::value, TPR = decltype(tt)::value;
-    constexpr int G = grad_threads(TPR) / TPR;
+    constexpr int G = kGradThreads / TPR;
     P = grad_blocks((p.n + G - 1) / G);
-    if (P > 0) block_norm_grad_kernel<BF, TAIL, C, TPR><<<P, grad_threads(TPR), 0, st>>>(p);
+    if (P > 0) block_norm_grad_kernel<BF, TAIL, C, TPR><<<P, kGradThreads, 0, st>>>(p);
     return hipGetLastError();
   });
 }

@@ -69,6 +69,8 @@ __global__ __launch_bounds__(kThreads) void quantize_mx4_kernel(const void *__re
   }
 }
 
+// The conversion instructions take the scale; a bf16 or float32 value is exact down to
+// 2^-128.
 template <bool BF>
 __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(const uint32_t *__restrict__ q,
                                                                   const uint8_t *__restrict__ s, size_t lanes,
@@ -77,21 +79,16 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(const uint32_t
   for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < lanes; i += stride) {
     const uint32_t w = q[i];
     const float sc = e8m0_to_f32(s[i >> 2]);
-    // E2M1 magnitudes are exact in bf16; the scale is applied in float32, where
-    // products down to 2^-128 are exact too.
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t c = (w >> (4 * j)) & 7u;
-      const float mag = c < 2u ? 0.5f * (float)c : __uint_as_float((126u + (c >> 1)) << 23 | (c & 1u) << 22);
-      v[j] = __uint_as_float(__float_as_uint(mag) | ((w >> (4 * j + 3)) & 1u) << 31) * sc;
-    }
     if constexpr (BF) {
-      ((u32x4 *)y)[i] = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                              pack_bf16x2(v[6], v[7])};
+      ((u32x4 *)y)[i] = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0)),
+                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1)),
+                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2)),
+                              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3))};
     } else {
-      ((f32x4 *)y)[2 * i] = f32x4{v[0], v[1], v[2], v[3]};
-      ((f32x4 *)y)[2 * i + 1] = f32x4{v[4], v[5], v[6], v[7]};
+      const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, sc, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, sc, 1);
+      const auto c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, sc, 2), e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, sc, 3);
+      ((f32x4 *)y)[2 * i] = f32x4{a[0], a[1], b[0], b[1]};
+      ((f32x4 *)y)[2 * i + 1] = f32x4{c[0], c[1], e[0], e[1]};
     }
   }
 }
