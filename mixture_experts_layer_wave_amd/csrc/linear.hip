@@ -148,20 +148,22 @@ bool rows_fit(int n, int d) {
 }
 
 // ---- many rows --------------------------------------------------------------------
-// A block takes BM rows of x by BN rows of W, K in steps of 128 bytes a row: 64 bf16
-// elements (W decoded into the workspace once, as the product's other operand) or
-// 256 MXFP4 ones (both operands in their stored form on the scaled MFMA).  A step is
-// four slices of two 16-byte chunks a row either way, so both share one loop: two LDS
-// stages filled by direct copies, chunks swizzled by row, the MFMA taking W's rows as
-// its first operand.  MXFP4: a step's scales are eight bytes a row, laid out step by
-// step by a kernel in front (scales as stored start at any byte); lane half h of slice
-// s takes byte 2 s + h.
+// A block takes BM rows of x by BN rows of W through two LDS stages filled by direct
+// copies, 16-byte chunks swizzled by row; the MFMA takes W's rows as its first operand.
+// A step is 128 bytes of a row of x, in four slices:
+//   bf16 rows (MX = false): 64 elements.  W's codes lie in LDS, 32 bytes a row; lane
+//     half h of a wave converts block h of the step (v_cvt_scalef32_pk_bf16_fp4), whose
+//     elements 8 s .. are slice s's, and takes x's elements 32 h + 8 s .. to match.  The
+//     scale is one byte a lane and step, straight from memory.
+//   MXFP4 rows: 256 elements, both operands in their stored form on the scaled MFMA.
+//     A step's scales are eight bytes a row, laid out step by step by a kernel in front
+//     (as stored they start at any byte); lane half h of slice s takes byte 2 s + h.
 struct GemmParams {
-  const uint8_t *a, *b;      // [n], [m] rows of rb bytes
-  const uint8_t *as, *bs;    // [steps][np], [steps][mp] x 8 scales
+  const uint8_t *a, *b;      // [n] rows of rb bytes, [m] rows of d / 2
+  const uint8_t *as, *bs;    // MX: [steps][np], [steps][mp] x 8 scales; else bs [m][d / 32]
   const float *bias;
   void *y;                   // [n][m], or with splits > 1 the planes [splits][n][mp4]
-  int n, m, rb, steps, np, mp, out_bf16;
+  int n, m, d, rb, steps, np, mp, out_bf16;
   int rt, ct;                // row and column tiles
   int splits, per;           // K splits, steps of each
 };
@@ -171,7 +173,8 @@ constexpr int kRowGroup = 4;  // row tiles that blocks running together share
 template <bool MX, int BM, int BN, int NW>
 struct GemmTile {
   static constexpr int WN_ = NW / 2, WM = BM / 2, WN = BN / WN_, TM = WM / 32, TN = WN / 32;
-  static constexpr int A = BM * 128, B = BN * 128, S = MX ? (BM + BN) * 8 : 0;
+  static constexpr int RB = MX ? 128 : 32;  // bytes of a row of W in a step
+  static constexpr int A = BM * 128, B = BN * RB, S = MX ? (BM + BN) * 8 : 0;
   static constexpr int STAGE = A + B + S;
   static constexpr int PITCH = WN + 4;  // floats a row of a wave's epilogue piece
   static constexpr int LDS = 2 * STAGE > NW * 32 * PITCH * 4 ? 2 * STAGE : NW * 32 * PITCH * 4;
@@ -200,10 +203,22 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
 
   // Copies: run q of wave w is the 1 KB of rows 8 (NW q + w) .. + 7, lane l's chunk l % 8.
   const __amdgpu_buffer_rsrc_t ra = rsrc(p.a + (size_t)row0 * p.rb, (uint32_t)rows * (uint32_t)p.rb);
-  const __amdgpu_buffer_rsrc_t rbw = rsrc(p.b + (size_t)col0 * p.rb, (uint32_t)cols * (uint32_t)p.rb);
+  const uint32_t wb = (uint32_t)p.d / 2;  // bytes of a row of W
+  const __amdgpu_buffer_rsrc_t rbw = rsrc(p.b + (size_t)col0 * wb, (uint32_t)cols * wb);
   const int crow = wave * 8 + (lane >> 3), chunk = (lane & 7) ^ swz_key<128>(crow);
   static_assert(NW * 8 % 16 == 0, "the swizzle key repeats every 16 rows");
   const uint32_t off0 = (uint32_t)crow * (uint32_t)p.rb + chunk * 16, rstep = (uint32_t)(NW * 8) * (uint32_t)p.rb;
+  const int wrow = wave * 32 + (lane >> 1), wchunk = (lane & 1) ^ swz_key<32>(wrow);  // not MX: 32 rows a copy
+  const int wm = wave / T::WN_, wn = wave % T::WN_;
+  // not MX: this lane's scales, of the blocks 2 kt + lg
+  const int KB = p.d / 32;
+  const uint8_t *sp[T::TN];
+  uint8_t sc[T::TN];
+#pragma unroll
+  for (int j = 0; j < T::TN; ++j) {
+    sp[j] = MX ? nullptr : p.bs + (size_t)(col0 + min(wn * T::WN + j * 32 + lr, cols - 1)) * KB;
+    sc[j] = 127;
+  }
   auto issue = [&](int kt, int st) {
     uint8_t *sa = smem + st * T::STAGE;
     const uint32_t k = (uint32_t)kt * 128u;
@@ -213,10 +228,16 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
       const bool in = crow + q * NW * 8 < rows;
       dma16(ra, sa + (NW * q + wave) * 1024, in ? (off0 + q * rstep + k) | out : kOOB);
     }
+    if constexpr (MX) {
 #pragma unroll
-    for (int q = 0; q < T::B / 1024 / NW; ++q) {
-      const bool in = crow + q * NW * 8 < cols;
-      dma16(rbw, sa + T::A + (NW * q + wave) * 1024, in ? (off0 + q * rstep + k) | out : kOOB);
+      for (int q = 0; q < T::B / 1024 / NW; ++q) {
+        const bool in = crow + q * NW * 8 < cols;
+        dma16(rbw, sa + T::A + (NW * q + wave) * 1024, in ? (off0 + q * rstep + k) | out : kOOB);
+      }
+    } else {
+      static_assert(MX || T::B / 1024 == NW, "a copy of W a wave");
+      const uint32_t kb = (uint32_t)kt * 32u + wchunk * 16;
+      dma16(rbw, sa + T::A + wave * 1024, (kt < k_hi && wrow < cols && kb < wb) ? (uint32_t)wrow * wb + kb : kOOB);
     }
     if constexpr (MX) {
       constexpr int RA = BM * 8 / 1024, RB = BN * 8 / 1024;  // copies of scales
@@ -231,7 +252,11 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
     }
   };
 
-  const int wm = wave / T::WN_, wn = wave % T::WN_;
+  auto load_scales = [&](int kt) {
+    if constexpr (!MX)
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) sc[j] = sp[j][min(2 * kt + lg, KB - 1)];
+  };
   f32x16 acc[T::TM][T::TN];
 #pragma unroll
   for (int i = 0; i < T::TM; ++i)
@@ -241,13 +266,20 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
   issue(k_lo, 0);
+  load_scales(k_lo);
   for (int kt = k_lo; kt < k_hi; ++kt) {
     const int st = (kt - k_lo) & 1;
     wait_vmcnt<0>();
     __syncthreads();
+    float scale[T::TN];
+    if constexpr (!MX)
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) scale[j] = e8m0_to_f32(2 * kt + lg < KB ? sc[j] : 127u);
     if (kt + 1 < k_hi) issue(kt + 1, st ^ 1);
+    load_scales(kt + 1);
     const uint8_t *sa = smem + st * T::STAGE, *sb = sa + T::A;
     u32x2 as[T::TM], bs[T::TN];
+    u32x4 codes[T::TN];
     if constexpr (MX) {
       const uint8_t *ss = sb + T::B;
 #pragma unroll
@@ -258,15 +290,27 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
       for (int i = 0; i < T::TM; ++i) as[i] = u32x2{as[i].x >> (8 * lg), as[i].y >> (8 * lg)};
 #pragma unroll
       for (int j = 0; j < T::TN; ++j) bs[j] = u32x2{bs[j].x >> (8 * lg), bs[j].y >> (8 * lg)};
+    } else {
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) codes[j] = *(const u32x4 *)(sb + swz<32>(wn * T::WN + j * 32 + lr, lg));
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       u32x4 af[T::TM], bf[T::TN];
-      const int ch = 2 * s + lg;
+      const int ch = MX ? 2 * s + lg : 4 * lg + s;
 #pragma unroll
       for (int i = 0; i < T::TM; ++i) af[i] = *(const u32x4 *)(sa + swz<128>(wm * T::WM + i * 32 + lr, ch));
 #pragma unroll
-      for (int j = 0; j < T::TN; ++j) bf[j] = *(const u32x4 *)(sb + swz<128>(wn * T::WN + j * 32 + lr, ch));
+      for (int j = 0; j < T::TN; ++j) {
+        if constexpr (MX)
+          bf[j] = *(const u32x4 *)(sb + swz<128>(wn * T::WN + j * 32 + lr, ch));
+        else
+          bf[j] = u32x4{
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 0)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 1)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 2)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 3))};
+      }
 #pragma unroll
       for (int i = 0; i < T::TM; ++i)
 #pragma unroll
@@ -395,7 +439,7 @@ __global__ __launch_bounds__(256) void linear_scales_kernel(const uint8_t *__res
 struct LinearPlan {
   bool rows;
   int tile, splits, per, steps, rb, np, mp;
-  size_t wb, xs, ws, part, total;  // workspace: decoded W; scales step by step; planes
+  size_t xs, ws, part, total;  // workspace: scales step by step; planes
 };
 
 LinearPlan plan_linear(int n, int d, int m, bool mx) {
@@ -424,8 +468,6 @@ LinearPlan plan_linear(int n, int d, int m, bool mx) {
   if (mx) {
     P.xs = take((size_t)P.steps * P.np * 8);
     P.ws = take((size_t)P.steps * P.mp * 8);
-  } else {
-    P.wb = take((size_t)m * d * 2);
   }
   P.part = take(P.splits > 1 ? (size_t)P.splits * n * ((m + 7) / 8 * 8) * 4 : 0);
   P.total = o;
@@ -472,9 +514,10 @@ hipError_t launch_many(const LinearArgs &a, hipStream_t st) {
   p.splits = P.splits;
   p.per = P.per;
   p.y = P.splits > 1 ? (void *)(ws + P.part) : a.y;
-  hipError_t e;
+  p.b = a.w;
+  p.d = a.d;
+  hipError_t e = hipSuccess;
   if (MX) {
-    p.b = a.w;
     p.as = (uint8_t *)ws + P.xs;
     p.bs = (uint8_t *)ws + P.ws;
     const long long total = (long long)(P.np + P.mp) * P.steps;
@@ -482,8 +525,7 @@ hipError_t launch_many(const LinearArgs &a, hipStream_t st) {
         a.x_s, (uint2 *)(ws + P.xs), a.n, P.np, a.w_s, (uint2 *)(ws + P.ws), a.m, P.mp, a.d / 32, P.steps);
     e = hipGetLastError();
   } else {
-    p.b = (uint8_t *)ws + P.wb;
-    e = launch_dequantize_mx4(a.w, a.w_s, (size_t)a.m * (a.d / 32), ws + P.wb, true, st);
+    p.bs = a.w_s;
   }
   if (e != hipSuccess) return e;
   e = P.tile == 256 ? launch_gemm<MX, 256, 8>(p, st) : launch_gemm<MX, 128, 4>(p, st);

@@ -43,16 +43,25 @@ struct Chunk {
   }
   // Element j of the chunk at col is inside the row.
   static __device__ __forceinline__ bool in(int col, int j, int d) { return TAIL ? col + j < d : col < d; }
+  // NT: a store that leaves the caches to others.
+  template <bool NT = false>
   static __device__ __forceinline__ void store(void *p, size_t row, int col, int d, const float *v) {
     if (col >= d) return;
     if constexpr (BF) {
       const u32x4 o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                        pack_bf16x2(v[6], v[7])};
-      *(u32x4 *)((uint16_t *)p + row * d + col) = o;
+      u32x4 *at = (u32x4 *)((uint16_t *)p + row * d + col);
+      if constexpr (NT)
+        __builtin_nontemporal_store(o, at);
+      else
+        *at = o;
     } else {
       float *f = (float *)p + row * d + col;
       if (!TAIL || col + 4 <= d)
-        *(f32x4_any *)f = f32x4{v[0], v[1], v[2], v[3]};
+        if constexpr (NT)
+          __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4_any *)f);
+        else
+          *(f32x4_any *)f = f32x4{v[0], v[1], v[2], v[3]};
       else
 #pragma unroll
         for (int j = 0; j < 3; ++j)
