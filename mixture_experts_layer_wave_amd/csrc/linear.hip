@@ -19,9 +19,9 @@ namespace {
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kRows = 16;  // the M of the MFMA
 constexpr int kRowsLds = 76 * 1024;  // x in LDS where it fits
-constexpr int kRowsBf = 64, kRowsMx = 32;  // rows up to which weights are streamed
-constexpr int kLargeTiles = 256;  // 256 x 256 tiles from which they are taken
-constexpr int kSplitBlocks = 512;
+constexpr int kRowsMany = 16;  // rows above which the GEMM takes over
+constexpr int kLargeTiles = 200;  // 256 x 256 tiles from which they are taken
+constexpr int kSplitBlocks = 512;  // blocks up to which K is split
 
 struct LinearParams {
   const uint8_t *x, *xs, *w, *ws;
@@ -167,6 +167,30 @@ struct GemmParams {
   int rt, ct;                // row and column tiles
   int splits, per;           // K splits, steps of each
 };
+
+typedef u32x4 u32x4_any2 __attribute__((aligned(2)));
+
+// Eight columns of a row of y from element `at` on, of which `left` are inside the row.
+__device__ __forceinline__ void store_columns8(char *y, size_t at, int left, bool half, const float (&o)[8]) {
+  if (left >= 8) {
+    if (half) {
+      *(u32x4_any2 *)((uint16_t *)y + at) = u32x4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                                                  pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
+    } else {
+      *(f32x4_any *)((float *)y + at) = f32x4{o[0], o[1], o[2], o[3]};
+      *(f32x4_any *)((float *)y + at + 4) = f32x4{o[4], o[5], o[6], o[7]};
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < left) {
+      if (half)
+        ((uint16_t *)y)[at + e] = (uint16_t)f32_to_bf16_bits(o[e]);
+      else
+        ((float *)y)[at + e] = o[e];
+    }
+}
 
 constexpr int kRowGroup = 4;  // row tiles that blocks running together share
 
@@ -333,14 +357,18 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
   }
   __syncthreads();
   // Epilogue: 32 rows at a time through the wave's own piece of LDS, so that stores
-  // take whole rows of it; 16 bytes a lane where rows of y start at multiples of
-  // eight columns, else column by column.
+  // take whole rows of it, eight columns a lane (y's rows start at any element).
   float *piece = (float *)smem + wave * 32 * T::PITCH;
   const int c0 = col0 + wn * T::WN;
-  const bool plane = p.splits > 1, wide = plane || p.m % 8 == 0;
-  const int pitch = plane ? (p.m + 7) / 8 * 8 : p.m;
+  const bool plane = p.splits > 1;
+  const int pitch = plane ? (p.m + 7) / 8 * 8 : p.m, width = plane ? pitch : p.m;
   char *out = (char *)p.y + (plane ? (size_t)split * p.n * pitch * 4 : 0);
   const bool half = p.out_bf16 && !plane;
+  constexpr int LPR = T::WN / 8, RPI = 64 / LPR;  // lanes a row, rows an instruction
+  const int cl = lane % LPR * 8, c = c0 + cl;
+  float bv[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) bv[e] = p.bias && !plane && c + e < p.m ? p.bias[c + e] : 0.f;
 #pragma unroll
   for (int i = 0; i < T::TM; ++i) {
 #pragma unroll
@@ -350,64 +378,42 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
         *(f32x4 *)(piece + lr * T::PITCH + j * 32 + q * 8 + lg * 4) =
             f32x4{acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
     const int r0 = wm * T::WM + i * 32;
-    if (wide) {
-      constexpr int LPR = T::WN / 8, RPI = 64 / LPR;  // lanes a row, rows an instruction
-      const int cl = lane % LPR * 8, c = c0 + cl;
-      float bv[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) bv[e] = p.bias && !plane && c + e < p.m ? p.bias[c + e] : 0.f;
+    for (int v = 0; v < 32 / RPI; ++v) {
+      const int r = v * RPI + lane / LPR;
+      const f32x4 x0 = *(const f32x4 *)(piece + r * T::PITCH + cl), x1 = *(const f32x4 *)(piece + r * T::PITCH + cl + 4);
+      if (r0 + r < rows) {
+        float o[8];
 #pragma unroll
-      for (int v = 0; v < 32 / RPI; ++v) {
-        const int r = v * RPI + lane / LPR;
-        const f32x4 x0 = *(const f32x4 *)(piece + r * T::PITCH + cl), x1 = *(const f32x4 *)(piece + r * T::PITCH + cl + 4);
-        if (r0 + r < rows && c < p.m) {
-          const size_t at = (size_t)(row0 + r0 + r) * pitch + c;
-          if (half) {
-            *(u32x4 *)((uint16_t *)out + at) =
-                u32x4{pack_bf16x2(x0[0] + bv[0], x0[1] + bv[1]), pack_bf16x2(x0[2] + bv[2], x0[3] + bv[3]),
-                      pack_bf16x2(x1[0] + bv[4], x1[1] + bv[5]), pack_bf16x2(x1[2] + bv[6], x1[3] + bv[7])};
-          } else {
-            *(f32x4 *)((float *)out + at) = f32x4{x0[0] + bv[0], x0[1] + bv[1], x0[2] + bv[2], x0[3] + bv[3]};
-            *(f32x4 *)((float *)out + at + 4) = f32x4{x1[0] + bv[4], x1[1] + bv[5], x1[2] + bv[6], x1[3] + bv[7]};
-          }
-        }
+        for (int e = 0; e < 4; ++e) o[e] = x0[e] + bv[e], o[4 + e] = x1[e] + bv[4 + e];
+        store_columns8(out, (size_t)(row0 + r0 + r) * pitch + c, width - c, half, o);
       }
-    } else {
-      const int cl = lane % T::WN, c = c0 + cl;
-      const float b = p.bias && c < p.m ? p.bias[c] : 0.f;
-      for (int r = lane / T::WN; r < 32; r += 64 / T::WN)
-        if (r0 + r < rows && c < p.m) {
-          const float v = piece[r * T::PITCH + cl] + b;
-          const size_t at = (size_t)(row0 + r0 + r) * p.m + c;
-          if (half)
-            ((uint16_t *)out)[at] = (uint16_t)f32_to_bf16_bits(v);
-          else
-            ((float *)out)[at] = v;
-        }
     }
     __builtin_amdgcn_wave_barrier();  // the piece is read before the next rows go there
   }
 }
 
-// y = bias + the planes' sum, in plane order.
+// y = bias + the planes' sum, in plane order: blocks of 8 x 256 columns of a row.
 __global__ __launch_bounds__(256) void linear_sum_kernel(const float *__restrict__ part, int splits, int n, int m, int mp,
-                                                         const float *__restrict__ bias, void *__restrict__ y,
+                                                         const float *__restrict__ bias, char *__restrict__ y,
                                                          int out_bf16) {
-  const size_t lanes = (size_t)n * (mp / 4), plane = (size_t)n * mp, stride = (size_t)gridDim.x * 256;
-  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < lanes; i += stride) {
-    const size_t r = i / (mp / 4);
-    const int c = (int)(i - r * (mp / 4)) * 4;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < splits; ++s) v += *(const f32x4 *)(part + s * plane + r * mp + c);
+  const size_t plane = (size_t)n * mp;
+  const int c = (blockIdx.x * 256 + threadIdx.x) * 8;
+  if (c >= m) return;
+  float bv[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c + e < m) {
-        const float o = bias ? v[e] + bias[c + e] : v[e];
-        if (out_bf16)
-          ((uint16_t *)y)[r * m + c + e] = (uint16_t)f32_to_bf16_bits(o);
-        else
-          ((float *)y)[r * m + c + e] = o;
-      }
+  for (int e = 0; e < 8; ++e) bv[e] = bias && c + e < m ? bias[c + e] : 0.f;
+  for (int r = blockIdx.y; r < n; r += gridDim.y) {
+    const float *p = part + (size_t)r * mp + c;
+    f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+    for (int s = 0; s < splits; ++s) {
+      a += *(const f32x4 *)(p + s * plane);
+      b += *(const f32x4 *)(p + s * plane + 4);
+    }
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = a[e] + bv[e], o[4 + e] = b[e] + bv[4 + e];
+    store_columns8(y, (size_t)r * m + c, m - c, out_bf16, o);
   }
 }
 
@@ -444,7 +450,7 @@ struct LinearPlan {
 
 LinearPlan plan_linear(int n, int d, int m, bool mx) {
   LinearPlan P{};
-  P.rows = n <= (mx ? kRowsMx : kRowsBf);
+  P.rows = n <= kRowsMany;
   if (P.rows) return P;
   auto tiles = [&](int t) { return (long long)((n + t - 1) / t) * ((m + t - 1) / t); };
   P.tile = tiles(256) >= kLargeTiles ? 256 : 128;
@@ -453,7 +459,7 @@ LinearPlan plan_linear(int n, int d, int m, bool mx) {
   P.splits = 1;
   if (P.tile == 128) {
     const long long t = tiles(128);
-    while (P.splits < 8 && t * P.splits * 2 <= kSplitBlocks && P.steps / (P.splits * 2) >= 4) P.splits *= 2;
+    while (P.splits < 8 && t * P.splits * 2 <= kSplitBlocks && P.steps / (P.splits * 2) >= (mx ? 4 : 11)) P.splits *= 2;
   }
   P.per = (P.steps + P.splits - 1) / P.splits;
   P.splits = (P.steps + P.per - 1) / P.per;
@@ -531,9 +537,8 @@ hipError_t launch_many(const LinearArgs &a, hipStream_t st) {
   e = P.tile == 256 ? launch_gemm<MX, 256, 8>(p, st) : launch_gemm<MX, 128, 4>(p, st);
   if (e != hipSuccess || P.splits == 1) return e;
   const int mp = (a.m + 7) / 8 * 8;
-  const long long lanes = (long long)a.n * (mp / 4);
-  linear_sum_kernel<<<(int)std::min<long long>((lanes + 255) / 256, 2048), 256, 0, st>>>(
-      (const float *)(ws + P.part), P.splits, a.n, a.m, mp, a.bias, a.y, a.out_bf16);
+  linear_sum_kernel<<<dim3((mp / 8 + 255) / 256, std::min(a.n, 32768)), 256, 0, st>>>(
+      (const float *)(ws + P.part), P.splits, a.n, a.m, mp, a.bias, (char *)a.y, a.out_bf16);
   return hipGetLastError();
 }
 
