@@ -44,7 +44,7 @@ namespace {
 
 constexpr int kT = kFewMaxTokens;  // 16: the M of the MFMA
 constexpr int kWaves = 8, kThreads = kWaves * 64;
-constexpr int kInFlight = 4;  // chunks of weights in flight a wave
+constexpr int kInFlight = 2;  // chunks of weights in flight a wave
 constexpr int kFewLds = 160 * 1024;
 // Tries of a waiting output part (each at least a microsecond): seconds, where a
 // call takes microseconds.  Past it the part writes NaN.

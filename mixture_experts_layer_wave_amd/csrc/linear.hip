@@ -16,9 +16,9 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kRows = 16;  // the M of the MFMA
-constexpr int kRowsLds = 76 * 1024;  // x in LDS where it fits
+constexpr int kRowsLds = 160 * 1024 - kWaves * kExchange;  // x in LDS where it fits
 constexpr int kRowsMany = 16;  // rows above which the GEMM takes over
 constexpr int kLargeTiles = 200;  // 256 x 256 tiles from which they are taken
 constexpr int kSplitBlocks = 512;  // blocks up to which K is split
@@ -46,8 +46,7 @@ __global__ __launch_bounds__(kThreads) void linear_rows_kernel(LinearParams p) {
   using F = Form<WT>;
   constexpr int NF = F::kActBytes / 16, RC = kRowChunk<WT>, SL = (RC - 16) / 16;
   extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];
-  __shared__ __attribute__((aligned(16))) uint8_t s_ex[kWaves][kExchange];
-  __shared__ __attribute__((aligned(16))) float s_red[kWaves][64][4];
+  __shared__ __attribute__((aligned(16))) uint8_t s_ex[kWaves][kExchange];  // later the waves' sums
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int part = blockIdx.x % p.G, t0 = blockIdx.x / p.G * kRows, rows = min(kRows, p.n - t0);
@@ -108,11 +107,11 @@ __global__ __launch_bounds__(kThreads) void linear_rows_kernel(LinearParams p) {
           if (r < cnt && 4 * g + q < rows) put(p, t0 + 4 * g + q, c + r, v[q]);
       });
   if (KS == 1) return;
-  *(f32x4 *)s_red[wave][lane] = sum;
+  *(f32x4 *)(s_ex[wave] + lane * 16) = sum;
   __syncthreads();
   if (kp == 0 && segs > 0) {
     const int c = col(mine), cnt = col(mine + 1) - c;
-    for (int j = 1; j < KS; ++j) sum += *(const f32x4 *)s_red[wave + j][lane];
+    for (int j = 1; j < KS; ++j) sum += *(const f32x4 *)(s_ex[wave + j] + lane * 16);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       if (r < cnt && 4 * g + q < rows) put(p, t0 + 4 * g + q, c + r, sum[q]);
