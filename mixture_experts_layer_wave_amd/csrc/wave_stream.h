@@ -22,6 +22,7 @@ struct Form {
 };
 
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 struct __attribute__((packed, aligned(1))) u32_any {
   uint32_t v;
