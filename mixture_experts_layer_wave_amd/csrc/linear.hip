@@ -156,7 +156,7 @@ bool rows_fit(int n, int d) {
 //     scale is one byte a lane and step, straight from memory.
 //   MXFP4 rows: 256 elements, both operands in their stored form on the scaled MFMA.
 //     A step's scales are eight bytes a row, laid out step by step by a kernel in front
-//     (as stored they start at any byte); lane half h of slice s takes byte 2 s + h.
+//     (as stored they start at any byte); slice s of lane half h takes byte 4 h + s.
 struct GemmParams {
   const uint8_t *a, *b;      // [n] rows of rb bytes, [m] rows of d / 2
   const uint8_t *as, *bs;    // MX: [steps][np], [steps][mp] x 8 scales; else bs [m][d / 32]
@@ -193,6 +193,12 @@ __device__ __forceinline__ void store_columns8(char *y, size_t at, int left, boo
 
 constexpr int kRowGroup = 4;  // row tiles that blocks running together share
 
+// b a + c of 64 MXFP4 elements, byte S of each scale.
+template <int S>
+__device__ __forceinline__ f32x16 scaled(v8i b, v8i a, f32x16 c, uint32_t bs, uint32_t as) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 4, 4, S, (int)bs, S, (int)as);
+}
+
 template <bool MX, int BM, int BN, int NW>
 struct GemmTile {
   static constexpr int WN_ = NW / 2, WM = BM / 2, WN = BN / WN_, TM = WM / 32, TN = WN / 32;
@@ -200,11 +206,12 @@ struct GemmTile {
   static constexpr int A = BM * 128, B = BN * RB, S = MX ? (BM + BN) * 8 : 0;
   static constexpr int STAGE = A + B + S;
   static constexpr int PITCH = WN + 4;  // floats a row of a wave's epilogue piece
-  static constexpr int LDS = 2 * STAGE > NW * 32 * PITCH * 4 ? 2 * STAGE : NW * 32 * PITCH * 4;
+  static constexpr int PIECES = NW * 32 * PITCH * 4;  // the epilogue's: in a stage, if they fit
+  static constexpr int LDS = 2 * STAGE + (PIECES > STAGE ? PIECES : 0);
   static_assert(A / 1024 % NW == 0 && B / 1024 % NW == 0, "whole copies a wave");
 };
 
-template <bool MX, int BM, int BN, int NW>
+template <bool MX, int BM, int BN, int NW, bool MANY>
 __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
   using T = GemmTile<MX, BM, BN, NW>;
   using namespace gemm;
@@ -213,21 +220,14 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Block -> tile: an eighth of the list to each XCD; groups of kRowGroup row tiles,
   // column tile by column tile within a group.
-  const int total = p.rt * p.ct * p.splits, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-  int base = 0;
+  const int total = p.rt * p.ct * p.splits, xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
+  int base = 0, slot = blockIdx.x >> 3;
   for (int x = 0; x < xcd; ++x) base += (total - x + 7) >> 3;
-  if (slot >= (total - xcd + 7) >> 3) return;
-  const int item = base + slot, split = item % p.splits, L = item / p.splits;
-  const int grp = L / (kRowGroup * p.ct), within = L - grp * kRowGroup * p.ct;
-  const int gr = min(kRowGroup, p.rt - grp * kRowGroup);
-  const int row0 = (grp * kRowGroup + within % gr) * BM, col0 = within / gr * BN;
-  const int rows = min(BM, p.n - row0), cols = min(BN, p.m - col0);
-  const int k_lo = split * p.per, k_hi = min(p.steps, k_lo + p.per);
+  const int slots = (total - xcd + 7) >> 3;
+  if (slot >= slots) return;
 
   // Copies: run q of wave w is the 1 KB of rows 8 (NW q + w) .. + 7, lane l's chunk l % 8.
-  const __amdgpu_buffer_rsrc_t ra = rsrc(p.a + (size_t)row0 * p.rb, (uint32_t)rows * (uint32_t)p.rb);
   const uint32_t wb = (uint32_t)p.d / 2;  // bytes of a row of W
-  const __amdgpu_buffer_rsrc_t rbw = rsrc(p.b + (size_t)col0 * wb, (uint32_t)cols * wb);
   const int crow = wave * 8 + (lane >> 3), chunk = (lane & 7) ^ swz_key<128>(crow);
   static_assert(NW * 8 % 16 == 0, "the swizzle key repeats every 16 rows");
   const uint32_t off0 = (uint32_t)crow * (uint32_t)p.rb + chunk * 16, rstep = (uint32_t)(NW * 8) * (uint32_t)p.rb;
@@ -237,40 +237,50 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
   const int KB = p.d / 32;
   const uint8_t *sp[T::TN];
   uint8_t sc[T::TN];
+  int split, row0, col0, rows, cols, k_lo, k_hi;  // the tile whose copies are issued
+  __amdgpu_buffer_rsrc_t ra, rbw;
+  auto open = [&] {
+    const int item = base + min(slot, slots - 1), L = item / p.splits;
+    split = item % p.splits;
+    const int grp = L / (kRowGroup * p.ct), within = L - grp * kRowGroup * p.ct;
+    const int gr = min(kRowGroup, p.rt - grp * kRowGroup);
+    row0 = (grp * kRowGroup + within % gr) * BM;
+    col0 = within / gr * BN;
+    rows = min(BM, p.n - row0);
+    cols = min(BN, p.m - col0);
+    k_lo = split * p.per;
+    k_hi = slot < slots ? min(p.steps, k_lo + p.per) : 0;  // (behind the last tile: nothing)
+    ra = rsrc(p.a + (size_t)row0 * p.rb, (uint32_t)rows * (uint32_t)p.rb);
+    rbw = rsrc(p.b + (size_t)col0 * wb, (uint32_t)cols * wb);
+    if constexpr (!MX)
 #pragma unroll
-  for (int j = 0; j < T::TN; ++j) {
-    sp[j] = MX ? nullptr : p.bs + (size_t)(col0 + min(wn * T::WN + j * 32 + lr, cols - 1)) * KB;
-    sc[j] = 127;
-  }
+      for (int j = 0; j < T::TN; ++j)
+        sp[j] = p.bs + (size_t)(col0 + min(wn * T::WN + j * 32 + lr, cols - 1)) * KB;
+  };
   auto issue = [&](int kt, int st) {
     uint8_t *sa = smem + st * T::STAGE;
     const uint32_t k = (uint32_t)kt * 128u;
     const uint32_t out = (kt < k_hi && (int)k + chunk * 16 < p.rb) ? 0u : kOOB;
+    // (rows past the tile lie past the buffer's record count: zeros)
+    const uint32_t at = (off0 + k) | out;
 #pragma unroll
-    for (int q = 0; q < T::A / 1024 / NW; ++q) {
-      const bool in = crow + q * NW * 8 < rows;
-      dma16(ra, sa + (NW * q + wave) * 1024, in ? (off0 + q * rstep + k) | out : kOOB);
-    }
+    for (int q = 0; q < T::A / 1024 / NW; ++q) dma16(ra, sa + (NW * q + wave) * 1024, at + q * rstep);
     if constexpr (MX) {
 #pragma unroll
-      for (int q = 0; q < T::B / 1024 / NW; ++q) {
-        const bool in = crow + q * NW * 8 < cols;
-        dma16(rbw, sa + T::A + (NW * q + wave) * 1024, in ? (off0 + q * rstep + k) | out : kOOB);
-      }
+      for (int q = 0; q < T::B / 1024 / NW; ++q) dma16(rbw, sa + T::A + (NW * q + wave) * 1024, at + q * rstep);
     } else {
       static_assert(MX || T::B / 1024 == NW, "a copy of W a wave");
       const uint32_t kb = (uint32_t)kt * 32u + wchunk * 16;
       dma16(rbw, sa + T::A + wave * 1024, (kt < k_hi && wrow < cols && kb < wb) ? (uint32_t)wrow * wb + kb : kOOB);
     }
     if constexpr (MX) {
-      constexpr int RA = BM * 8 / 1024, RB = BN * 8 / 1024;  // copies of scales
-      const int kc = min(kt, p.steps - 1);
-      if (wave < RA) {
-        const __amdgpu_buffer_rsrc_t rs = rsrc(p.as + ((size_t)kc * p.np + row0) * 8, BM * 8);
-        dma16(rs, sa + T::A + T::B + wave * 1024, wave * 1024 + lane * 16);
-      } else if (wave < RA + RB) {
-        const __amdgpu_buffer_rsrc_t rs = rsrc(p.bs + ((size_t)kc * p.mp + col0) * 8, BN * 8);
-        dma16(rs, sa + T::A + T::B + wave * 1024, (wave - RA) * 1024 + lane * 16);
+      static_assert(BM == BN && BM * 8 / 256 % NW == 0, "whole copies of scales a wave");
+      const size_t kc = (size_t)min(kt, p.steps - 1);
+#pragma unroll
+      for (int q = 0; q < BM * 8 / 256 / NW; ++q) {
+        const int piece = (NW * q + wave) * 256;
+        dma4(rsrc(p.as + (kc * p.np + row0) * 8, BM * 8), sa + T::A + T::B + piece, piece + lane * 4);
+        dma4(rsrc(p.bs + (kc * p.mp + col0) * 8, BN * 8), sa + T::A + T::B + BM * 8 + piece, piece + lane * 4);
       }
     }
   };
@@ -281,115 +291,201 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
       for (int j = 0; j < T::TN; ++j) sc[j] = sp[j][min(2 * kt + lg, KB - 1)];
   };
   f32x16 acc[T::TM][T::TN];
-#pragma unroll
-  for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-    for (int j = 0; j < T::TN; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-  issue(k_lo, 0);
-  load_scales(k_lo);
-  for (int kt = k_lo; kt < k_hi; ++kt) {
-    const int st = (kt - k_lo) & 1;
-    wait_vmcnt<0>();
-    __syncthreads();
-    float scale[T::TN];
-    if constexpr (!MX)
-#pragma unroll
-      for (int j = 0; j < T::TN; ++j) scale[j] = e8m0_to_f32(2 * kt + lg < KB ? sc[j] : 127u);
-    if (kt + 1 < k_hi) issue(kt + 1, st ^ 1);
-    load_scales(kt + 1);
-    const uint8_t *sa = smem + st * T::STAGE, *sb = sa + T::A;
-    u32x2 as[T::TM], bs[T::TN];
-    u32x4 codes[T::TN];
+  // The loop is rotated by one slice against its barriers: behind the barrier that
+  // publishes a step a wave reads slice 0 of it and then multiplies the last slice of
+  // the step before, so that no wave stands at a barrier with nothing to multiply.
+  u32x4 a0[T::TM], b0[T::TN], a1[T::TM], b1[T::TN];
+  uint32_t as[T::TM], bs[T::TN], an[T::TM], bn[T::TN];  // MX: this step's scales, the next one's
+  u32x4 codes[T::TN];                                // not MX: this step's codes
+  float scale[T::TN];
+  auto read_step = [&](const uint8_t *sa) {
+    const uint8_t *sb = sa + T::A;
     if constexpr (MX) {
-      const uint8_t *ss = sb + T::B;
+      const uint8_t *pa = sb + T::B + ((wm * T::WM + lr) * 8 + lg * 4);
+      const uint8_t *pb = sb + T::B + ((BM + wn * T::WN + lr) * 8 + lg * 4);
 #pragma unroll
-      for (int i = 0; i < T::TM; ++i) as[i] = *(const u32x2 *)(ss + (wm * T::WM + i * 32 + lr) * 8);
+      for (int i = 0; i < T::TM; ++i) an[i] = *(const uint32_t *)(pa + i * 32 * 8);
 #pragma unroll
-      for (int j = 0; j < T::TN; ++j) bs[j] = *(const u32x2 *)(ss + (BM + wn * T::WN + j * 32 + lr) * 8);
-#pragma unroll
-      for (int i = 0; i < T::TM; ++i) as[i] = u32x2{as[i].x >> (8 * lg), as[i].y >> (8 * lg)};
-#pragma unroll
-      for (int j = 0; j < T::TN; ++j) bs[j] = u32x2{bs[j].x >> (8 * lg), bs[j].y >> (8 * lg)};
+      for (int j = 0; j < T::TN; ++j) bn[j] = *(const uint32_t *)(pb + j * 32 * 8);
     } else {
 #pragma unroll
       for (int j = 0; j < T::TN; ++j) codes[j] = *(const u32x4 *)(sb + swz<32>(wn * T::WN + j * 32 + lr, lg));
     }
+  };
+  auto begin_step = [&] {
+    if constexpr (MX) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      u32x4 af[T::TM], bf[T::TN];
-      const int ch = MX ? 2 * s + lg : 4 * lg + s;
+      for (int i = 0; i < T::TM; ++i) as[i] = an[i];
 #pragma unroll
-      for (int i = 0; i < T::TM; ++i) af[i] = *(const u32x4 *)(sa + swz<128>(wm * T::WM + i * 32 + lr, ch));
+      for (int j = 0; j < T::TN; ++j) bs[j] = bn[j];
+    }
+  };
+  auto convert = [&](int s, u32x4 *bf) {
+    if constexpr (!MX)
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j)
+        bf[j] = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 3))};
+  };
+  // (rows 32 apart have the same swizzle)
+  const int la = swz<128>(wm * T::WM + lr, MX ? lg : 4 * lg), lb = T::A + swz<128>(wn * T::WN + lr, lg);
+  auto read_slice = [&](const uint8_t *sa, int s, u32x4 *af, u32x4 *bf) {
+    const int flip = (MX ? 2 * s : s) << 4;  // from slice 0's chunk to slice s's
+    const uint8_t *pa = sa + (la ^ flip), *pb = sa + (lb ^ flip);
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) af[i] = *(const u32x4 *)(pa + i * 32 * 128);
+    if constexpr (MX)
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) bf[j] = *(const u32x4 *)(pb + j * 32 * 128);
+  };
+  auto multiply_slice = [&](int s, const u32x4 *af, const u32x4 *bf) {
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i)
 #pragma unroll
       for (int j = 0; j < T::TN; ++j) {
-        if constexpr (MX)
-          bf[j] = *(const u32x4 *)(sb + swz<128>(wn * T::WN + j * 32 + lr, ch));
-        else
-          bf[j] = u32x4{
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 0)),
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 1)),
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 2)),
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 3))};
-      }
-#pragma unroll
-      for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) {
-          if constexpr (MX) {
-            const v8i bv = {(int)bf[j].x, (int)bf[j].y, (int)bf[j].z, (int)bf[j].w, 0, 0, 0, 0};
-            const v8i av = {(int)af[i].x, (int)af[i].y, (int)af[i].z, (int)af[i].w, 0, 0, 0, 0};
-            if (s & 1)
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bv, av, acc[i][j], 4, 4, 2, (int)bs[j][s >> 1],
-                                                                          2, (int)as[i][s >> 1]);
-            else
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bv, av, acc[i][j], 4, 4, 0, (int)bs[j][s >> 1],
-                                                                          0, (int)as[i][s >> 1]);
-          } else {
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bf[j]),
-                                                                __builtin_bit_cast(bf16x8, af[i]), acc[i][j], 0, 0, 0);
-          }
+        if constexpr (MX) {
+          const v8i bv = {(int)bf[j].x, (int)bf[j].y, (int)bf[j].z, (int)bf[j].w, 0, 0, 0, 0};
+          const v8i av = {(int)af[i].x, (int)af[i].y, (int)af[i].z, (int)af[i].w, 0, 0, 0, 0};
+          acc[i][j] = s == 0   ? scaled<0>(bv, av, acc[i][j], bs[j], as[i])
+                      : s == 1 ? scaled<1>(bv, av, acc[i][j], bs[j], as[i])
+                      : s == 2 ? scaled<2>(bv, av, acc[i][j], bs[j], as[i])
+                               : scaled<3>(bv, av, acc[i][j], bs[j], as[i]);
+        } else {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bf[j]),
+                                                              __builtin_bit_cast(bf16x8, af[i]), acc[i][j], 0, 0, 0);
         }
-    }
-  }
-  __syncthreads();
-  // Epilogue: 32 rows at a time through the wave's own piece of LDS, so that stores
-  // take whole rows of it, eight columns a lane (y's rows start at any element).
-  float *piece = (float *)smem + wave * 32 * T::PITCH;
-  const int c0 = col0 + wn * T::WN;
-  const bool plane = p.splits > 1;
-  const int pitch = plane ? (p.m + 7) / 8 * 8 : p.m, width = plane ? pitch : p.m;
-  char *out = (char *)p.y + (plane ? (size_t)split * p.n * pitch * 4 : 0);
-  const bool half = p.out_bf16 && !plane;
-  constexpr int LPR = T::WN / 8, RPI = 64 / LPR;  // lanes a row, rows an instruction
-  const int cl = lane % LPR * 8, c = c0 + cl;
-  float bv[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) bv[e] = p.bias && !plane && c + e < p.m ? p.bias[c + e] : 0.f;
-#pragma unroll
-  for (int i = 0; i < T::TM; ++i) {
-#pragma unroll
-    for (int j = 0; j < T::TN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(f32x4 *)(piece + lr * T::PITCH + j * 32 + q * 8 + lg * 4) =
-            f32x4{acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
-    const int r0 = wm * T::WM + i * 32;
-#pragma unroll
-    for (int v = 0; v < 32 / RPI; ++v) {
-      const int r = v * RPI + lane / LPR;
-      const f32x4 x0 = *(const f32x4 *)(piece + r * T::PITCH + cl), x1 = *(const f32x4 *)(piece + r * T::PITCH + cl + 4);
-      if (r0 + r < rows) {
-        float o[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = x0[e] + bv[e], o[4 + e] = x1[e] + bv[4 + e];
-        store_columns8(out, (size_t)(row0 + r0 + r) * pitch + c, width - c, half, o);
       }
+  };
+  constexpr int NM = T::TM * T::TN, NR = MX ? T::TM + T::TN : T::TM;  // products and reads of a slice
+  // Slices 0 .. 2 of a step: each reads the next one's operands while it multiplies.
+  auto slices = [&](const uint8_t *sa) {
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      u32x4 *ac = s & 1 ? a1 : a0, *bc = s & 1 ? b1 : b0, *ax = s & 1 ? a0 : a1, *bx = s & 1 ? b0 : b1;
+      read_slice(sa, s + 1, ax, bx);
+      convert(s + 1, bx);
+      multiply_slice(s, ac, bc);
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (i < NR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_wave_barrier();  // the piece is read before the next rows go there
+  };
+  auto take_scales = [&](int kt) {
+    if constexpr (!MX)
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) scale[j] = e8m0_to_f32(2 * kt + lg < KB ? sc[j] : 127u);
+  };
+  // MANY: a block's tiles, one behind the other; the first copies of the next one are
+  // issued in front of the epilogue's stores.
+  constexpr int LPR = T::WN / 8, RPI = 64 / LPR;  // lanes a row, rows an instruction of the epilogue
+  constexpr int kStores = T::TM * (32 / RPI);     // instructions of a wave's 16-byte stores, at least
+  open();
+  issue(k_lo, 0);
+  load_scales(k_lo);
+  int first = 0;         // the stage of the tile's first step
+  bool counted = false;  // kStores or more stores of this wave lie behind its copies
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    if (counted)
+      wait_vmcnt<kStores>();
+    else
+      wait_vmcnt<0>();
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+    __builtin_amdgcn_s_barrier();  // (no fence: it would wait for the stores)
+    take_scales(k_lo);
+    read_step(smem + first * T::STAGE);
+    read_slice(smem + first * T::STAGE, 0, a0, b0);
+    issue(k_lo + 1, first ^ 1);
+    load_scales(k_lo + 1);
+    begin_step();
+    convert(0, b0);
+    __builtin_amdgcn_sched_barrier(0);
+    int st = first;
+    for (int kt = k_lo; kt + 1 < k_hi; ++kt, st ^= 1) {
+      slices(smem + st * T::STAGE);
+      // the next stage's copies are there, and every wave has the last of this one
+      wait_vmcnt<0>();
+      __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // lgkmcnt(0)
+      __syncthreads();
+      const uint8_t *sa = smem + (st ^ 1) * T::STAGE;
+      read_step(sa);
+      read_slice(sa, 0, a0, b0);
+      multiply_slice(3, a1, b1);
+      __builtin_amdgcn_sched_group_barrier(0x100, NR + (MX ? T::TM + T::TN : T::TN), 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, NM, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      take_scales(kt + 1);
+      issue(kt + 2, st);
+      load_scales(kt + 2);
+      begin_step();
+      convert(0, b0);
+    }
+    slices(smem + st * T::STAGE);
+    multiply_slice(3, a1, b1);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<0>();  // (the copies past the end, which nobody reads)
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+    __syncthreads();
+    const int er0 = row0, erows = rows;
+    const bool whole = rows == BM && cols == BN, plane = p.splits > 1, half = p.out_bf16 && !plane;
+    const int pitch = plane ? (p.m + 7) / 8 * 8 : p.m, width = plane ? pitch : p.m;
+    char *out = (char *)p.y + (plane ? (size_t)split * p.n * pitch * 4 : 0);
+    // (the lane is read afresh, so that nothing of the epilogue stays live in the loop)
+    const int el = __lane_id(), cl = el % LPR * 8, c = col0 + wn * T::WN + cl;
+    const __amdgpu_buffer_rsrc_t rbias = rsrc(p.bias, p.bias && !plane ? (uint32_t)p.m * 4 : 0);
+    float bv[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      bv[e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rbias, (uint32_t)(c + e) * 4, 0, 0));
+    // (no branch before the products are stored: they would sink behind it, and their
+    // operands stay in registers)
+    if constexpr (MANY) {
+      slot += stride;
+      open();
+      issue(k_lo, st ^ 1);
+      load_scales(k_lo);
+    }
+    // Epilogue: 32 rows at a time through the wave's own piece of LDS, so that stores
+    // take whole rows of it, eight columns a lane (y's rows start at any element).
+    float *piece = (float *)(smem + (T::PIECES > T::STAGE ? 2 : st) * T::STAGE) + wave * 32 * T::PITCH;
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) {
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(f32x4 *)(piece + el % 32 * T::PITCH + j * 32 + q * 8 + el / 32 * 4) =
+              f32x4{acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+      const int r0 = wm * T::WM + i * 32;
+#pragma unroll
+      for (int v = 0; v < 32 / RPI; ++v) {
+        const int r = v * RPI + el / LPR;
+        const f32x4 x0 = *(const f32x4 *)(piece + r * T::PITCH + cl), x1 = *(const f32x4 *)(piece + r * T::PITCH + cl + 4);
+        if (r0 + r < erows) {
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = x0[e] + bv[e], o[4 + e] = x1[e] + bv[4 + e];
+          store_columns8(out, (size_t)(er0 + r0 + r) * pitch + c, width - c, half, o);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();  // the piece is read before the next rows go there
+    }
+    if (!MANY || slot >= slots) break;
+    first = st ^ 1;
+    counted = whole;
   }
+  if constexpr (MANY) wait_vmcnt<0>();  // (no copy into LDS outlives its block)
 }
 
 // y = bias + the planes' sum, in plane order: blocks of 8 x 256 columns of a row.
@@ -416,8 +512,8 @@ __global__ __launch_bounds__(256) void linear_sum_kernel(const float *__restrict
   }
 }
 
-// Scales [rows][KB] of two matrices as [steps][padded rows][8], 127 (one) where there
-// are none.
+// Scales [rows][KB] of two matrices as [steps][padded rows][8], a step's even blocks
+// before its odd ones, 127 (one) where there are none.
 __global__ __launch_bounds__(256) void linear_scales_kernel(const uint8_t *__restrict__ xs, uint2 *__restrict__ xo, int n,
                                                             int np, const uint8_t *__restrict__ ws,
                                                             uint2 *__restrict__ wo, int m, int mp, int KB, int steps) {
@@ -432,8 +528,8 @@ __global__ __launch_bounds__(256) void linear_scales_kernel(const uint8_t *__res
     uint32_t lo = 0, hi = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      lo |= (in && kt * 8 + j < KB ? s[j] : 127u) << (8 * j);
-      hi |= (in && kt * 8 + 4 + j < KB ? s[4 + j] : 127u) << (8 * j);
+      lo |= (in && kt * 8 + 2 * j < KB ? s[2 * j] : 127u) << (8 * j);
+      hi |= (in && kt * 8 + 2 * j + 1 < KB ? s[2 * j + 1] : 127u) << (8 * j);
     }
     (first ? xo : wo)[(size_t)kt * (first ? np : mp) + row] = uint2{lo, hi};
   }
@@ -482,7 +578,8 @@ LinearPlan plan_linear(int n, int d, int m, bool mx) {
 template <bool MX, int BM, int NW>
 hipError_t launch_gemm(const GemmParams &p, hipStream_t st) {
   using T = GemmTile<MX, BM, BM, NW>;
-  auto kern = linear_gemm_kernel<MX, BM, BM, NW>;
+  constexpr bool kMany = BM == 256;  // a block a CU, which takes several tiles
+  auto kern = linear_gemm_kernel<MX, BM, BM, NW, kMany>;
   if (T::LDS > 64 * 1024) {
     static std::atomic<uint64_t> attr_done{0};
     int dev = 0;
@@ -496,7 +593,8 @@ hipError_t launch_gemm(const GemmParams &p, hipStream_t st) {
     }
   }
   const int total = p.rt * p.ct * p.splits;
-  kern<<<(total + 7) / 8 * 8, NW * 64, T::LDS, st>>>(p);
+  const int blocks = (total + 7) / 8 * 8, most = kMany ? std::max(8, cu_count() / 8 * 8) : blocks;
+  kern<<<std::min(blocks, most), NW * 64, T::LDS, st>>>(p);
   return hipGetLastError();
 }
 

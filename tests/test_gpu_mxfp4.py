@@ -177,6 +177,20 @@ def test_linear(act, n, d, m):
 
 
 @pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("n,d,m", [(4600, 288, 4500), (7000, 64, 4200), (300, 544, 70001), (4352, 512, 4096)])
+def test_linear_of_more_tiles_than_compute_units(act, n, d, m):
+    """Blocks that take several tiles: ragged and whole ones behind each other, of one K
+    step, of an odd and of an even number."""
+    for out, bias in (("bf16", True), ("f32", False)):
+        say(f"[mxfp4 linear] tiles in turn, {act} {n} x {d} -> {m}, {out}")
+        y, x64, w64, b64 = _product(n, d, m, act, out, bias)
+        for r in range(0, n, 1024):
+            x = x64[r:r + 1024]
+            ref = x @ w64.T + b64
+            assert (np.abs(_f64(y[r:r + 1024]) - ref) <= _tolerance(ref, x, w64, b64, out)).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
 @pytest.mark.parametrize("n", [3, 70, 300])
 def test_linear_keeps_nan_and_infinities_where_they_are(act, n):
     """A NaN block of W spoils its output column, one of x its row, no other."""
