@@ -21,7 +21,9 @@ constexpr int kRows = 16;  // the M of the MFMA
 constexpr int kRowsLds = 160 * 1024 - kWaves * kExchange;  // x in LDS where it fits
 constexpr int kRowsMany = 16;  // rows above which the GEMM takes over
 constexpr int kLargeTiles = 200;  // 256 x 256 tiles from which they are taken
-constexpr int kSplitBlocks = 512;  // blocks up to which K is split
+constexpr int kBlocks = 256;       // blocks of one round: the device's CUs
+constexpr int kSplitSteps = 11;    // K steps that a plane has at least
+constexpr int kShort = 48;         // K steps up to which three groups share a tile
 
 struct LinearParams {
   const uint8_t *x, *xs, *w, *ws;
@@ -147,16 +149,28 @@ bool rows_fit(int n, int d) {
 }
 
 // ---- many rows --------------------------------------------------------------------
+// y = x W^T with x's rows as the second and W's as the first operand of 32 x 32 MFMAs.
 // A block takes BM rows of x by BN rows of W through two LDS stages filled by direct
-// copies, 16-byte chunks swizzled by row; the MFMA takes W's rows as its first operand.
-// A step is 128 bytes of a row of x, in four slices:
-//   bf16 rows (MX = false): 64 elements.  W's codes lie in LDS, 32 bytes a row; lane
-//     half h of a wave converts block h of the step (v_cvt_scalef32_pk_bf16_fp4), whose
-//     elements 8 s .. are slice s's, and takes x's elements 32 h + 8 s .. to match.  The
-//     scale is one byte a lane and step, straight from memory.
+// copies, 16-byte chunks swizzled by row.  A step is 128 bytes of a row of x, in four
+// slices:
+//   bf16 rows (MX = false): 64 elements.  Lane half h of a wave converts W's block h of
+//     the step (v_cvt_scalef32_pk_bf16_fp4), whose elements 8 s .. are slice s's, and
+//     takes x's elements 32 h + 8 s .. to match.  W's codes of a step are 32 bytes a row;
+//     they come four steps at a time, a quarter of the rows with each step: copies of
+//     whole 128 bytes (32 at a time 8192 x 4096 -> 14336 took 831 us, so 821).  The scale
+//     is one byte a lane and step, straight from memory.
 //   MXFP4 rows: 256 elements, both operands in their stored form on the scaled MFMA.
 //     A step's scales are eight bytes a row, laid out step by step by a kernel in front
 //     (as stored they start at any byte); slice s of lane half h takes byte 4 h + s.
+// With 256 x 256 tiles a block takes several, one behind the other, and the next one's
+// first copies are under way during the stores (8192 x 4096 -> 14336 829 -> 809 us, MXFP4
+// rows 294 -> 286).
+// What bounds it: 8192 x 4096 -> 14336 takes 801 to 821 us (1.17 to 1.20 PFLOP/s) with bf16
+// rows, where a large bf16 product of the vendor's library takes 738 and a loop of MFMAs on registers
+// reaches 2.28; with MXFP4 rows 285 us (3.4 PFLOP/s), of which the scales take 5, the
+// stores about 50, and the loop runs at 4.6 of 9.5 PFLOP/s.  Neither a third and fourth stage, nor four
+// waves of 128 x 128 (a third fewer LDS reads), nor the rotation below changed the loop's
+// rate.
 struct GemmParams {
   const uint8_t *a, *b;      // [n] rows of rb bytes, [m] rows of d / 2
   const uint8_t *as, *bs;    // MX: [steps][np], [steps][mp] x 8 scales; else bs [m][d / 32]
@@ -199,25 +213,36 @@ __device__ __forceinline__ f32x16 scaled(v8i b, v8i a, f32x16 c, uint32_t bs, ui
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 4, 4, S, (int)bs, S, (int)as);
 }
 
-template <bool MX, int BM, int BN, int NW>
+template <bool MX, int BM, int BN, int NW, int KG, bool MANY>
 struct GemmTile {
   static constexpr int WN_ = NW / 2, WM = BM / 2, WN = BN / WN_, TM = WM / 32, TN = WN / 32;
-  static constexpr int RB = MX ? 128 : 32;  // bytes of a row of W in a step
-  static constexpr int A = BM * 128, B = BN * RB, S = MX ? (BM + BN) * 8 : 0;
-  static constexpr int STAGE = A + B + S;
-  static constexpr int PITCH = WN + 4;  // floats a row of a wave's epilogue piece
-  static constexpr int PIECES = NW * 32 * PITCH * 4;  // the epilogue's: in a stage, if they fit
-  static constexpr int LDS = 2 * STAGE + (PIECES > STAGE ? PIECES : 0);
+  // a stage: x's rows, and with MX W's rows and the scales; else W's rows lie four steps
+  // at a time in two buffers of their own behind the two stages
+  static constexpr int A = BM * 128, B = BN * 128, S = MX ? (BM + BN) * 8 : 0;
+  static constexpr int STAGE = A + (MX ? B + S : 0), W = 2 * STAGE;
+  // the epilogue's pieces of 32 x 64, a wave each: over the stages; with MANY in what the
+  // next tile's first copies leave free: with MX stage 1, else stage 1 and W's buffer 1.
+  // Rows 16 bytes apart from each other's banks: by their pitch, or where there is no
+  // room for that by a swizzle.
+  static constexpr int PITCH = MX ? 272 : 256, PIECE = 32 * PITCH, PIECES = NW * PIECE;
+  static constexpr int ALL = 2 * STAGE + (MX ? 0 : 2 * B), LDS = KG * ALL;
+  static_assert(WN % 64 == 0 && (!MANY ? PIECES <= ALL : MX ? PIECES <= STAGE : PIECES / 2 <= A && PIECES / 2 <= B),
+                "the pieces fit");
+  __device__ static int at(int row, int chunk) { return row * PITCH + ((MX ? chunk : chunk ^ (row & 15)) << 4); }
   static_assert(A / 1024 % NW == 0 && B / 1024 % NW == 0, "whole copies a wave");
 };
 
-template <bool MX, int BM, int BN, int NW, bool MANY>
-__global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
-  using T = GemmTile<MX, BM, BN, NW>;
+// KG: groups of NW waves in a block, each with stages of its own and every KG-th part of
+// the block's K range; the groups' products meet in LDS in front of the stores.
+template <bool MX, int BM, int BN, int NW, int KG, bool MANY>
+__global__ __launch_bounds__(NW * KG * 64, 1) void linear_gemm_kernel(GemmParams p) {
+  using T = GemmTile<MX, BM, BN, NW, KG, MANY>;
+  static_assert(KG == 1 || !MANY, "groups: a tile a block");
   using namespace gemm;
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  extern __shared__ __attribute__((aligned(16))) uint8_t all_smem[];
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lg = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int id = __builtin_amdgcn_readfirstlane(tid >> 6), wave = id % NW, group = id / NW;
+  uint8_t *smem = all_smem + group * T::ALL;
   // Block -> tile: an eighth of the list to each XCD; groups of kRowGroup row tiles,
   // column tile by column tile within a group.
   const int total = p.rt * p.ct * p.splits, xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
@@ -230,8 +255,8 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
   const uint32_t wb = (uint32_t)p.d / 2;  // bytes of a row of W
   const int crow = wave * 8 + (lane >> 3), chunk = (lane & 7) ^ swz_key<128>(crow);
   static_assert(NW * 8 % 16 == 0, "the swizzle key repeats every 16 rows");
+  static_assert(T::B / 4096 % NW == 0, "whole copies of a quarter of W's rows a wave");
   const uint32_t off0 = (uint32_t)crow * (uint32_t)p.rb + chunk * 16, rstep = (uint32_t)(NW * 8) * (uint32_t)p.rb;
-  const int wrow = wave * 32 + (lane >> 1), wchunk = (lane & 1) ^ swz_key<32>(wrow);  // not MX: 32 rows a copy
   const int wm = wave / T::WN_, wn = wave % T::WN_;
   // not MX: this lane's scales, of the blocks 2 kt + lg
   const int KB = p.d / 32;
@@ -248,7 +273,7 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
     col0 = within / gr * BN;
     rows = min(BM, p.n - row0);
     cols = min(BN, p.m - col0);
-    k_lo = split * p.per;
+    k_lo = (split * KG + group) * p.per;
     k_hi = slot < slots ? min(p.steps, k_lo + p.per) : 0;  // (behind the last tile: nothing)
     ra = rsrc(p.a + (size_t)row0 * p.rb, (uint32_t)rows * (uint32_t)p.rb);
     rbw = rsrc(p.b + (size_t)col0 * wb, (uint32_t)cols * wb);
@@ -268,23 +293,30 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
     if constexpr (MX) {
 #pragma unroll
       for (int q = 0; q < T::B / 1024 / NW; ++q) dma16(rbw, sa + T::A + (NW * q + wave) * 1024, at + q * rstep);
-    } else {
-      static_assert(MX || T::B / 1024 == NW, "a copy of W a wave");
-      const uint32_t kb = (uint32_t)kt * 32u + wchunk * 16;
-      dma16(rbw, sa + T::A + wave * 1024, (kt < k_hi && wrow < cols && kb < wb) ? (uint32_t)wrow * wb + kb : kOOB);
     }
     if constexpr (MX) {
-      static_assert(BM == BN && BM * 8 / 256 % NW == 0, "whole copies of scales a wave");
+      static_assert(BM * 8 / 256 % NW == 0 && BN * 8 / 256 % NW == 0, "whole copies of scales a wave");
       const size_t kc = (size_t)min(kt, p.steps - 1);
 #pragma unroll
-      for (int q = 0; q < BM * 8 / 256 / NW; ++q) {
-        const int piece = (NW * q + wave) * 256;
-        dma4(rsrc(p.as + (kc * p.np + row0) * 8, BM * 8), sa + T::A + T::B + piece, piece + lane * 4);
-        dma4(rsrc(p.bs + (kc * p.mp + col0) * 8, BN * 8), sa + T::A + T::B + BM * 8 + piece, piece + lane * 4);
-      }
+      for (int q = 0; q < BM * 8 / 256 / NW; ++q)
+        dma4(rsrc(p.as + (kc * p.np + row0) * 8, BM * 8), sa + T::A + T::B + (NW * q + wave) * 256,
+             (NW * q + wave) * 256 + lane * 4);
+#pragma unroll
+      for (int q = 0; q < BN * 8 / 256 / NW; ++q)
+        dma4(rsrc(p.bs + (kc * p.mp + col0) * 8, BN * 8), sa + T::A + T::B + BM * 8 + (NW * q + wave) * 256,
+             (NW * q + wave) * 256 + lane * 4);
     }
   };
 
+  // not MX: a quarter of W's rows, four steps of them from step kt on
+  auto issue_w = [&](int kt, int quarter, int buf) {
+    const uint32_t k = (uint32_t)kt * 32u + chunk * 16;
+    const uint32_t at = (uint32_t)(quarter * (BN / 4) + crow) * wb + k;
+#pragma unroll
+    for (int q = 0; q < T::B / 4096 / NW; ++q)
+      dma16(rbw, smem + T::W + buf * T::B + quarter * (T::B / 4) + (NW * q + wave) * 1024,
+            (kt < k_hi && k < wb) ? at + (uint32_t)(NW * 8 * q) * wb : kOOB);
+  };
   auto load_scales = [&](int kt) {
     if constexpr (!MX)
 #pragma unroll
@@ -299,9 +331,10 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
   uint32_t as[T::TM], bs[T::TN], an[T::TM], bn[T::TN];  // MX: this step's scales, the next one's
   u32x4 codes[T::TN];                                // not MX: this step's codes
   float scale[T::TN];
-  auto read_step = [&](const uint8_t *sa) {
-    const uint8_t *sb = sa + T::A;
+  const int lw = swz<128>(wn * T::WN + lr, lg);  // (rows 32 apart have the same swizzle)
+  auto read_step = [&](const uint8_t *sa, int i) {  // the tile's step i
     if constexpr (MX) {
+      const uint8_t *sb = sa + T::A;
       const uint8_t *pa = sb + T::B + ((wm * T::WM + lr) * 8 + lg * 4);
       const uint8_t *pb = sb + T::B + ((BM + wn * T::WN + lr) * 8 + lg * 4);
 #pragma unroll
@@ -309,8 +342,9 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
 #pragma unroll
       for (int j = 0; j < T::TN; ++j) bn[j] = *(const uint32_t *)(pb + j * 32 * 8);
     } else {
+      const uint8_t *sb = smem + T::W + ((i >> 2) & 1) * T::B + (lw ^ ((2 * (i & 3)) << 4));
 #pragma unroll
-      for (int j = 0; j < T::TN; ++j) codes[j] = *(const u32x4 *)(sb + swz<32>(wn * T::WN + j * 32 + lr, lg));
+      for (int j = 0; j < T::TN; ++j) codes[j] = *(const u32x4 *)(sb + j * 32 * 128);
     }
   };
   auto begin_step = [&] {
@@ -330,8 +364,7 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 2)),
                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[j][s], scale[j], 3))};
   };
-  // (rows 32 apart have the same swizzle)
-  const int la = swz<128>(wm * T::WM + lr, MX ? lg : 4 * lg), lb = T::A + swz<128>(wn * T::WN + lr, lg);
+  const int la = swz<128>(wm * T::WM + lr, MX ? lg : 4 * lg), lb = T::A + lw;
   auto read_slice = [&](const uint8_t *sa, int s, u32x4 *af, u32x4 *bf) {
     const int flip = (MX ? 2 * s : s) << 4;  // from slice 0's chunk to slice s's
     const uint8_t *pa = sa + (la ^ flip), *pb = sa + (lb ^ flip);
@@ -383,12 +416,24 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
   };
   // MANY: a block's tiles, one behind the other; the first copies of the next one are
   // issued in front of the epilogue's stores.
-  constexpr int LPR = T::WN / 8, RPI = 64 / LPR;  // lanes a row, rows an instruction of the epilogue
-  constexpr int kStores = T::TM * (32 / RPI);     // instructions of a wave's 16-byte stores, at least
+  constexpr int LPR = 8, RPI = 8, J = T::WN / 64;  // lanes a row, rows an instruction, pieces of the epilogue
+  constexpr int kStores = J * T::TM * (32 / RPI);  // instructions of a wave's 16-byte stores, at least
+  auto start = [&] {  // a tile's first copies
+    issue(k_lo, 0);
+    if constexpr (!MX)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) issue_w(k_lo, q, 0);
+    load_scales(k_lo);
+  };
+  // What is loaded behind the barrier in front of step i: the next step, and a quarter of
+  // the next four steps' rows of W, whose buffer is free since step i - i % 4.
+  auto more = [&](int i) {
+    issue(k_lo + i + 1, (i + 1) & 1);
+    if constexpr (!MX) issue_w(k_lo + (i & ~3) + 4, i & 3, ((i >> 2) + 1) & 1);
+    load_scales(k_lo + i + 1);
+  };
   open();
-  issue(k_lo, 0);
-  load_scales(k_lo);
-  int first = 0;         // the stage of the tile's first step
+  start();
   bool counted = false;  // kStores or more stores of this wave lie behind its copies
   for (;;) {
 #pragma unroll
@@ -404,34 +449,32 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
     __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
     __builtin_amdgcn_s_barrier();  // (no fence: it would wait for the stores)
     take_scales(k_lo);
-    read_step(smem + first * T::STAGE);
-    read_slice(smem + first * T::STAGE, 0, a0, b0);
-    issue(k_lo + 1, first ^ 1);
-    load_scales(k_lo + 1);
+    read_step(smem, 0);
+    read_slice(smem, 0, a0, b0);
+    more(0);
     begin_step();
     convert(0, b0);
     __builtin_amdgcn_sched_barrier(0);
-    int st = first;
-    for (int kt = k_lo; kt + 1 < k_hi; ++kt, st ^= 1) {
-      slices(smem + st * T::STAGE);
-      // the next stage's copies are there, and every wave has the last of this one
+    const int steps = KG == 1 ? k_hi - k_lo : p.per;  // (groups meet at barriers: as many steps each)
+    for (int i = 0; i + 1 < steps; ++i) {
+      slices(smem + (i & 1) * T::STAGE);
+      // the next step's copies are there, and every wave has the last of this one
       wait_vmcnt<0>();
       __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // lgkmcnt(0)
       __syncthreads();
-      const uint8_t *sa = smem + (st ^ 1) * T::STAGE;
-      read_step(sa);
+      const uint8_t *sa = smem + ((i + 1) & 1) * T::STAGE;
+      read_step(sa, i + 1);
       read_slice(sa, 0, a0, b0);
       multiply_slice(3, a1, b1);
       __builtin_amdgcn_sched_group_barrier(0x100, NR + (MX ? T::TM + T::TN : T::TN), 0);
       __builtin_amdgcn_sched_group_barrier(0x008, NM, 0);
       __builtin_amdgcn_sched_barrier(0);
-      take_scales(kt + 1);
-      issue(kt + 2, st);
-      load_scales(kt + 2);
+      take_scales(k_lo + i + 1);
+      more(i + 1);
       begin_step();
       convert(0, b0);
     }
-    slices(smem + st * T::STAGE);
+    slices(smem + ((steps - 1) & 1) * T::STAGE);
     multiply_slice(3, a1, b1);
     __builtin_amdgcn_sched_barrier(0);
     wait_vmcnt<0>();  // (the copies past the end, which nobody reads)
@@ -442,47 +485,65 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_gemm_kernel(GemmParams p) {
     const int pitch = plane ? (p.m + 7) / 8 * 8 : p.m, width = plane ? pitch : p.m;
     char *out = (char *)p.y + (plane ? (size_t)split * p.n * pitch * 4 : 0);
     // (the lane is read afresh, so that nothing of the epilogue stays live in the loop)
-    const int el = __lane_id(), cl = el % LPR * 8, c = col0 + wn * T::WN + cl;
+    int el = __lane_id();
+    asm volatile("" : "+v"(el));
+    const int cl = el % LPR * 8, c = col0 + wn * T::WN + cl;
     const __amdgpu_buffer_rsrc_t rbias = rsrc(p.bias, p.bias && !plane ? (uint32_t)p.m * 4 : 0);
-    float bv[8];
+    float bv[J][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      bv[e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rbias, (uint32_t)(c + e) * 4, 0, 0));
+    for (int e = 0; e < 8 * J; ++e)
+      bv[e / 8][e % 8] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(rbias, (uint32_t)(c + e / 8 * 64 + e % 8) * 4, 0, 0));
     // (no branch before the products are stored: they would sink behind it, and their
     // operands stay in registers)
     if constexpr (MANY) {
       slot += stride;
       open();
-      issue(k_lo, st ^ 1);
-      load_scales(k_lo);
+      start();
     }
     // Epilogue: 32 rows at a time through the wave's own piece of LDS, so that stores
     // take whole rows of it, eight columns a lane (y's rows start at any element).
-    float *piece = (float *)(smem + (T::PIECES > T::STAGE ? 2 : st) * T::STAGE) + wave * 32 * T::PITCH;
+    uint8_t *piece = smem + (!MANY                 ? wave * T::PIECE
+                             : MX || wave < NW / 2 ? T::STAGE + wave * T::PIECE
+                                                   : T::W + T::B + (wave - NW / 2) * T::PIECE);
 #pragma unroll
-    for (int i = 0; i < T::TM; ++i) {
+    for (int part = 0; part < T::TM * J; ++part) {
+      const int i = part / J, jj = part % J;
 #pragma unroll
-      for (int j = 0; j < T::TN; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *(f32x4 *)(piece + el % 32 * T::PITCH + j * 32 + q * 8 + el / 32 * 4) =
-              f32x4{acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+        for (int q = 0; q < 4; ++q) {
+          const f32x16 &v = acc[i][2 * jj + j];
+          *(f32x4 *)(piece + T::at(el % 32, j * 8 + q * 2 + el / 32)) =
+              f32x4{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
+        }
       const int r0 = wm * T::WM + i * 32;
+      if constexpr (KG > 1) lds_barrier();
 #pragma unroll
       for (int v = 0; v < 32 / RPI; ++v) {
+        if (KG > 1 && v % KG != group) continue;
         const int r = v * RPI + el / LPR;
-        const f32x4 x0 = *(const f32x4 *)(piece + r * T::PITCH + cl), x1 = *(const f32x4 *)(piece + r * T::PITCH + cl + 4);
+        f32x4 x0 = {0.f, 0.f, 0.f, 0.f}, x1 = x0;
+        const uint8_t *from = piece - group * T::ALL;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+          x0 += *(const f32x4 *)(from + k * T::ALL + T::at(r, cl / 4));
+          x1 += *(const f32x4 *)(from + k * T::ALL + T::at(r, cl / 4 + 1));
+        }
         if (r0 + r < erows) {
           float o[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = x0[e] + bv[e], o[4 + e] = x1[e] + bv[4 + e];
-          store_columns8(out, (size_t)(er0 + r0 + r) * pitch + c, width - c, half, o);
+          for (int e = 0; e < 4; ++e) o[e] = x0[e] + bv[jj][e], o[4 + e] = x1[e] + bv[jj][4 + e];
+          store_columns8(out, (size_t)(er0 + r0 + r) * pitch + c + jj * 64, width - c - jj * 64, half, o);
         }
       }
-      __builtin_amdgcn_wave_barrier();  // the piece is read before the next rows go there
+      // the pieces are read before the next rows go there
+      if constexpr (KG > 1)
+        lds_barrier();
+      else
+        __builtin_amdgcn_wave_barrier();
     }
     if (!MANY || slot >= slots) break;
-    first = st ^ 1;
     counted = whole;
   }
   if constexpr (MANY) wait_vmcnt<0>();  // (no copy into LDS outlives its block)
@@ -535,11 +596,21 @@ __global__ __launch_bounds__(256) void linear_scales_kernel(const uint8_t *__res
   }
 }
 
-// How a product is run: by rows (streamed weights) or by a GEMM of BM = BN tiles with K
-// split into planes.
+// How a product is run: by rows (streamed weights) or by a GEMM.
+//   256 x 256 tiles where there are enough of them to fill the device.
+//   MXFP4 rows: two K groups a block, on 64 x 128 tiles while there is a CU for each and
+//     128 x 128 tiles then (us, one group of 128 x 128 with K in planes / two groups of
+//     64 / of 128: 333 x 2880 -> 5001 20.9 / 16.8 / 17.5, 512 x 4096 -> 4096 26.8 / 17.7 /
+//     19.0, 1024 x 4096 -> 4096 32.5 / 27.9 / 21.2); with more tiles than CUs one group
+//     (300 x 4096 -> 14336 26.1 / 38.6 / 30.2).
+//   bf16 rows: the same idea pays less, as a block's W needs more LDS: two groups of
+//     128 x 128 where they are one round of blocks (1024 x 4096 -> 4096 49.3 -> 45.1),
+//     three of 64 x 128 where those are and K is short (333 x 2880 -> 5001 25.3 -> 23.5,
+//     but 512 x 4096 -> 4096 34.4 -> 36.9); else one group of 128 x 128 and K in planes
+//     while that gives more blocks (17 x 4096 -> 4096 33 -> 16).
 struct LinearPlan {
   bool rows;
-  int tile, splits, per, steps, rb, np, mp;
+  int bm, bn, groups, splits, per, steps, rb, np, mp;
   size_t xs, ws, part, total;  // workspace: scales step by step; planes
 };
 
@@ -547,17 +618,29 @@ LinearPlan plan_linear(int n, int d, int m, bool mx) {
   LinearPlan P{};
   P.rows = n <= kRowsMany;
   if (P.rows) return P;
-  auto tiles = [&](int t) { return (long long)((n + t - 1) / t) * ((m + t - 1) / t); };
-  P.tile = tiles(256) >= kLargeTiles ? 256 : 128;
+  auto tiles = [&](int bm, int bn) { return (long long)((n + bm - 1) / bm) * ((m + bn - 1) / bn); };
   P.rb = mx ? d / 2 : d * 2;
   P.steps = (P.rb + 127) / 128;
   P.splits = 1;
-  if (P.tile == 128) {
-    const long long t = tiles(128);
-    while (P.splits < 8 && t * P.splits * 2 <= kSplitBlocks && P.steps / (P.splits * 2) >= (mx ? 4 : 11)) P.splits *= 2;
+  P.bm = P.bn = 256;
+  P.groups = 1;
+  const long long t64 = tiles(64, 128), t128 = tiles(128, 128);
+  auto one_round = [&](long long t) { return t > kBlocks / 2 && t <= kBlocks; };
+  if (tiles(256, 256) < kLargeTiles) {
+    P.bn = 128;
+    if (mx ? t64 <= kBlocks : one_round(t64) && P.steps <= kShort) {
+      P.bm = 64;
+      P.groups = mx ? 2 : 3;
+    } else {
+      P.bm = 128;
+      P.groups = (mx ? t128 <= kBlocks : one_round(t128)) ? 2 : 1;
+      if (!mx && P.groups == 1)
+        while (P.splits < 8 && t128 * P.splits * 2 <= 2 * kBlocks && P.steps / (P.splits * 2) >= kSplitSteps)
+          P.splits *= 2;
+    }
   }
-  P.per = (P.steps + P.splits - 1) / P.splits;
-  P.splits = (P.steps + P.per - 1) / P.per;
+  P.per = (P.steps + P.splits * P.groups - 1) / (P.splits * P.groups);
+  P.splits = (P.steps + P.per * P.groups - 1) / (P.per * P.groups);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -575,11 +658,11 @@ LinearPlan plan_linear(int n, int d, int m, bool mx) {
   return P;
 }
 
-template <bool MX, int BM, int NW>
+template <bool MX, int BM, int BN, int NW, int KG>
 hipError_t launch_gemm(const GemmParams &p, hipStream_t st) {
-  using T = GemmTile<MX, BM, BM, NW>;
-  constexpr bool kMany = BM == 256;  // a block a CU, which takes several tiles
-  auto kern = linear_gemm_kernel<MX, BM, BM, NW, kMany>;
+  constexpr bool MANY = BM == 256;  // a block a CU, which takes several tiles
+  using T = GemmTile<MX, BM, BN, NW, KG, MANY>;
+  auto kern = linear_gemm_kernel<MX, BM, BN, NW, KG, MANY>;
   if (T::LDS > 64 * 1024) {
     static std::atomic<uint64_t> attr_done{0};
     int dev = 0;
@@ -593,8 +676,8 @@ hipError_t launch_gemm(const GemmParams &p, hipStream_t st) {
     }
   }
   const int total = p.rt * p.ct * p.splits;
-  const int blocks = (total + 7) / 8 * 8, most = kMany ? std::max(8, cu_count() / 8 * 8) : blocks;
-  kern<<<std::min(blocks, most), NW * 64, T::LDS, st>>>(p);
+  const int blocks = (total + 7) / 8 * 8, most = MANY ? std::max(8, cu_count() / 8 * 8) : blocks;
+  kern<<<std::min(blocks, most), NW * KG * 64, T::LDS, st>>>(p);
   return hipGetLastError();
 }
 
@@ -612,8 +695,8 @@ hipError_t launch_many(const LinearArgs &a, hipStream_t st) {
   p.np = P.np;
   p.mp = P.mp;
   p.out_bf16 = a.out_bf16;
-  p.rt = (a.n + P.tile - 1) / P.tile;
-  p.ct = (a.m + P.tile - 1) / P.tile;
+  p.rt = (a.n + P.bm - 1) / P.bm;
+  p.ct = (a.m + P.bn - 1) / P.bn;
   p.splits = P.splits;
   p.per = P.per;
   p.y = P.splits > 1 ? (void *)(ws + P.part) : a.y;
@@ -631,7 +714,10 @@ hipError_t launch_many(const LinearArgs &a, hipStream_t st) {
     p.bs = a.w_s;
   }
   if (e != hipSuccess) return e;
-  e = P.tile == 256 ? launch_gemm<MX, 256, 8>(p, st) : launch_gemm<MX, 128, 4>(p, st);
+  e = P.bm == 256     ? launch_gemm<MX, 256, 256, 8, 1>(p, st)
+      : P.bm == 64    ? launch_gemm<MX, 64, 128, 2, MX ? 2 : 3>(p, st)
+      : P.groups == 2 ? launch_gemm<MX, 128, 128, 4, 2>(p, st)
+                      : launch_gemm<MX, 128, 128, 4, 1>(p, st);
   if (e != hipSuccess || P.splits == 1) return e;
   const int mp = (a.m + 7) / 8 * 8;
   linear_sum_kernel<<<dim3((mp / 8 + 255) / 256, std::min(a.n, 32768)), 256, 0, st>>>(

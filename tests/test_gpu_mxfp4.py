@@ -177,6 +177,19 @@ def test_linear(act, n, d, m):
 
 
 @pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("n,d,m", [(450, 672, 2600), (200, 32, 6500), (450, 3200, 2600), (1025, 416, 2100),
+                                   (1025, 64, 2100), (2100, 160, 2200), (2100, 32, 2200)])
+def test_linear_of_about_as_many_tiles_as_compute_units(act, n, d, m):
+    """Blocks whose groups of waves share K: steps that do not divide among them, fewer
+    steps than groups, and the next larger tiles."""
+    for out, bias in (("bf16", False), ("f32", True)):
+        say(f"[mxfp4 linear] shared K, {act} {n} x {d} -> {m}, {out}")
+        y, x64, w64, b64 = _product(n, d, m, act, out, bias)
+        ref = x64 @ w64.T + b64
+        assert (np.abs(_f64(y) - ref) <= _tolerance(ref, x64, w64, b64, out)).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
 @pytest.mark.parametrize("n,d,m", [(4600, 288, 4500), (7000, 64, 4200), (300, 544, 70001), (4352, 512, 4096)])
 def test_linear_of_more_tiles_than_compute_units(act, n, d, m):
     """Blocks that take several tiles: ragged and whole ones behind each other, of one K
