@@ -20,17 +20,26 @@
 // among it).  What a part computes depends on its ticket alone, so results do
 // not depend on who takes it.
 //
-// A wave streams weight rows straight into registers: one 16-byte load per lane
-// and step, 16 rows by 4 blocks (of 32 MXFP4, 8 bf16 or 4 float32 elements) to a
-// step, PF steps in flight.  The products run on 16x16 MFMAs with the tokens as
-// rows (M) and the 16 weight rows as columns.  Up: a tile is 8 rows of W1 and the
-// same 8 of W3, over all of K, so gate and value meet in one wave; every wave of
-// the grid takes an equal run of hidden columns.  Output: a workgroup takes an
-// equal run of output columns over all chosen experts, its waves equal runs of
-// (expert, K step); each wave adds an expert's product to its tokens' sums where
-// the expert's K range ends, and the waves' sums meet in LDS in a fixed order.
-// The hidden is multiplied by its combine weight before its one rounding, so
-// that the output needs no pass of its own.
+// The products (wave_stream.h) take the tokens as the 16 rows of a 16 x 16 MFMA and 16
+// weight rows as its columns.  Up: a tile is 8 rows of W1 and the same 8 of W3, over all
+// of K, so gate and value meet in one wave; a part is an equal run of the chosen experts'
+// hidden columns, whose tiles its waves take in turn.  Output: a part is an equal run of
+// output columns over all chosen experts, its waves equal runs of (expert, chunk of K);
+// each wave adds an expert's product to its tokens' sums where its run of the expert
+// ends, and the waves' sums meet in LDS in a fixed order.  The hidden is multiplied by
+// its combine weight before its one rounding, so that the output needs no pass of its
+// own.  It is handed over through memory by write-through stores and counters; with a
+// release fence a workgroup the hand-over took 15 us.
+//
+// What bounds it: reading the chosen experts, and about 17 us around that: two launches,
+// the logits (5.8 us), the top-k, the hand-over.  d = d_ff = 2880, 128 MXFP4 experts, k = 4
+// (us; a copy's rate takes 10, 20, 73 and 125 for the weights alone): 1 token 29.5, 2 40.5,
+// 8 102, 16 172, against 33, 45, 97 and 142 in the steps of moe_forward, whose products
+// share a weight conversion among more columns: the streaming here reaches 4.4 TB/s, and
+// 5.2 with the products left out.  d = 4096, d_ff = 14336, 8 bf16 experts, k = 2: 1 token 121 (moe_forward 183), 16 570 (588);
+// d = 1024, d_ff = 4096, k = 1: 24 (45) and 45 (63).
+// 8 waves with two chunks in flight each: 16 waves with one or two, or four chunks, cost
+// 1 to 4% at 1 and at 8 tokens.
 #include <algorithm>
 #include <atomic>
 
