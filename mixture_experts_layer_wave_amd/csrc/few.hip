@@ -429,45 +429,48 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
 constexpr int kRouterThreads = 512;
 
 // logits[t][e] = x_t . wg_e + bias_e, one workgroup per expert; the first also
-// clears the next kernel's counters.  Rows of bf16 in 16-byte pieces.
-template <bool BF>
+// clears the next kernel's counters.  N >= n tokens: the loads of all of them are
+// in flight together, rows past the last one as the last (waited for one by one,
+// 8 tokens of 2880 took 5.4 us and 16 of 1024 5.5).  Rows of bf16 in 16-byte pieces.
+template <bool BF, int N>
 __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(const void *__restrict__ x, const void *__restrict__ wg,
                                                          const float *__restrict__ bias, int n, int d, int E,
                                                          float *__restrict__ logits, int *__restrict__ count) {
-  __shared__ float s_sum[kRouterThreads / 64][kT];
+  __shared__ float s_sum[kRouterThreads / 64][N];
   const int e = blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   if (e == 0 && tid <= kDone) count[tid * kCountInts] = 0;
-  float acc[kT] = {};
+  float acc[N] = {};
   if constexpr (BF) {
     const u32x4 *wr = (const u32x4 *)((const uint16_t *)wg + (size_t)e * d);
     for (int c = tid; c < d / 8; c += kRouterThreads) {
       const u32x4 w = wr[c];
+      u32x4 v[N];
 #pragma unroll
-      for (int t = 0; t < kT; ++t)
-        if (t < n) {
-          const u32x4 v = ((const u32x4 *)((const uint16_t *)x + (size_t)t * d))[c];
+      for (int t = 0; t < N; ++t) v[t] = ((const u32x4 *)((const uint16_t *)x + (size_t)min(t, n - 1) * d))[c];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            acc[t] = fmaf(__uint_as_float(w[i] << 16), __uint_as_float(v[i] << 16), acc[t]);
-            acc[t] = fmaf(__uint_as_float(w[i] & 0xffff0000u), __uint_as_float(v[i] & 0xffff0000u), acc[t]);
-          }
+      for (int t = 0; t < N; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[t] = fmaf(__uint_as_float(w[i] << 16), __uint_as_float(v[t][i] << 16), acc[t]);
+          acc[t] = fmaf(__uint_as_float(w[i] & 0xffff0000u), __uint_as_float(v[t][i] & 0xffff0000u), acc[t]);
         }
     }
   } else {
     const float *wr = (const float *)wg + (size_t)e * d;
     for (int c = tid; c < d; c += kRouterThreads) {
       const float w = wr[c];
+      float v[N];
 #pragma unroll
-      for (int t = 0; t < kT; ++t)
-        if (t < n) acc[t] = fmaf(w, ((const float *)x)[(size_t)t * d + c], acc[t]);
+      for (int t = 0; t < N; ++t) v[t] = ((const float *)x)[(size_t)min(t, n - 1) * d + c];
+#pragma unroll
+      for (int t = 0; t < N; ++t) acc[t] = fmaf(w, v[t], acc[t]);
     }
   }
 #pragma unroll
-  for (int t = 0; t < kT; ++t)
-    if (t < n) {
-      const float v = group_sum(acc[t], 64);
-      if (lane == 0) s_sum[wave][t] = v;
-    }
+  for (int t = 0; t < N; ++t) {
+    const float v = group_sum(acc[t], 64);
+    if (lane == 0) s_sum[wave][t] = v;
+  }
   __syncthreads();
   if (tid < n) {
     float v = 0.f;
@@ -475,6 +478,15 @@ __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(const void *
     for (int j = 0; j < kRouterThreads / 64; ++j) v += s_sum[j][tid];
     logits[(size_t)tid * E + e] = bias ? v + bias[e] : v;
   }
+}
+
+template <bool BF>
+void launch_router(const FewArgs &a, float *logits, int *count, hipStream_t st) {
+  auto kern = a.n == 1   ? few_router_kernel<BF, 1>
+              : a.n <= 4 ? few_router_kernel<BF, 4>
+              : a.n <= 8 ? few_router_kernel<BF, 8>
+                         : few_router_kernel<BF, kT>;
+  kern<<<a.E, kRouterThreads, 0, st>>>(a.x, a.wg, a.bias, a.n, a.d, a.E, logits, count);
 }
 
 int up16(int v) { return (v + 15) / 16 * 16; }
@@ -585,9 +597,9 @@ hipError_t launch_forward_few(const FewArgs &a, hipStream_t st) {
   p.G = cu_count();
   float *logits = (float *)(base + P.logits);
   if (f32)
-    few_router_kernel<false><<<a.E, kRouterThreads, 0, st>>>(a.x, a.wg, a.bias, a.n, a.d, a.E, logits, p.count);
+    launch_router<false>(a, logits, p.count, st);
   else
-    few_router_kernel<true><<<a.E, kRouterThreads, 0, st>>>(a.x, a.wg, a.bias, a.n, a.d, a.E, logits, p.count);
+    launch_router<true>(a, logits, p.count, st);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const bool few = topk_per(a.E) == 2;

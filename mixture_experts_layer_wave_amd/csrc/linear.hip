@@ -454,7 +454,9 @@ __global__ __launch_bounds__(NW * KG * 64, 1) void linear_gemm_kernel(GemmParams
     else
       wait_vmcnt<0>();
     __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();  // (no fence: it would wait for the stores)
+    asm volatile("" ::: "memory");
     take_scales(k_lo);
     read_step(smem, 0);
     read_slice(smem, 0, a0, b0);
