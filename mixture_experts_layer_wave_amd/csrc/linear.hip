@@ -27,7 +27,7 @@ constexpr int kRows = 16;  // the M of the MFMA
 // of 4096 11.9 us, 16 rows 20.0).
 constexpr int kRowsLds = 160 * 1024 - kWaves * kExchange;
 constexpr int kRowsMany = 16;  // rows above which the GEMM takes over (see above)
-constexpr int kLargeTiles = 200;  // 256 x 256 tiles from which they are taken
+constexpr int kLargeTiles = 150;  // 256 x 256 tiles from which they are taken
 constexpr int kBlocks = 256;       // blocks of one round: the device's CUs
 constexpr int kSplitSteps = 11;    // K steps that a plane has at least
 constexpr int kShort = 48;         // K steps up to which three groups share a tile
@@ -606,7 +606,9 @@ __global__ __launch_bounds__(256) void linear_scales_kernel(const uint8_t *__res
 }
 
 // How a product is run: by rows (streamed weights) or by a GEMM.
-//   256 x 256 tiles where there are enough of them to fill the device.
+//   256 x 256 tiles where there are enough of them to fill most of the device (bf16 and
+//     MXFP4 rows, us, smaller tiles / these: 128 tiles 70 / 91 and 31.5 / 36.5, 160 tiles
+//     118 / 93 and 43.0 / 39.3, 192 tiles 121 / 104 and 48.3 / 44.7).
 //   MXFP4 rows: two K groups a block, on 64 x 128 tiles while there is a CU for each and
 //     128 x 128 tiles then (us, one group of 128 x 128 with K in planes / two groups of
 //     64 / of 128: 333 x 2880 -> 5001 20.9 / 16.8 / 17.5, 512 x 4096 -> 4096 26.8 / 17.7 /
