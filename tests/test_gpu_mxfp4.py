@@ -176,6 +176,77 @@ def test_linear(act, n, d, m):
         assert err.max() <= 1.0
 
 
+@pytest.mark.parametrize("act,n,d,m", [("bf16", 16, 3584, 50), ("bf16", 16, 4096, 300), ("bf16", 13, 5024, 33),
+                                       ("bf16", 15, 4096, 17), ("mxfp4", 16, 14848, 40), ("mxfp4", 16, 16384, 20)])
+def test_linear_rows_about_as_large_as_lds(act, n, d, m):
+    say(f"[mxfp4 linear] long rows, {act} {n} x {d} -> {m}")
+    y, x64, w64, b64 = _product(n, d, m, act, "f32", True)
+    ref = x64 @ w64.T + b64
+    assert (np.abs(_f64(y) - ref) <= _tolerance(ref, x64, w64, b64, "f32")).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("n,d,m", [(60, (1 << 24) - 32, 60), (16, (1 << 26) - 32, 15)])
+def test_linear_of_the_longest_rows(act, n, d, m):
+    """Matrices of close to 2^30 elements: x is 0 but in its first and last columns."""
+    torch, B = _torch()
+    say(f"[mxfp4 linear] far, {act} {n} x {d} -> {m}")
+    torch.manual_seed(n)
+    wq = torch.randint(0, 256, (m, d // 2), dtype=torch.uint8, device="cuda")
+    ws = torch.randint(120, 130, (m, d // 32), dtype=torch.uint8, device="cuda")
+
+    def both(t, per):
+        return torch.cat([t[:, :512 // per], t[:, -512 // per:]], 1).cpu().numpy()
+
+    w64 = oracle.decode_mxfp4(both(wq, 2), both(ws, 32))
+    xs = None
+    if act == "bf16":
+        x = torch.zeros((n, d), dtype=torch.bfloat16, device="cuda")
+        x[:, :512] = torch.randn((n, 512), device="cuda")
+        x[:, -512:] = torch.randn((n, 512), device="cuda")
+        x64 = _f64(torch.cat([x[:, :512], x[:, -512:]], 1))
+    else:
+        x = torch.zeros((n, d // 2), dtype=torch.uint8, device="cuda")
+        x[:, :256] = torch.randint(0, 256, (n, 256), dtype=torch.uint8, device="cuda")
+        x[:, -256:] = torch.randint(0, 256, (n, 256), dtype=torch.uint8, device="cuda")
+        xs = torch.full((n, d // 32), 125, dtype=torch.uint8, device="cuda")
+        x64 = oracle.decode_mxfp4(both(x, 2), both(xs, 32))
+    assert x64.shape[1] == w64.shape[1] == 1024
+    y = torch.full((n, m), 7.0, device="cuda")
+    nb = B.moe_mxfp4_linear_workspace_bytes(n, d, m, act)
+    work = torch.empty(nb + 16, dtype=torch.uint8, device="cuda")
+    B.moe_mxfp4_linear(n, d, m, x, xs, act, wq, ws, None, y, "f32", work, nb)
+    torch.cuda.synchronize()
+    ref = x64 @ w64.T
+    assert (np.abs(_f64(y) - ref) <= _tolerance(ref, x64, w64, np.zeros(m), "f32")).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+def test_linear_of_the_largest_output(act):
+    """Close to 2^30 outputs, thousands of tiles: rows from all over against 64 bits."""
+    torch, B = _torch()
+    n, d, m = 32700, 64, 32701
+    say(f"[mxfp4 linear] large output, {act} {n} x {d} -> {m}")
+    torch.manual_seed(2)
+    wq = torch.randint(0, 256, (m, d // 2), dtype=torch.uint8, device="cuda")
+    ws = torch.randint(120, 130, (m, d // 32), dtype=torch.uint8, device="cuda")
+    w64 = oracle.decode_mxfp4(wq.cpu().numpy(), ws.cpu().numpy())
+    x, xs = torch.randn((n, d), device="cuda").bfloat16(), None
+    if act == "mxfp4":
+        x, xs = (t.contiguous() for t in _encode(x, "bf16"))
+    y = torch.full((n * m + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    nb = B.moe_mxfp4_linear_workspace_bytes(n, d, m, act)
+    work = torch.empty(nb + 16, dtype=torch.uint8, device="cuda")
+    B.moe_mxfp4_linear(n, d, m, x, xs, act, wq, ws, None, y, "bf16", work, nb)
+    torch.cuda.synchronize()
+    assert (y[n * m:] == 7).all()
+    rows = [0, 1, 255, 256, 8191, 16385, 25000, n - 257, n - 2, n - 1]
+    x64 = oracle.decode_mxfp4(x[rows].cpu().numpy(), xs[rows].cpu().numpy()) if xs is not None else _f64(x[rows])
+    ref = x64 @ w64.T
+    got = _f64(y[: n * m].view(n, m)[rows])
+    assert (np.abs(got - ref) <= _tolerance(ref, x64, w64, np.zeros(m), "bf16")).all()
+
+
 @pytest.mark.parametrize("act", ["bf16", "mxfp4"])
 @pytest.mark.parametrize("n,d,m", [(450, 672, 2600), (200, 32, 6500), (450, 3200, 2600), (1025, 416, 2100),
                                    (1025, 64, 2100), (2100, 160, 2200), (2100, 32, 2200)])
