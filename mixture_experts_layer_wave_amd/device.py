@@ -182,8 +182,8 @@ class DecodeBlock:
 
         self.h, self.u, self.z = empty(n, d), empty(n, d), empty(n, d)
         self.idx, self.topw = empty(n, k, dtype=torch.int32), empty(n, k, dtype=torch.float32)
-        # 128 experts 2880 x 2880, top-4: 1 token 29.5 us here and 33 in moe_forward's steps,
-        # 4 tokens 63 and 66, 8 tokens 102 and 97, 16 tokens 172 and 142
+        # 128 experts 2880 x 2880, top-4: 1 token 29 us here and 33 in moe_forward's steps,
+        # 4 tokens 61 and 66, 8 tokens 99 and 97, 16 tokens 168 and 142
         self.layer, size = ((B.moe_forward_few, B.moe_forward_few_workspace_bytes) if n <= 4 else
                             (B.moe_forward, B.moe_workspace_bytes))
         need = size(self.shape, "mxfp4")
