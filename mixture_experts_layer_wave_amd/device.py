@@ -161,7 +161,8 @@ class DecodeBlock:
     [E][d][d_ff] and ``head`` [m][d] (or None) are bf16 or float32 device
     tensors, encoded once; ``wg`` [E][d] is bf16, ``bias`` float32 or None.
     ``post`` and ``pre`` are dicts (kind "layer" or "rms", weight, bias, eps)
-    or None.  :meth:`step` works on the block's own h and u [n][d] in place and
+    or None; without ``pre`` u is h itself.  :meth:`step` works on the block's
+    own h and u [n][d] in place, returns the logits or, without a head, u, and
     neither allocates nor synchronises, so it can be captured in a HIP graph.
     """
 
@@ -180,7 +181,8 @@ class DecodeBlock:
         def empty(*shape, dtype=torch.bfloat16):
             return torch.empty(shape, dtype=dtype, device=dev)
 
-        self.h, self.u, self.z = empty(n, d), empty(n, d), empty(n, d)
+        self.h, self.z = empty(n, d), empty(n, d)
+        self.u = empty(n, d) if pre else self.h
         self.idx, self.topw = empty(n, k, dtype=torch.int32), empty(n, k, dtype=torch.float32)
         # 128 experts 2880 x 2880, top-4: 1 token 29 us here and 33 in moe_forward's steps,
         # 4 tokens 61 and 66, 8 tokens 99 and 97, 16 tokens 168 and 142
@@ -196,11 +198,12 @@ class DecodeBlock:
 
     def step(self, stream=None):
         nb = self.ws.numel()
-        self.layer(self.shape, self.u, "bf16", self.wg, self.bias, self.weights, self.z, "bf16", self.idx,
+        u = self.u if self.pre else self.h
+        self.layer(self.shape, u, "bf16", self.wg, self.bias, self.weights, self.z, "bf16", self.idx,
                    self.topw, self.ws, nb, stream)
         B.moe_block_norm(self.n, self.d, self.h, self.z, "bf16", self.scale, self.gate, self.post, self.pre,
-                         self.h, self.u if self.pre else None, None, stream)
+                         self.h, u if self.pre else None, None, stream)
         if self.head:
-            B.moe_mxfp4_linear(self.n, self.d, self.m, self.u if self.pre else self.h, None, "bf16", *self.head,
-                               None, self.logits, "f32", self.ws, nb, stream)
-        return self.logits if self.head else self.u
+            B.moe_mxfp4_linear(self.n, self.d, self.m, u, None, "bf16", *self.head, None, self.logits, "f32", self.ws,
+                               nb, stream)
+        return self.logits if self.head else u
