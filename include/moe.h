@@ -518,8 +518,10 @@ typedef struct {
  *   stats  [4][n] f32 for the gradient, or NULL: post's mean and rstd, pre's
  *          mean and rstd (mean 0 for an RMS norm; rows of absent norms are
  *          left as they were)
- * Sums are float32 (the mean's of MOE_F32 rows float64), variances are taken
- * from differences.  Sizes and alignment as in moe_layer_norm. */
+ * Sums are float32, but for a mean's over float32 values, which is float64:
+ * pre's (h before its rounding) in calls of either type, post's of MOE_F32
+ * rows.  Variances are taken from differences.  Sizes and alignment as in
+ * moe_layer_norm. */
 int moe_block_norm(int32_t n, int32_t d, const void *x, const void *z, int act, float scale,
                    const float *gate, const moe_norm *post, const moe_norm *pre, void *h, void *u,
                    float *stats, void *stream);

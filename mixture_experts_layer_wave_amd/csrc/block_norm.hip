@@ -49,12 +49,18 @@ struct BlockNormParams {
 };
 
 // Mean (as value and rest, see norm.hip) and rstd of the rows held in v; v turns
-// into the differences from the mean, 0 past the row's end.
-template <bool BF, bool TAIL, int TPR, int C, int V, class Mean, class Var>
+// into the differences from the mean, 0 past the row's end.  Sum: what the mean's
+// sum is taken in.  float does for values of bf16 precision, whose sums lose
+// nothing where they lie close together; float32 values, which the norm in front
+// gets in calls of either type, need double: with float a row of equal values
+// near 1e4 came out 0.3 weight off its bias (8192 x 4096 bf16, two layer norms:
+// 57.6 us with float for both, 60.5 so; eight values added in float before their
+// conversion 59.6).
+template <bool BF, bool TAIL, int TPR, class Sum, int C, int V, class Mean, class Var>
 __device__ __forceinline__ void center(int kind, float eps, int d, int gl, float (&v)[C][V], Mean &mean_sum,
                                        Var &var_sum, float &mu, float &rs) {
   using K = Chunk<BF, TAIL>;
-  typedef typename std::conditional<BF, float, double>::type Sum;
+  constexpr bool kRest = std::is_same<Sum, double>::value;
   mu = 0.f;
   if (kind == kLayer) {
     Sum total[1] = {0};
@@ -64,7 +70,7 @@ __device__ __forceinline__ void center(int kind, float eps, int d, int gl, float
       for (int j = 0; j < V; ++j) total[0] += (Sum)v[c][j];
     mean_sum(total);
     float rest = 0.f;
-    if constexpr (BF) {
+    if constexpr (!kRest) {
       mu = total[0] / (float)d;
     } else {
       const double inv_d = 1.0 / (double)d;
@@ -75,7 +81,7 @@ __device__ __forceinline__ void center(int kind, float eps, int d, int gl, float
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float away = BF ? v[c][j] - mu : v[c][j] - mu - rest;
+        const float away = kRest ? v[c][j] - mu - rest : v[c][j] - mu;
         v[c][j] = K::in((c * TPR + gl) * V, j, d) ? away : 0.f;
       }
   }
@@ -93,10 +99,12 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
   using K = Chunk<BF, TAIL>;
   constexpr int V = K::V;
   constexpr int NT = TPR > 256 ? TPR : 256, G = NT / TPR;
-  typedef typename std::conditional<BF, float, double>::type Sum;
-  __shared__ Sum s_mean[2][1][NT / 64];
+  typedef typename std::conditional<BF, float, double>::type Sum;  // of z's mean; h's is double
+  __shared__ Sum s_post[2][1][NT / 64];
+  __shared__ double s_pre[2][1][NT / 64];
   __shared__ float s_var[2][1][NT / 64];
-  RowSum<Sum, TPR, NT, 1> mean_sum(s_mean);
+  RowSum<Sum, TPR, NT, 1> post_sum(s_post);
+  RowSum<double, TPR, NT, 1> pre_sum(s_pre);
   RowSum<float, TPR, NT, 1> var_sum(s_var);
   const int n = p.n, d = p.d, grp = threadIdx.x / TPR, gl = threadIdx.x % TPR, stride = gridDim.x * G;
   const int post = p.post.kind, pre = p.pre.kind;
@@ -136,7 +144,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
     load_row(row + stride);  // runs under this row's sums
     float mu, rs = 1.f;
     if (post) {
-      center<BF, TAIL, TPR>(post, p.post.eps, d, gl, v, mean_sum, var_sum, mu, rs);
+      center<BF, TAIL, TPR, Sum>(post, p.post.eps, d, gl, v, post_sum, var_sum, mu, rs);
       if (row < n && gl == 0 && p.stats) {
         p.stats[row] = mu;
         p.stats[(size_t)n + row] = rs;
@@ -152,7 +160,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
       if (row < n) K::template store<kNt>(p.h, row, (c * TPR + gl) * V, d, v[c]);
     }
     if (pre) {
-      center<BF, TAIL, TPR>(pre, p.pre.eps, d, gl, v, mean_sum, var_sum, mu, rs);
+      center<BF, TAIL, TPR, double>(pre, p.pre.eps, d, gl, v, pre_sum, var_sum, mu, rs);
       if (row < n) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
