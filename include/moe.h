@@ -477,8 +477,8 @@ int moe_mxfp4_linear(int32_t n, int32_t d, int32_t m, const void *x, const uint8
  * chosen experts and of the launches between its steps.
  *   Arguments, results and refusals: as moe_forward, but for the workspace
  *   (moe_forward_few_workspace_bytes) and for what is refused beside:
- *   n > MOE_FEW_MAX_TOKENS and n * k * d_ff >= 2^30 (MOE_ERR_SHAPE), and
- *   act_quant (MOE_ERR_DTYPE).
+ *   n > MOE_FEW_MAX_TOKENS, n * k * d_ff >= 2^30, and with MOE_F32 weights d
+ *   or d_ff >= 2^26 (MOE_ERR_SHAPE), and act_quant (MOE_ERR_DTYPE).
  * With MXFP4 weights and more than about 4 tokens moe_forward takes less time
  * (d = d_ff = 2880, 128 experts, k = 4: 97 against 99 us at 8 tokens, 142 against 168 at 16).
  * Each hidden value is multiplied by its combine weight in float32 and rounded

@@ -34,6 +34,9 @@ int check_few(const moe_shape *s, int wdt) {
   if (s->n > MOE_FEW_MAX_TOKENS) return MOE_ERR_SHAPE;
   st = check_dtypes(s, wdt == MOE_F32 ? MOE_F32 : MOE_BF16, wdt);
   if (st != MOE_OK) return st;
+  // A group of eight weight rows is read by 32-bit byte offsets (wave_stream.h); bf16 and
+  // MXFP4 matrices are small enough by check_dtypes.
+  if (wdt == MOE_F32 && std::max(s->d, s->d_ff) >= (1 << 26)) return MOE_ERR_SHAPE;
   // the hidden columns of all chosen experts are counted in 32 bits
   if ((long long)s->n * s->k * s->d_ff >= (1ll << 30)) return MOE_ERR_SHAPE;
   return MOE_OK;

@@ -122,7 +122,7 @@ __device__ __forceinline__ void stream(int C, int K, uint8_t *xbuf, Seg seg, Rea
     ready();
     return;
   }
-  uint32_t off[kSteps];  // of the lane's pieces, from its group's first row
+  uint32_t off[kSteps];  // of the lane's pieces, from its group's first row (callers keep 8 rows below 2^31 bytes)
   const uint8_t *sp = nullptr;
   int ld_seg = 0, ld_c = 0, ld_left = 0, issued = 1;  // the chunk to load next, and its number
   bool more = true;
