@@ -343,7 +343,9 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
             const int mid = (ca + cb) >> 1;
             (v & 1 ? ca : cb) = mid;
             const uint8_t *src = (const uint8_t *)p.h + q * hrow;
-            uint8_t *dst = s_x + (pre * Cf + (row - pre) - ur.w0) * RC + lane % SL * 16;
+            // (row chunks are counted first: all of a pile's, in bytes, do not fit 31 bits)
+            const int to = pre * Cf + (row - pre) - ur.w0;
+            uint8_t *dst = s_x + lane % SL * 16;
             for (int c = ca + lane / SL; c < cb; c += kStage * (64 / SL)) {
               u32x4 w[kStage];
 #pragma unroll
@@ -351,7 +353,7 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewParams p) {
                 if (c + i * (64 / SL) < cb) w[i] = row_chunk_piece<WT>(src, c + i * (64 / SL), f, lane % SL);
 #pragma unroll
               for (int i = 0; i < kStage; ++i)
-                if (c + i * (64 / SL) < cb) *(u32x4 *)(dst + m * (c + i * (64 / SL)) * RC) = w[i];
+                if (c + i * (64 / SL) < cb) *(u32x4 *)(dst + (to + m * (c + i * (64 / SL))) * RC) = w[i];
             }
           }
           lds_barrier();
