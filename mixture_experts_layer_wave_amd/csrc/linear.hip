@@ -509,6 +509,10 @@ __global__ __launch_bounds__(NW * KG * 64, 1) void linear_gemm_kernel(GemmParams
       slot += stride;
       open();
       start();
+      // The next tile waits for these copies by counting the stores behind them, so no
+      // store may move in front of one: neither in the IR nor in the schedule.
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
     }
     // Epilogue: 32 rows at a time through the wave's own piece of LDS, so that stores
     // take whole rows of it, eight columns a lane (y's rows start at any element).
