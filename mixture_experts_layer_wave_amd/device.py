@@ -12,6 +12,8 @@ device memory and streams only.
 
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -142,13 +144,27 @@ class TrainingLayer(DeviceLayer):
 
 
 def encode_mxfp4(w, stream=None):
-    """(codes, scales) of a device tensor [..., cols] of bf16 or float32 in
-    MXFP4, by moe_quantize_mxfp4."""
-    act = "f32" if w.dtype == torch.float32 else "bf16"
-    cols = w.shape[-1]
-    q = torch.empty((*w.shape[:-1], cols // 2), dtype=torch.uint8, device=w.device)
-    s = torch.empty((*w.shape[:-1], cols // 32), dtype=torch.uint8, device=w.device)
-    B.moe_quantize_mxfp4(w.numel() // cols, cols, w, act, q, s, stream)
+    """(codes, scales) of a device tensor [..., cols] of bf16 or float32, of any
+    strides, in MXFP4, by moe_quantize_mxfp4.  Everything runs on ``stream``
+    (the current one by default), the copy of a tensor that is not contiguous
+    included."""
+    if w.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"encode_mxfp4 takes bfloat16 or float32 tensors, not {w.dtype}")
+    if not w.is_cuda or w.dim() == 0 or w.shape[-1] == 0:
+        raise ValueError(f"encode_mxfp4 takes device tensors [..., cols], not {w.device} {list(w.shape)}")
+    if stream is None:
+        on = contextlib.nullcontext()
+    else:
+        on = torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
+    with on:
+        if w.device.index != torch.cuda.current_device():
+            raise ValueError(f"encode_mxfp4: the tensor is on {w.device}, the stream on cuda:{torch.cuda.current_device()}")
+        # (memory of this stream, so that it is free for others only behind the encoder)
+        w = w.contiguous()
+        cols = w.shape[-1]
+        q = torch.empty((*w.shape[:-1], cols // 2), dtype=torch.uint8, device=w.device)
+        s = torch.empty((*w.shape[:-1], cols // 32), dtype=torch.uint8, device=w.device)
+        B.moe_quantize_mxfp4(w.numel() // cols, cols, w, "f32" if w.dtype == torch.float32 else "bf16", q, s)
     return q, s
 
 
