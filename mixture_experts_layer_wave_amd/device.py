@@ -168,6 +168,18 @@ def encode_mxfp4(w, stream=None):
     return q, s
 
 
+def _expect(name, t, shape, dtypes, device, contiguous=True):
+    """Raises unless t is a tensor of this shape, of one of these types, there."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is {list(t.shape)}, not {list(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
 class DecodeBlock:
     """A layer with the norms around it, for at most 16 tokens a step:
 
@@ -175,17 +187,39 @@ class DecodeBlock:
 
     with the experts and the head in MXFP4.  ``w1``, ``w3`` [E][d_ff][d], ``w2``
     [E][d][d_ff] and ``head`` [m][d] (or None) are bf16 or float32 device
-    tensors, encoded once; ``wg`` [E][d] is bf16, ``bias`` float32 or None.
-    ``post`` and ``pre`` are dicts (kind "layer" or "rms", weight, bias, eps)
-    or None; without ``pre`` u is h itself.  :meth:`step` works on the block's
-    own h and u [n][d] in place, returns the logits or, without a head, u, and
-    neither allocates nor synchronises, so it can be captured in a HIP graph.
+    tensors, encoded once; ``wg`` [E][d] is bf16, ``bias`` [E] and ``gate`` [d]
+    float32 or None.  ``post`` and ``pre`` are dicts (kind "layer" or "rms",
+    weight, bias, eps; [d] float32) or None.  ValueError for any other shape,
+    type or device, and for parameters used as they are (not encoded) that are
+    not contiguous.  Without ``pre`` u is h itself.  :meth:`step` works on the
+    block's own h and u [n][d] in place, returns the logits or, without a head,
+    u, and neither allocates nor synchronises, so it can be captured in a HIP
+    graph.
     """
 
     def __init__(self, n, wg, w1, w3, w2, k, bias=None, scale=1.0, gate=None, post=None, pre=None, head=None,
                  renorm=-1):
+        if w1.dim() != 3:
+            raise ValueError(f"w1 is {list(w1.shape)}, not [E, d_ff, d]")
         E, d_ff, d = w1.shape
         dev = w1.device
+        f32, stored = (torch.float32,), (torch.bfloat16, torch.float32)
+        _expect("w1", w1, (E, d_ff, d), stored, dev, False)
+        _expect("w3", w3, (E, d_ff, d), stored, dev, False)
+        _expect("w2", w2, (E, d, d_ff), stored, dev, False)
+        if head is not None:
+            _expect("head", head, (head.shape[0] if head.dim() else 0, d), stored, dev, False)
+        _expect("wg", wg, (E, d), (torch.bfloat16,), dev)
+        vectors = [("bias", bias, E), ("gate", gate, d)]
+        for side, norm in (("post", post), ("pre", pre)):
+            if isinstance(norm, dict):
+                if norm["kind"] not in (*B.NORMS, *B.NORMS.values()):
+                    raise ValueError(f"{side}: no norm {norm['kind']!r}")
+                _expect(side + " weight", norm["weight"], (d,), f32, dev)
+                vectors.append((side + " bias", norm.get("bias"), d))
+        for name, v, size in vectors:
+            if v is not None:
+                _expect(name, v, (size,), f32, dev)
         self.n, self.d, self.wg, self.bias = n, d, wg, bias
         self.shape = B.Shape(n, d, E, k, d_ff, renorm)
         self.scale, self.gate, self.post, self.pre = scale, gate, post, pre
