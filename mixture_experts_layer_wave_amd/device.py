@@ -234,9 +234,14 @@ class DecodeBlock:
         self.h, self.z = empty(n, d), empty(n, d)
         self.u = empty(n, d) if pre else self.h
         self.idx, self.topw = empty(n, k, dtype=torch.int32), empty(n, k, dtype=torch.float32)
-        # 128 experts 2880 x 2880, top-4: 1 token 29 us here and 33 in moe_forward's steps,
-        # 4 tokens 61 and 66, 8 tokens 99 and 97, 16 tokens 168 and 142
-        self.layer, size = ((B.moe_forward_few, B.moe_forward_few_workspace_bytes) if n <= 4 else
+        # moe_forward_few or moe_forward, us: 128 experts 2880 x 2880, top-4, 1 token 29 and 32,
+        # 4 tokens 61 and 65, 8 tokens 98 and 95, 16 tokens 170 and 145; 8 experts 1024 x 4096,
+        # top-2, 4 tokens 29 and 32, 8 tokens 35 and 35, 16 tokens 44 and 37.  Rows past 7168
+        # elements do not fit moe_forward's kernels with the codes in LDS: 8 experts 4096 wide,
+        # top-2, d_ff = 7168, 16 tokens 170 and 141, 7200 175 and 195, 14336 306 and 337 (8
+        # tokens: 77 and 141, 87 and 194, 143 and 334).
+        few = n <= 4 or (n <= B.MOE_FEW_MAX_TOKENS and max(d, d_ff) > 7168)
+        self.layer, size = ((B.moe_forward_few, B.moe_forward_few_workspace_bytes) if few else
                             (B.moe_forward, B.moe_workspace_bytes))
         need = size(self.shape, "mxfp4")
         self.head = None
