@@ -27,7 +27,7 @@
 namespace moe {
 namespace {
 
-constexpr bool kNt = true;  // rows leave the caches to the parameters (8192 x 4096: forward 67 -> 65 us, gradient 105 -> 102)
+constexpr bool kNt = true;  // rows leave the caches to the parameters (8192 x 4096: forward 2 us less, gradient 105 -> 102)
 
 enum { kNone = 0, kLayer = 1, kRms = 2 };
 

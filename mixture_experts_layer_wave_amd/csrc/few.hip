@@ -33,11 +33,12 @@
 //
 // What bounds it: reading the chosen experts, and about 17 us around that: two launches,
 // the logits (4.6 us), the top-k, the hand-over.  d = d_ff = 2880, 128 MXFP4 experts, k = 4
-// (us; a copy's rate takes 10, 20, 39, 73 and 125 for the weights alone): 1 token 29, 2 40, 4 61,
-// 8 99, 16 168, against 33, 45, 66, 97 and 142 in the steps of moe_forward: the streaming
-// here reaches 4.4 TB/s, and 5.2 with the products left out.  d = 4096, d_ff = 14336,
-// 8 bf16 experts, k = 2: 1 token 120 (moe_forward 183), 16 566 (588); d = 1024,
-// d_ff = 4096, k = 1: 24 (45) and 42 (63).
+// (us; a copy's rate takes 10, 20, 38, 73 and 129 for the weights alone): 1 token 29, 2 39, 4 61,
+// 8 98, 16 170, against 32, 46, 65, 95 and 145 in the steps of moe_forward: the streaming
+// here reaches 4.5 TB/s, and 5.2 with the products left out.  d = 4096, d_ff = 14336,
+// k = 2, 8 MXFP4 experts: 1 token 45 (moe_forward 106), 8 143 (334), 16, whose rows do not
+// fit LDS, 306 (337); 8 bf16 experts: 120 (184), 16 530 (567); d = 1024, d_ff = 4096, 8
+// bf16 experts, k = 1: 24 (46) and 49 (64).
 // 8 waves with two chunks in flight each: four cost 3% at 1 token and 2% at 8.
 #include <algorithm>
 #include <atomic>

@@ -8,8 +8,11 @@
 // 14336, takes 8.9 us, 31 MB at 3.5 TB/s (at a large copy's rate 6.0); 2880 -> 2880 5.1,
 // near a launch.  8 waves: with 16 the one row took 9.1 and 12 rows 17.9 instead of 11.9,
 // as their exchange buffers left no room for the rows.
-// Many rows (linear_gemm_kernel) are a GEMM, from 17 on: 16 rows 4096 -> 14336 take 20.0 us
-// here and 17 21.7 there; 2880 -> 2880 8.0 and 12.4.
+// Many rows (linear_gemm_kernel) are a GEMM, from 17 on, where the rows' second group of 16
+// would read W again (us, rows kernel / GEMM): 4096 -> 14336 16 rows 19.9 / 21.6, 17 30.6 /
+// 21.7, 32 37.7 / 22.7; MXFP4 rows with their encoding 16 13.2 / 17.2, 17 15.6 / 17.4, 32 18.5 /
+// 17.6.  Narrow matrices would be better off later: 2880 -> 2880 16 rows 8.0 / 12.2, 17
+// 11.7 / 12.4, 32 14.3 / 12.9, 1024 -> 4096 17 rows 6.3 / 11.9, 32 6.6 / 12.2.
 #include <algorithm>
 #include <atomic>
 
@@ -30,7 +33,7 @@ constexpr int kRowsMany = 16;  // rows above which the GEMM takes over (see abov
 constexpr int kLargeTiles = 150;  // 256 x 256 tiles from which they are taken
 constexpr int kBlocks = 256;       // blocks of one round: the device's CUs
 constexpr int kSplitSteps = 11;    // K steps that a plane has at least
-constexpr int kShort = 48;         // K steps up to which three groups share a tile
+constexpr int kShort = 48;         // K steps up to which three groups share a tile (see LinearPlan)
 
 struct LinearParams {
   const uint8_t *x, *xs, *w, *ws;
@@ -171,13 +174,14 @@ bool rows_fit(int n, int d) {
 //     (as stored they start at any byte); slice s of lane half h takes byte 4 h + s.
 // With 256 x 256 tiles a block takes several, one behind the other, and the next one's
 // first copies are under way during the stores (8192 x 4096 -> 14336 829 -> 809 us, MXFP4
-// rows 294 -> 286).
+// rows with their encoding 294 -> 286).
 // What bounds it: 8192 x 4096 -> 14336 takes 801 to 821 us (1.17 to 1.20 PFLOP/s) with bf16
 // rows, where a large bf16 product of the vendor's library takes 738 and a loop of MFMAs on registers
-// reaches 2.28; with MXFP4 rows 285 us (3.4 PFLOP/s), of which the scales take 5, the
-// stores about 50, and the loop runs at 4.6 of 9.5 PFLOP/s.  Neither a third and fourth stage, nor four
-// waves of 128 x 128 (a third fewer LDS reads), nor the rotation below changed the loop's
-// rate.
+// reaches 2.28; with MXFP4 rows 260 us (3.7 PFLOP/s; 283 to 285 with their encoding), of
+// which the scales take 5, the stores about 50, and the loop runs at 4.7 of 9.5 PFLOP/s: its
+// LDS traffic, 267 KB a step at 128 bytes a clock, takes as long as its products.  Neither a
+// third and fourth stage, nor four waves of 128 x 128 (a third fewer LDS reads), nor the
+// rotation below changed the loop's rate.
 struct GemmParams {
   const uint8_t *a, *b;      // [n] rows of rb bytes, [m] rows of d / 2
   const uint8_t *as, *bs;    // MX: [steps][np], [steps][mp] x 8 scales; else bs [m][d / 32]
@@ -609,7 +613,8 @@ __global__ __launch_bounds__(256) void linear_scales_kernel(const uint8_t *__res
   }
 }
 
-// How a product is run: by rows (streamed weights) or by a GEMM.
+// How a product is run: by rows (streamed weights) or by a GEMM.  (Times of MXFP4 rows are
+// with their encoding in front.)
 //   256 x 256 tiles where there are enough of them to fill most of the device (bf16 and
 //     MXFP4 rows, us, smaller tiles / these: 128 tiles 70 / 91 and 31.5 / 36.5, 160 tiles
 //     118 / 93 and 43.0 / 39.3, 192 tiles 121 / 104 and 48.3 / 44.7).
@@ -621,8 +626,12 @@ __global__ __launch_bounds__(256) void linear_scales_kernel(const uint8_t *__res
 //   bf16 rows: the same idea pays less, as a block's W needs more LDS: two groups of
 //     128 x 128 where they are one round of blocks (1024 x 4096 -> 4096 49.3 -> 45.1),
 //     three of 64 x 128 where those are and K is short (333 x 2880 -> 5001 25.3 -> 23.5,
-//     but 512 x 4096 -> 4096 34.4 -> 36.9); else one group of 128 x 128 and K in planes
-//     while that gives more blocks (17 x 4096 -> 4096 33 -> 16).
+//     300 x 2048 -> 6000 22.8 -> 20.4, 200 x 2880 -> 8192 26.1 -> 22.1, but 512 x 4096 -> 4096
+//     34.4 -> 36.9; between 48 and 64 steps the border could lie higher: 500 x 3584 -> 4096
+//     30.7 -> 28.5); else one group of 128 x 128 and K in planes while that gives more blocks
+//     and a plane has kSplitSteps (no planes / 22 / 11 / 6 steps at least: 17 x 4096 -> 4096
+//     37.5 / 23.4 / 15.8 / 14.0, 65 x 4096 -> 14336 51 / 33.1 / 26.4 / 26.3, 300 x 8192 -> 2048
+//     98 / 33.3 / 27.8 / 27.7, 200 x 2048 -> 2048 21.7 / 21.4 / 16.9 / 15.7).
 struct LinearPlan {
   bool rows;
   int bm, bn, groups, splits, per, steps, rb, np, mp;
