@@ -158,7 +158,7 @@ def encode_mxfp4(w, stream=None):
         on = torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
     with on:
         if w.device.index != torch.cuda.current_device():
-            raise ValueError(f"encode_mxfp4: the tensor is on {w.device}, the stream on cuda:{torch.cuda.current_device()}")
+            raise ValueError(f"encode_mxfp4: a tensor on {w.device}, a stream on cuda:{torch.cuda.current_device()}")
         # (memory of this stream, so that it is free for others only behind the encoder)
         w = w.contiguous()
         cols = w.shape[-1]
